@@ -88,8 +88,24 @@ typedef enum {
   MOE_LORA_OP_SGMV_EXPAND = 3,
   MOE_LORA_OP_DENSE = 4,
   MOE_LORA_OP_FORWARD_BF16 = 5,  /* moe_lora_forward with ML_BF16 experts only  */
-  MOE_LORA_OP_FORWARD_E4M3 = 6   /* moe_lora_forward with ML_E4M3 experts only  */
+  MOE_LORA_OP_FORWARD_E4M3 = 6,  /* moe_lora_forward with ML_E4M3 experts only  */
+  MOE_LORA_OP_ROUTE_SCORED = 7,
+  MOE_LORA_OP_DENSE_FUSED = 8
 } moe_lora_op;
+
+/* Router scores of moe_lora_route_scored and the rule that scores a group of experts. */
+typedef enum { ML_SCORE_SOFTMAX = 0, ML_SCORE_SIGMOID = 1 } ml_score;
+typedef enum { ML_GROUP_MAX = 0, ML_GROUP_TOP2 = 1 } ml_group_rule;
+
+/* Activations of dense_lora_fused. */
+typedef enum {
+  ML_ACT_NONE = 0,
+  ML_ACT_RELU = 1,
+  ML_ACT_GELU = 2,         /* v (1 + erf(v / sqrt 2)) / 2                              */
+  ML_ACT_GELU_TANH = 3,    /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2        */
+  ML_ACT_SILU = 4,         /* v / (1 + exp(-v))                                        */
+  ML_ACT_SILU_AND_MUL = 5  /* silu(gate) * up, gate = features [0, h_out), up the rest */
+} ml_activation;
 
 /* Supported ranges (outside them: MOE_LORA_ERR_UNSUPPORTED).
  *   r in {8, 16, 32, 64, 128}; 1 <= k <= E <= 256; 0 <= L <= 64;
@@ -128,6 +144,59 @@ MOE_LORA_API moe_lora_status moe_lora_route(
     const void* x, const void* w_router, const float* bias, const float* logits_in,
     const int32_t* adapter_ids, int M, int H, int E, int k, int L,
     float* logits_out, int32_t* topk_ids, float* topk_w,
+    int32_t* sorted_pairs, int32_t* seg_offsets,
+    void* workspace, size_t workspace_bytes, moe_lora_stream stream);
+
+/* How moe_lora_route_scored turns logits into experts and weights (NULL: the defaults,
+ * {ML_SCORE_SOFTMAX, 1, 1, ML_GROUP_MAX, 1, 1.0f}: the routing of moe_lora_route).
+ *   score        ml_score: s = softmax over all E logits, or s_e = 1 / (1 + exp(-l_e)).
+ *   n_group      the E experts form n_group groups of E / n_group neighbours (n_group
+ *                divides E); 1 = no groups.
+ *   topk_group   groups a token may choose from; topk_group * (E / n_group) >= k.
+ *   group_rule   ml_group_rule: a group's score is its largest selection score, or the sum
+ *                of its two largest (its only one where a group has one expert; the two
+ *                scores and the two biases are summed apart, then together).
+ *   renormalize  1: the k weights are divided by their sum; 0: they stay as scored.
+ *   scale        multiplies the weights (finite). */
+typedef struct {
+  int score;
+  int n_group;
+  int topk_group;
+  int group_rule;
+  int renormalize;
+  float scale;
+} moe_lora_route_format;
+
+/* ---------------------------------------------------------------------------------
+ * moe_lora_route_scored -- moe_lora_route with softmax or sigmoid scores, a selection
+ * bias per expert (load balance without an auxiliary loss), expert groups and optional
+ * renormalisation.  With l = x W_r^T + bias or logits_in, and s its scores:
+ *   c_e  = s_e + score_bias_e                    selection score (decides who is chosen)
+ *   keep   the topk_group groups of largest group score (equal ones: the lower group)
+ *   ids    the k largest c among the kept groups, descending (equal ones: the lower e)
+ *   w_j  = s_ids[j], divided by the sum over j if renormalize, times scale: the bias
+ *          moves the choice, never the weight.
+ * The pages describe the router only as choosing each token's most relevant experts
+ * ([vLLM MoE-LoRA page], "Entendendo os Modelos MoE"); the scores, bias, groups and
+ * scaling are the generic forms of that choice.
+ *
+ *   score_bias fp32 [E] or NULL (zero).  The other arguments, outputs and limits are those
+ *              of moe_lora_route; outputs feed moe_lora_forward unchanged.
+ *   workspace  >= moe_lora_workspace_size(MOE_LORA_OP_ROUTE_SCORED, M, H, 0, E, k, L, 0).
+ * The choice is that of these formulas in 64-bit arithmetic on the fp32 logits (without a
+ * score_bias, and without ML_GROUP_TOP2 groups, scores are compared as logits: the same
+ * order); weights are fp32.  For given logits the outputs are deterministic.
+ *   - An infinite logit or score_bias counts as the largest finite float of its sign: an
+ *     expert masked by -inf has weight 0, and a token whose chosen experts are all masked
+ *     gets equal weights if renormalised.
+ *   - A NaN logit or score_bias makes its expert the last choice (lower index first), a
+ *     NaN logit has weight 0; it sets MOE_LORA_ERR_DEVICE_CHECK, as does an adapter id
+ *     outside [-1, L), which is treated as -1.
+ * ------------------------------------------------------------------------------- */
+MOE_LORA_API moe_lora_status moe_lora_route_scored(
+    const void* x, const void* w_router, const float* bias, const float* logits_in,
+    const float* score_bias, const int32_t* adapter_ids, int M, int H, int E, int k, int L,
+    const moe_lora_route_format* format, float* logits_out, int32_t* topk_ids, float* topk_w,
     int32_t* sorted_pairs, int32_t* seg_offsets,
     void* workspace, size_t workspace_bytes, moe_lora_stream stream);
 
@@ -236,6 +305,36 @@ MOE_LORA_API moe_lora_status dense_lora_forward(
     void* workspace, size_t workspace_bytes, moe_lora_stream stream);
 
 /* ---------------------------------------------------------------------------------
+ * dense_lora_fused -- one dense projection with segmented multi-LoRA, bias, activation and
+ * residual in one pass over the output:
+ *   h_t = W x_t + bias + [a(t) >= 0] lora_scale (x_t A_a(t)) B_a(t)
+ *   y_t = act(h_t) + residual_t
+ * With ML_ACT_SILU_AND_MUL the projection has 2 h_out features, the gate first:
+ *   act(h) = silu(h[0:h_out]) * h[h_out:2 h_out].
+ * y = xW + (xA)B per projection ([vLLM MoE-LoRA page], "O Papel da Multi-LoRA"), the add
+ * fused into the base output ("Otimizações em Nível de Kernel"); segments as in SGMV
+ * ([Punica review page], "提案手法").  With n = h_out (2 h_out when gated):
+ *
+ *   x [T, h_in], w [n][h_in], bias [n] or NULL, residual [T, h_out] or NULL, all of type
+ *   dt (ML_F32 or ML_BF16); lora_a [L][r][h_in], lora_b [L][r][n] (NULL iff L = 0).
+ *   seg_offsets, seg_adapter: segments as in sgmv_shrink; a token outside every segment
+ *   counts as one without an adapter.  Both may be NULL, with S = 0, when L = 0.
+ *   y [T, h_out] of type dt, overwritten; it may be the residual itself (the same
+ *   pointer: an update in place) and may overlap no other argument.
+ *   workspace >= moe_lora_workspace_size(MOE_LORA_OP_DENSE_FUSED, T, h_in, h_out, 1, 1, L, r).
+ * Sums, bias, activation and residual are fp32 and rounded to dt once (the adapters' xA is
+ * rounded to bf16 for ML_BF16).  A tenant's adapter reaches only its own tokens, whatever
+ * it holds.  An adapter id outside [-1, L) or offsets that are not monotone set
+ * MOE_LORA_ERR_DEVICE_CHECK; the tokens concerned count as without an adapter.
+ * h_in and h_out are multiples of 8; T <= 2^20.
+ * ------------------------------------------------------------------------------- */
+MOE_LORA_API moe_lora_status dense_lora_fused(
+    const void* x, const void* w, const void* bias, const void* lora_a, const void* lora_b,
+    const int32_t* seg_offsets, const int32_t* seg_adapter, int S, int T, int h_in, int h_out,
+    int r, int L, int activation, float lora_scale, const void* residual, ml_dtype dt, void* y,
+    void* workspace, size_t workspace_bytes, moe_lora_stream stream);
+
+/* ---------------------------------------------------------------------------------
  * moe_lora_route_noalloc -- moe_lora_route for callers that cannot allocate device
  * memory.  The pages have no counterpart to this entry point; it exists for callers
  * that receive only their input and output buffers from a host framework (a plugin
@@ -286,7 +385,8 @@ MOE_LORA_API const char* moe_lora_last_error(void);
  *   6 combine, 7 SGMV expand, 8 fp32 dense GEMM, 9 dense bf16 GEMM,
  *   10 e4m3 activation planes, 11 segmented LoRA of gate_up (or dense) and the LoRA
  *   work lists, 12 one-launch routing (small batches), 13 segmented LoRA of down,
- *   14 token-row gather into (expert, adapter) order.
+ *   14 token-row gather into (expert, adapter) order, 15 fused dense projection,
+ *   16 its adapters' shrink, 17 scored routing.
  * Launches captured into a CUDA graph record their events as graph nodes, so every
  * replay of the graph re-records them (the last replay's times are read).
  * moe_lora_profile_read() waits for the recorded events and returns the summed

@@ -18,21 +18,31 @@ LIB_PATH = os.path.join(_PKG, "libmoe_lora.so")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_DEVICE_CHECK, ERR_TIMEOUT = range(6)
 ML_F32, ML_BF16, ML_E4M3 = 0, 1, 2
 OP_ROUTE, OP_FORWARD, OP_SGMV_SHRINK, OP_SGMV_EXPAND, OP_DENSE, OP_FORWARD_BF16, OP_FORWARD_E4M3 = range(7)
+OP_ROUTE_SCORED, OP_DENSE_FUSED = 7, 8
+SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_RULES = {"max": 0, "top2": 1}
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "silu_and_mul": 5}
 
 EXPORTS = ("moe_lora_route", "moe_lora_forward", "sgmv_shrink", "sgmv_expand", "dense_lora_forward",
            "moe_lora_workspace_size", "moe_lora_check_status", "moe_lora_last_error", "moe_lora_version",
            "moe_lora_profile_enable", "moe_lora_profile_read", "moe_lora_launch_count",
-           "moe_lora_route_noalloc")
+           "moe_lora_route_noalloc", "moe_lora_route_scored", "dense_lora_fused")
 KERNEL_IDS = {"router_logits": 0, "topk": 1, "sort": 2, "shrink": 3, "gemm_gateup": 4, "gemm_down": 5,
               "combine": 6, "expand": 7, "dense_f32": 8, "gemm_dense": 9, "quant": 10,
               "lora": 11, "route": 12, "lora_down": 13,
-              "gather": 14}
+              "gather": 14, "dense_fused": 15, "fused_shrink": 16, "route_scored": 17}
 
 
 class AdapterFormat(ctypes.Structure):
     """moe_lora_adapter_format: gate_up adapter layout (0 fused, 1 separate gate and up
     adapters) and the per-projection scales of the LoRA deltas."""
     _fields_ = [("gate_up_split", ctypes.c_int), ("scale_gu", ctypes.c_float), ("scale_d", ctypes.c_float)]
+
+
+class RouteFormat(ctypes.Structure):
+    """moe_lora_route_format: scores, expert groups, renormalisation and scale of the weights."""
+    _fields_ = [("score", ctypes.c_int), ("n_group", ctypes.c_int), ("topk_group", ctypes.c_int),
+                ("group_rule", ctypes.c_int), ("renormalize", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 class MoELoRAError(RuntimeError):
@@ -60,6 +70,10 @@ def lib() -> ctypes.CDLL:
         L.sgmv_shrink.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]
         L.sgmv_expand.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]
         L.dense_lora_forward.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]
+        L.moe_lora_route_scored.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.POINTER(RouteFormat),
+                                            _P, _P, _P, _P, _P, _P, _SZ, _P]
+        L.dense_lora_fused.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P,
+                                       _I, _P, _P, _SZ, _P]
         L.moe_lora_workspace_size.argtypes = [_I] * 8
         L.moe_lora_workspace_size.restype = _SZ
         L.moe_lora_check_status.argtypes = [_P, _P]
@@ -71,7 +85,7 @@ def lib() -> ctypes.CDLL:
         L.moe_lora_profile_read.restype = _I
         L.moe_lora_launch_count.restype = ctypes.c_longlong
         for name in ("moe_lora_route", "moe_lora_forward", "sgmv_shrink", "sgmv_expand",
-                     "dense_lora_forward", "moe_lora_check_status"):
+                     "dense_lora_forward", "moe_lora_route_scored", "dense_lora_fused", "moe_lora_check_status"):
             getattr(L, name).restype = _I
         _lib = L
     return _lib
@@ -167,6 +181,92 @@ def route(adapter_ids: torch.Tensor, k: int, L: int, *, x=None, w_router=None, b
     return res
 
 
+def _expect(name: str, t: torch.Tensor | None, shape: tuple, dtype: torch.dtype) -> None:
+    if t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype} of shape {shape}, got {t.dtype} of shape {tuple(t.shape)}")
+
+
+def _one_device(*tensors) -> torch.device:
+    """The device of all tensors given (None left out): it has to be the current one, since the
+    library launches on the current device."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"tensors on several devices: {sorted(map(str, devs))}")
+    dev = devs.pop()
+    if dev.type != "cuda":
+        raise ValueError("tensors passed to the library must be CUDA tensors")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _used_on(stream, *tensors) -> None:
+    """Buffers made here for a stream other than the current one are not reused before it is done."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _choice(name: str, value: str, of: dict) -> int:
+    if value not in of:
+        raise ValueError(f"{name} must be one of {', '.join(of)}, got {value!r}")
+    return of[value]
+
+
+def route_scored(adapter_ids: torch.Tensor, k: int, L: int, *, x=None, w_router=None, bias=None, logits_in=None,
+                 score: str = "softmax", score_bias=None, n_group: int = 1, topk_group: int = 1,
+                 group_rule: str = "max", renormalize: bool = True, scale: float = 1.0, want_logits=False,
+                 out=None, workspace=None, stream=None) -> dict:
+    """moe_lora_route_scored: routing by "softmax" or "sigmoid" scores.  score_bias (fp32 [E])
+    moves the choice of experts, not their weights; topk_group of n_group groups of experts
+    are kept by group_rule ("max", or "top2": the sum of the two largest); the weights are
+    divided by their sum if renormalize, then multiplied by scale.  Returns what route() does."""
+    if logits_in is None and (x is None or w_router is None):
+        raise ValueError("route_scored needs x and w_router, or logits_in")
+    M = adapter_ids.shape[0]
+    E, H = (logits_in.shape[1], 0) if logits_in is not None else w_router.shape
+    _expect("adapter_ids", adapter_ids, (M,), torch.int32)
+    if logits_in is not None:
+        _expect("logits_in", logits_in, (M, E), torch.float32)
+    else:
+        _expect("x", x, (M, H), torch.bfloat16)
+        _expect("w_router", w_router, (E, H), torch.bfloat16)
+        _expect("bias", bias, (E,), torch.float32)
+    _expect("score_bias", score_bias, (E,), torch.float32)
+    fmt = RouteFormat(_choice("score", score, SCORES), int(n_group), int(topk_group),
+                      _choice("group_rule", group_rule, GROUP_RULES), 1 if renormalize else 0, float(scale))
+    o = out if out is not None else {}
+    dev = _one_device(adapter_ids, x, w_router, bias, logits_in, score_bias, workspace, *o.values())
+    made = []
+
+    def buf(name, shape, dtype):
+        t = o.get(name)
+        if t is None:
+            made.append(torch.empty(shape, dtype=dtype, device=dev))
+            return made[-1]
+        if t.numel() < torch.Size(shape).numel() or t.dtype != dtype:
+            raise ValueError(f"out[{name!r}] must be {dtype} with at least {torch.Size(shape).numel()} elements")
+        return t
+
+    ids = buf("topk_ids", (M, k), torch.int32)
+    w = buf("topk_w", (M, k), torch.float32)
+    sp = buf("sorted_pairs", (M * k,), torch.int32)
+    so = buf("seg_offsets", (E * (L + 1) + 1,), torch.int32)
+    lg = buf("logits", (M, E), torch.float32) if want_logits else None
+    if workspace is None:
+        workspace = new_workspace(workspace_size(OP_ROUTE_SCORED, M, H, 0, E, k, L, 0), dev)
+        made.append(workspace)
+    _check(lib().moe_lora_route_scored(
+        _ptr(x), _ptr(w_router), _ptr(bias), _ptr(logits_in), _ptr(score_bias), _ptr(adapter_ids), M, H, E, k, L,
+        ctypes.byref(fmt), _ptr(lg), _ptr(ids), _ptr(w), _ptr(sp), _ptr(so), _ptr(workspace), workspace.numel(),
+        _stream(stream)))
+    _used_on(stream, *made)
+    res = {"topk_ids": ids, "topk_w": w, "sorted_pairs": sp[: M * k], "seg_offsets": so, "workspace": workspace}
+    if want_logits:
+        res["logits"] = lg
+    return res
+
+
 def forward(x: torch.Tensor, routing: dict, weights: dict, *, k: int, L: int, y=None, workspace=None,
             stream=None, scale_gu: float = 1.0, scale_d: float = 1.0) -> torch.Tensor:
     """moe_lora_forward.  weights: w_gu [E,2I,H], w_d [E,H,I] (bf16 or e4m3), scales [E,2]
@@ -237,4 +337,50 @@ def dense_lora_forward(x, w, lora_a, lora_b, seg_offsets, seg_adapter, *, y=None
                                     _ptr(lora_b) if L else None, _ptr(seg_offsets), _ptr(seg_adapter),
                                     S, T, h_in, h_out, r, L, _dt(x), _ptr(y), _ptr(workspace),
                                     workspace.numel(), _stream(stream)))
+    return y
+
+
+def dense_lora_fused(x, w, lora_a=None, lora_b=None, seg_offsets=None, seg_adapter=None, *, bias=None,
+                     activation: str = "none", residual=None, lora_scale: float = 1.0, y=None, workspace=None,
+                     stream=None):
+    """dense_lora_fused: y = act(x w^T + bias + lora_scale (x A) B) + residual, bf16 or fp32.
+    activation: "none", "relu", "gelu", "gelu_tanh", "silu", or "silu_and_mul", where w (and
+    bias and lora_b) hold 2 h_out features, the gate first.  Without lora_a and lora_b no
+    segments are needed; y may be the residual (an update in place)."""
+    act = _choice("activation", activation, ACTIVATIONS)
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    T, h_in = x.shape
+    n = w.shape[0]
+    if act == 5 and n % 2:
+        raise ValueError("silu_and_mul needs an even number of weight rows (gate, then up)")
+    h_out = n // 2 if act == 5 else n
+    if (lora_a is None) != (lora_b is None):
+        raise ValueError("lora_a and lora_b go together")
+    L, r = (lora_a.shape[0], lora_a.shape[1]) if lora_a is not None else (0, 0)
+    if L > 0 and (seg_offsets is None or seg_adapter is None):
+        raise ValueError("adapters need seg_offsets and seg_adapter")
+    S = seg_adapter.shape[0] if seg_adapter is not None else 0
+    dt = x.dtype
+    _expect("w", w, (n, h_in), dt)
+    _expect("bias", bias, (n,), dt)
+    _expect("residual", residual, (T, h_out), dt)
+    _expect("lora_a", lora_a, (L, r, h_in), dt)
+    _expect("lora_b", lora_b, (L, r, n), dt)
+    _expect("y", y, (T, h_out), dt)
+    _expect("seg_adapter", seg_adapter, (S,), torch.int32)
+    _expect("seg_offsets", seg_offsets, (S + 1,), torch.int32)
+    dev = _one_device(x, w, lora_a, lora_b, seg_offsets, seg_adapter, bias, residual, y, workspace)
+    made = []
+    if y is None:
+        y = torch.empty((T, h_out), dtype=dt, device=dev)
+        made.append(y)
+    if workspace is None:
+        workspace = new_workspace(workspace_size(OP_DENSE_FUSED, T, h_in, h_out, 1, 1, L, r), dev)
+        made.append(workspace)
+    _check(lib().dense_lora_fused(_ptr(x), _ptr(w), _ptr(bias), _ptr(lora_a) if L else None,
+                                  _ptr(lora_b) if L else None, _ptr(seg_offsets), _ptr(seg_adapter), S, T, h_in,
+                                  h_out, r, L, act, float(lora_scale), _ptr(residual), _dt(x), _ptr(y),
+                                  _ptr(workspace), workspace.numel(), _stream(stream)))
+    _used_on(stream, *made)
     return y

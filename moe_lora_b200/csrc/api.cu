@@ -2,6 +2,7 @@
 // sequence of each call.  No allocation, no synchronisation, no host read-back
 // (moe_lora_check_status excepted).
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -263,6 +264,31 @@ RouteWs route_layout(void* base, int M, int E, int L) {
   return w;
 }
 
+RouteWs scored_layout(void* base, int M, int E, int L) { return route_layout(base, M, E, L); }
+
+struct FusedWs {
+  int* status;
+  float* z;
+  int32_t* row_adapter;
+  size_t bytes;
+};
+
+FusedWs fused_layout(void* base, int T, int r) {
+  size_t off = kStatusBytes;
+  FusedWs w{};
+  uint8_t* b = static_cast<uint8_t*>(base);
+  auto take = [&](size_t bytes) {
+    uint8_t* p = b ? b + off : nullptr;
+    off += align256(bytes);
+    return p;
+  };
+  w.status = reinterpret_cast<int*>(b);
+  w.z = reinterpret_cast<float*>(take(static_cast<size_t>(T) * r * 4));
+  w.row_adapter = reinterpret_cast<int32_t*>(take(r ? static_cast<size_t>(T) * 4 : 0));
+  w.bytes = off;
+  return w;
+}
+
 struct DenseWs {
   int* status;
   float* z;             // fp32 path: shrink output
@@ -386,6 +412,8 @@ size_t moe_lora_workspace_size(int op, int M, int H, int I, int E, int k, int L,
     case MOE_LORA_OP_FORWARD_BF16:
       return forward_layout(nullptr, M, H, I, k, L > 0 ? r : 0, false, lora_place(1LL * M * k, E), E * (L + 1))
           .bytes;
+    case MOE_LORA_OP_ROUTE_SCORED: return scored_layout(nullptr, M, E, L).bytes;
+    case MOE_LORA_OP_DENSE_FUSED: return fused_layout(nullptr, M, L > 0 ? r : 0).bytes;
     case MOE_LORA_OP_SGMV_SHRINK:
     case MOE_LORA_OP_SGMV_EXPAND: return kStatusBytes;
     case MOE_LORA_OP_DENSE: {
@@ -473,6 +501,92 @@ moe_lora_status moe_lora_route(const void* x, const void* w_router, const float*
   a.num_sms = num_sms();
   a.tickets_zeroed = tickets > 0 ? 1 : 0;
   ML_CUDA(launch_route(a, cs), "moe_lora_route launch");
+  return MOE_LORA_OK;
+}
+
+moe_lora_status moe_lora_route_scored(const void* x, const void* w_router, const float* bias,
+                                      const float* logits_in, const float* score_bias,
+                                      const int32_t* adapter_ids, int M, int H, int E, int k, int L,
+                                      const moe_lora_route_format* format, float* logits_out,
+                                      int32_t* topk_ids, float* topk_w, int32_t* sorted_pairs,
+                                      int32_t* seg_offsets, void* workspace, size_t workspace_bytes,
+                                      moe_lora_stream stream) {
+  ML_REQUIRE(M >= 0 && E >= 1 && k >= 1 && L >= 0, MOE_LORA_ERR_INVALID_ARG,
+             "need M >= 0, E >= 1, k >= 1, L >= 0 (got M=%d E=%d k=%d L=%d)", M, E, k, L);
+  ML_REQUIRE(k <= E && E <= 256 && L <= 64, MOE_LORA_ERR_UNSUPPORTED,
+             "supported: k <= E <= 256, L <= 64 (got k=%d E=%d L=%d)", k, E, L);
+  ML_REQUIRE(static_cast<long long>(M) * k <= (1 << 20), MOE_LORA_ERR_UNSUPPORTED, "M*k > 2^20");
+  const moe_lora_route_format fmt =
+      format ? *format : moe_lora_route_format{ML_SCORE_SOFTMAX, 1, 1, ML_GROUP_MAX, 1, 1.0f};
+  ML_REQUIRE(fmt.score == ML_SCORE_SOFTMAX || fmt.score == ML_SCORE_SIGMOID, MOE_LORA_ERR_INVALID_ARG,
+             "format->score must be ML_SCORE_SOFTMAX or ML_SCORE_SIGMOID");
+  ML_REQUIRE(fmt.group_rule == ML_GROUP_MAX || fmt.group_rule == ML_GROUP_TOP2, MOE_LORA_ERR_INVALID_ARG,
+             "format->group_rule must be ML_GROUP_MAX or ML_GROUP_TOP2");
+  ML_REQUIRE(fmt.renormalize == 0 || fmt.renormalize == 1, MOE_LORA_ERR_INVALID_ARG,
+             "format->renormalize must be 0 or 1");
+  ML_REQUIRE(std::isfinite(fmt.scale), MOE_LORA_ERR_INVALID_ARG, "format->scale must be finite");
+  ML_REQUIRE(fmt.n_group >= 1 && fmt.n_group <= E && E % fmt.n_group == 0, MOE_LORA_ERR_INVALID_ARG,
+             "format->n_group must divide E (got n_group=%d E=%d)", fmt.n_group, E);
+  ML_REQUIRE(fmt.topk_group >= 1 && fmt.topk_group <= fmt.n_group, MOE_LORA_ERR_INVALID_ARG,
+             "format->topk_group must be in [1, n_group]");
+  ML_REQUIRE(k <= fmt.topk_group * (E / fmt.n_group), MOE_LORA_ERR_INVALID_ARG,
+             "the topk_group groups hold fewer than k experts");
+  ML_PTR(seg_offsets);
+  const RouteWs need = scored_layout(nullptr, M, E, L);
+  moe_lora_status st = check_ws(workspace, workspace_bytes, need.bytes);
+  if (st != MOE_LORA_OK) return st;
+  if (score_bias) ML_PTR(score_bias);
+  if (M > 0) {
+    ML_PTR(adapter_ids);
+    ML_PTR(topk_ids);
+    ML_PTR(topk_w);
+    ML_PTR(sorted_pairs);
+    if (logits_in == nullptr) {
+      ML_PTR(x);
+      ML_PTR(w_router);
+      ML_REQUIRE(H > 0 && H % 8 == 0, MOE_LORA_ERR_UNSUPPORTED, "H must be a positive multiple of 8");
+      if (bias) ML_PTR(bias);
+    } else {
+      ML_PTR(logits_in);
+    }
+    if (logits_out) ML_PTR(logits_out);
+  }
+  st = check_device();
+  if (st != MOE_LORA_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const RouteWs w = scored_layout(workspace, M, E, L);
+  ML_CUDA(cudaMemsetAsync(workspace, 0, 8, cs), "status clear");
+  RouteArgs a{};
+  a.x = static_cast<const __nv_bfloat16*>(x);
+  a.w_router = static_cast<const __nv_bfloat16*>(w_router);
+  a.bias = bias;
+  a.logits_in = logits_in;
+  a.adapter_ids = adapter_ids;
+  a.M = M;
+  a.H = H;
+  a.E = E;
+  a.k = k;
+  a.L = L;
+  a.logits = logits_out ? logits_out : w.logits;
+  a.logits_out = logits_out;
+  a.topk_ids = topk_ids;
+  a.topk_w = topk_w;
+  a.sorted_pairs = sorted_pairs;
+  a.seg_offsets = seg_offsets;
+  a.key_count = w.key_count;
+  a.a_key = w.a_key;
+  a.status = w.status;
+  a.num_sms = num_sms();
+  ScoreFormat f{};
+  f.sigmoid = fmt.score == ML_SCORE_SIGMOID;
+  f.n_group = fmt.n_group;
+  f.topk_group = fmt.topk_group;
+  f.group_size = E / fmt.n_group;
+  f.top2 = fmt.group_rule == ML_GROUP_TOP2;
+  f.renorm = fmt.renormalize;
+  f.by_logit = score_bias == nullptr && !(fmt.n_group > 1 && f.top2);
+  f.scale = fmt.scale;
+  ML_CUDA(launch_route_scored(a, f, score_bias, cs), "moe_lora_route_scored launch");
   return MOE_LORA_OK;
 }
 
@@ -987,6 +1101,72 @@ moe_lora_status dense_lora_forward(const void* x, const void* w, const void* lor
 
   g.num_sms = num_sms();
   ML_CUDA(launch_gemm_tc(g, cs), "dense GEMM launch");
+  return MOE_LORA_OK;
+}
+
+moe_lora_status dense_lora_fused(const void* x, const void* w, const void* bias, const void* lora_a,
+                                 const void* lora_b, const int32_t* seg_offsets, const int32_t* seg_adapter,
+                                 int S, int T, int h_in, int h_out, int r, int L, int activation,
+                                 float lora_scale, const void* residual, ml_dtype dt, void* y, void* workspace,
+                                 size_t workspace_bytes, moe_lora_stream stream) {
+  ML_REQUIRE(S >= 0 && T >= 0 && L >= 0 && h_in > 0 && h_out > 0, MOE_LORA_ERR_INVALID_ARG,
+             "need S, T, L >= 0 and h_in, h_out > 0");
+  ML_REQUIRE(dt == ML_F32 || dt == ML_BF16, MOE_LORA_ERR_INVALID_ARG, "dt must be ML_F32 or ML_BF16");
+  ML_REQUIRE(activation >= ML_ACT_NONE && activation <= ML_ACT_SILU_AND_MUL, MOE_LORA_ERR_INVALID_ARG,
+             "activation must be an ml_activation (got %d)", activation);
+  ML_REQUIRE(h_in % 8 == 0 && h_out % 8 == 0 && L <= 64 && T <= (1 << 20), MOE_LORA_ERR_UNSUPPORTED,
+             "h_in, h_out must be multiples of 8, L <= 64, T <= 2^20");
+  ML_REQUIRE(h_in <= (1 << 20) && h_out <= (1 << 20) && S <= (1 << 21), MOE_LORA_ERR_UNSUPPORTED,
+             "h_in, h_out <= 2^20 and S <= 2^21");
+  if (L > 0) ML_REQUIRE(rank_ok(r), MOE_LORA_ERR_UNSUPPORTED, "r must be one of 8, 16, 32, 64, 128");
+  ML_REQUIRE(S >= 1 || T == 0 || L == 0, MOE_LORA_ERR_INVALID_ARG, "adapters need segments (S >= 1)");
+  ML_REQUIRE(std::isfinite(lora_scale), MOE_LORA_ERR_INVALID_ARG, "lora_scale must be finite");
+  const int rr = L > 0 ? r : 0;
+  const FusedWs need = fused_layout(nullptr, T, rr);
+  moe_lora_status st = check_ws(workspace, workspace_bytes, need.bytes);
+  if (st != MOE_LORA_OK) return st;
+  if (T == 0) return MOE_LORA_OK;
+  ML_PTR(x);
+  ML_PTR(w);
+  ML_PTR(y);
+  if (bias) ML_PTR(bias);
+  if (residual) ML_PTR(residual);
+  if (L > 0) {
+    ML_PTR(lora_a);
+    ML_PTR(lora_b);
+    ML_PTR(seg_offsets);
+    ML_PTR(seg_adapter);
+  }
+  st = check_device();
+  if (st != MOE_LORA_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const FusedWs ws = fused_layout(workspace, T, rr);
+  ML_CUDA(cudaMemsetAsync(workspace, 0, 8, cs), "status clear");
+  DenseFusedArgs a{};
+  a.x = x;
+  a.w = w;
+  a.bias = bias;
+  a.lora_a = lora_a;
+  a.lora_b = lora_b;
+  a.seg_offsets = seg_offsets;
+  a.seg_adapter = seg_adapter;
+  a.S = S;
+  a.T = T;
+  a.h_in = h_in;
+  a.h_out = h_out;
+  a.n = activation == ML_ACT_SILU_AND_MUL ? 2 * h_out : h_out;
+  a.r = rr;
+  a.L = L;
+  a.act = activation;
+  a.scale = lora_scale;
+  a.residual = residual;
+  a.y = y;
+  a.f32 = dt == ML_F32;
+  a.z = ws.z;
+  a.row_adapter = ws.row_adapter;
+  a.status = ws.status;
+  a.num_sms = num_sms();
+  ML_CUDA(launch_dense_fused(a, cs), "dense_lora_fused launch");
   return MOE_LORA_OK;
 }
 

@@ -31,9 +31,25 @@ struct RouteArgs {
   int tickets_zeroed = 0;  // the caller's status clear already zeroed the tickets
 };
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t st);
+// The logits of a routing call on their own: a.logits_in (copied to a.logits_out if set) or
+// x W_r^T + bias into a.logits; *lg is where they are.
+cudaError_t launch_router_logits(const RouteArgs& a, const float** lg, cudaStream_t st);
+// seg_offsets and sorted_pairs from topk_ids, the tokens' adapter keys and the key counts.
+cudaError_t launch_sort_scatter(const RouteArgs& a, cudaStream_t st);
 // Tickets (ints at a_key) of the one-launch routing for M tokens of k pairs, or 0 when the
 // routing takes the multi-kernel path.
 int route_fused_tickets(int M, int k);
+
+// Scored routing (moe_lora_route_scored).
+struct ScoreFormat {
+  int sigmoid;     // 0: softmax over all E
+  int n_group, topk_group, group_size;
+  int top2;        // group score: sum of the two largest (else the largest)
+  int renorm;
+  int by_logit;    // the selection compares logits (no score_bias, no sums of scores)
+  float scale;
+};
+cudaError_t launch_route_scored(const RouteArgs& a, const ScoreFormat& f, const float* score_bias, cudaStream_t st);
 
 // Segmented shrink z[s] = src_row(s) . A_seg(s)^T (SIMT: 128-bit loads, warp-shuffle
 // split-K reduction).  Segments come either from a dense (offsets, adapter) table or
@@ -190,6 +206,29 @@ struct DenseF32Args {
   float* y;
 };
 cudaError_t launch_dense_f32(const DenseF32Args& a, cudaStream_t st);
+
+// y = act(x W^T + bias + lora_scale (x A) B) + residual (dense_lora_fused).
+struct DenseFusedArgs {
+  const void* x;
+  const void* w;
+  const void* bias;           // [n] or null
+  const void* lora_a;         // [L][r][h_in]
+  const void* lora_b;         // [L][r][n]
+  const int32_t* seg_offsets;
+  const int32_t* seg_adapter;
+  int S, T, h_in, h_out, n;   // n = h_out, or 2 h_out with SiLU-and-mul
+  int r, L;                   // r = 0 when L = 0
+  int act;
+  float scale;
+  const void* residual;       // [T][h_out] or null (may be y)
+  void* y;
+  bool f32;
+  float* z;                   // workspace [T][r]: scale (x A), fp32
+  int32_t* row_adapter;       // workspace [T]
+  int* status;
+  int num_sms;
+};
+cudaError_t launch_dense_fused(const DenseFusedArgs& a, cudaStream_t st);
 
 // Tensor-core grouped GEMM with operand swap: the weight rows fill the 128-row MMA
 // M slot, the tokens of one expert (or of the dense batch) the N slot.

@@ -23,7 +23,10 @@ enum KernelId : int {
   K_ROUTE = 12,
   K_LORA_DOWN = 13,  // the down projection's LoRA kernel (K_LORA: gate_up's and the work lists)
   K_GATHER = 14,     // token rows gathered into (expert, adapter) order
-  K_COUNT = 15
+  K_DENSE_FUSED = 15,  // the projection of dense_lora_fused
+  K_FUSED_SHRINK = 16,  // its adapters' shrink
+  K_ROUTE_SCORED = 17,
+  K_COUNT = 18
 };
 
 void prof_begin(int id, cudaStream_t st);
