@@ -270,6 +270,7 @@ struct FusedWs {
   int* status;
   float* z;
   int32_t* row_adapter;
+  uint64_t* tile_mask;
   size_t bytes;
 };
 
@@ -285,6 +286,7 @@ FusedWs fused_layout(void* base, int T, int r) {
   w.status = reinterpret_cast<int*>(b);
   w.z = reinterpret_cast<float*>(take(static_cast<size_t>(T) * r * 4));
   w.row_adapter = reinterpret_cast<int32_t*>(take(r ? static_cast<size_t>(T) * 4 : 0));
+  w.tile_mask = reinterpret_cast<uint64_t*>(take(r ? (static_cast<size_t>(T) + 127) / 128 * 8 : 0));
   w.bytes = off;
   return w;
 }
@@ -1141,7 +1143,11 @@ moe_lora_status dense_lora_fused(const void* x, const void* w, const void* bias,
   if (st != MOE_LORA_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const FusedWs ws = fused_layout(workspace, T, rr);
-  ML_CUDA(cudaMemsetAsync(workspace, 0, 8, cs), "status clear");
+  if (dt == ML_BF16 && !tensor_map_encode_available())
+    return fail(MOE_LORA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  // the status word, and (bf16) the mask of broken adapters beside it; without adapters the
+  // bf16 projection clears the word itself
+  if (dt == ML_F32 || rr > 0) ML_CUDA(cudaMemsetAsync(workspace, 0, kStatusBytes, cs), "status clear");
   DenseFusedArgs a{};
   a.x = x;
   a.w = w;
@@ -1164,6 +1170,7 @@ moe_lora_status dense_lora_fused(const void* x, const void* w, const void* bias,
   a.f32 = dt == ML_F32;
   a.z = ws.z;
   a.row_adapter = ws.row_adapter;
+  a.tile_mask = ws.tile_mask;
   a.status = ws.status;
   a.num_sms = num_sms();
   ML_CUDA(launch_dense_fused(a, cs), "dense_lora_fused launch");

@@ -2,24 +2,10 @@
 // multi-LoRA ([vLLM MoE-LoRA page], "O Papel da Multi-LoRA"; segments as in SGMV, [Punica
 // review page], "提案手法"), everything behind the product fused into its epilogue
 // ("Otimizações em Nível de Kernel").
-#include "common.cuh"
-#include "kernels.h"
+#include "fused_tc.cuh"
 #include "prof.h"
 
 namespace mlb {
-
-__device__ __forceinline__ float act_apply(int act, float v) {
-  switch (act) {
-    case ML_ACT_RELU: return v > 0.f ? v : (v != v ? v : 0.f);
-    case ML_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    case ML_ACT_GELU_TANH: {
-      const float u = 0.79788456080286536f * (v + 0.044715f * v * v * v);
-      return 0.5f * v * (1.f + tanhf(u));
-    }
-    case ML_ACT_SILU: return silu(v);
-    default: return v;
-  }
-}
 
 // ---------------------------------------------------------------- adapters of the rows
 // Each row's adapter from the segments by binary search: the last segment that begins at or
@@ -43,15 +29,7 @@ __global__ void __launch_bounds__(256) row_adapter_kernel(const int32_t* __restr
   row_adapter[i] = (a >= 0 && a < L) ? a : -1;
 }
 
-template <typename T>
-__device__ __forceinline__ float ld1(const T* p) { return static_cast<float>(*p); }
-template <>
-__device__ __forceinline__ float ld1<__nv_bfloat16>(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void st1(float* p, float v) { *p = v; }
-__device__ __forceinline__ void st1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
 // z[t] = c x_t A_a(t): a warp per (row, 4 ranks), lanes split h_in.
-template <typename T>
 __global__ void __launch_bounds__(256) fused_shrink_simt(const DenseFusedArgs a) {
   const int lane = threadIdx.x & 31;
   const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -60,16 +38,16 @@ __global__ void __launch_bounds__(256) fused_shrink_simt(const DenseFusedArgs a)
   const int ad = a.row_adapter[t];
   float s = 0.f;
   if (ad >= 0) {
-    const T* x = static_cast<const T*>(a.x) + static_cast<size_t>(t) * a.h_in;
-    const T* A = static_cast<const T*>(a.lora_a) + (static_cast<size_t>(ad) * a.r + i) * a.h_in;
-    for (int h = lane; h < a.h_in; h += 32) s = fmaf(ld1(x + h), ld1(A + h), s);
+    const float* x = static_cast<const float*>(a.x) + static_cast<size_t>(t) * a.h_in;
+    const float* A = static_cast<const float*>(a.lora_a) + (static_cast<size_t>(ad) * a.r + i) * a.h_in;
+    for (int h = lane; h < a.h_in; h += 32) s = fmaf(*(x + h), *(A + h), s);
     s = warp_sum(s);
   }
   if (lane == 0) a.z[static_cast<size_t>(t) * a.r + i] = a.scale * s;
 }
 
 // CUDA-core projection: 32 tokens x 64 features per CTA (both halves of a gated feature).
-template <typename T, bool GATED>
+template <bool GATED>
 __global__ void __launch_bounds__(256) fused_simt_kernel(const DenseFusedArgs a) {
   constexpr int NH = GATED ? 2 : 1;
   __shared__ float xs[32][33];
@@ -77,19 +55,19 @@ __global__ void __launch_bounds__(256) fused_simt_kernel(const DenseFusedArgs a)
   const int tid = threadIdx.x;
   const int ty = tid >> 4, tx = tid & 15;
   const int t0 = blockIdx.y * 32, f0 = blockIdx.x * 64;
-  const T* x = static_cast<const T*>(a.x);
-  const T* w = static_cast<const T*>(a.w);
+  const float* x = static_cast<const float*>(a.x);
+  const float* w = static_cast<const float*>(a.w);
   float acc[NH][2][4] = {};
   for (int k0 = 0; k0 < a.h_in; k0 += 32) {
     for (int idx = tid; idx < 32 * 32; idx += 256) {
       const int rr = idx >> 5, kk = idx & 31;
       const int t = t0 + rr, k = k0 + kk;
-      xs[rr][kk] = (t < a.T && k < a.h_in) ? ld1(x + static_cast<size_t>(t) * a.h_in + k) : 0.f;
+      xs[rr][kk] = (t < a.T && k < a.h_in) ? *(x + static_cast<size_t>(t) * a.h_in + k) : 0.f;
     }
     for (int idx = tid; idx < NH * 64 * 32; idx += 256) {
       const int h = idx >> 11, rr = (idx >> 5) & 63, kk = idx & 31;
       const int f = f0 + rr, k = k0 + kk;
-      ws[h][rr][kk] = (f < a.h_out && k < a.h_in) ? ld1(w + (static_cast<size_t>(h) * a.h_out + f) * a.h_in + k) : 0.f;
+      ws[h][rr][kk] = (f < a.h_out && k < a.h_in) ? *(w + (static_cast<size_t>(h) * a.h_out + f) * a.h_in + k) : 0.f;
     }
     __syncthreads();
 #pragma unroll 8
@@ -120,39 +98,54 @@ __global__ void __launch_bounds__(256) fused_simt_kernel(const DenseFusedArgs a)
       for (int h = 0; h < NH; ++h) {
         v[h] = acc[h][u][j];
         const int fh = f + h * a.h_out;
-        if (a.bias != nullptr) v[h] += ld1(static_cast<const T*>(a.bias) + fh);
+        if (a.bias != nullptr) v[h] += *(static_cast<const float*>(a.bias) + fh);
         if (ad >= 0) {
           const float* zr = a.z + static_cast<size_t>(t) * a.r;
-          const T* bp = static_cast<const T*>(a.lora_b) + static_cast<size_t>(ad) * a.r * a.n + fh;
-          for (int i = 0; i < a.r; ++i) v[h] = fmaf(zr[i], ld1(bp + static_cast<size_t>(i) * a.n), v[h]);
+          const float* bp = static_cast<const float*>(a.lora_b) + static_cast<size_t>(ad) * a.r * a.n + fh;
+          for (int i = 0; i < a.r; ++i) v[h] = fmaf(zr[i], *(bp + static_cast<size_t>(i) * a.n), v[h]);
         }
       }
       float o = GATED ? silu(v[0]) * v[NH - 1] : act_apply(a.act, v[0]);
       const size_t at = static_cast<size_t>(t) * a.h_out + f;
-      if (a.residual != nullptr) o += ld1(static_cast<const T*>(a.residual) + at);
-      st1(static_cast<T*>(a.y) + at, o);
+      if (a.residual != nullptr) o += *(static_cast<const float*>(a.residual) + at);
+      static_cast<float*>(a.y)[at] = o;
     }
   }
 }
 
-template <typename T>
 static cudaError_t launch_simt(const DenseFusedArgs& a, cudaStream_t st) {
   if (a.r > 0) {
     ProfScope ps(K_FUSED_SHRINK, st);
     const long long warps = static_cast<long long>(a.T) * a.r;
-    fused_shrink_simt<T><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, st>>>(a);
+    fused_shrink_simt<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, st>>>(a);
     count_launch();
   }
   ProfScope ps(K_DENSE_FUSED, st);
   const dim3 grid((a.h_out + 63) / 64, (a.T + 31) / 32);
-  if (a.act == ML_ACT_SILU_AND_MUL) fused_simt_kernel<T, true><<<grid, 256, 0, st>>>(a);
-  else fused_simt_kernel<T, false><<<grid, 256, 0, st>>>(a);
+  if (a.act == ML_ACT_SILU_AND_MUL) fused_simt_kernel<true><<<grid, 256, 0, st>>>(a);
+  else fused_simt_kernel<false><<<grid, 256, 0, st>>>(a);
   count_launch();
   return cudaGetLastError();
 }
 
+// Token counts up to here take the weight-streaming kernel (all tokens in the MMA's N), more
+// the tiled one.
+constexpr int kDecodeTokens = 256;
+
 cudaError_t launch_dense_fused(const DenseFusedArgs& a, cudaStream_t st) {
   if (a.T <= 0) return cudaSuccess;
+  if (!a.f32) {
+    FusedTcArgs f{};
+    f.a = a;
+    f.z = reinterpret_cast<__nv_bfloat16*>(a.z);
+    f.tile_mask = a.tile_mask;
+    f.bad = reinterpret_cast<uint64_t*>(a.status + 32);  // in the status block, cleared with it
+    if (a.r > 0) {
+      const cudaError_t e = launch_fused_shrink_tc(f, st);
+      if (e != cudaSuccess) return e;
+    }
+    return a.T <= kDecodeTokens ? launch_fused_decode_tc(f, st) : launch_fused_prefill_tc(f, st);
+  }
   if (a.r > 0) {
     ProfScope ps(K_FUSED_SHRINK, st);
     const int n = a.T > a.S ? a.T : a.S;
@@ -160,7 +153,7 @@ cudaError_t launch_dense_fused(const DenseFusedArgs& a, cudaStream_t st) {
                                                         a.status);
     count_launch();
   }
-  return a.f32 ? launch_simt<float>(a, st) : launch_simt<__nv_bfloat16>(a, st);
+  return launch_simt(a, st);
 }
 
 }  // namespace mlb

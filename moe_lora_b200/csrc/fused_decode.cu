@@ -1,0 +1,396 @@
+// dense_lora_fused for few tokens (T <= 256): y = act(x W^T + bias + z B) + residual.
+//
+// Bound by the weight stream from HBM.  As in the grouped GEMM the weight rows fill the
+// MMA's M (128 rows; gated: 64 gate rows and the matching 64 up rows) and all T tokens its N
+// ([SageMaker MoE kernels page], first item: the large dimension as the first operand), so
+// each weight is read once.  h_out / 128 tiles are too few or too uneven for 148 SMs, so a
+// cluster of C CTAs splits h_in for one tile: each streams its K range, then adds up every
+// C-th token's partial sums from its peers' shared memory, in rank order (the same bits
+// every time), and finishes those rows: bias, activation, residual, one rounding, 8-byte
+// stores of 128 neighbouring features per warp.
+//
+// Adapters: h = [x, z] [W; B].  The tokens' adapters follow as extra K columns (see
+// AdapterGroups), B_a^T read as the MN-major A operand straight from its storage order; the
+// groups are dealt out over the cluster.  They wait for the shrink kernel, which this kernel
+// overlaps (programmatic dependent launch): only the adapters' part needs z.
+#include "fused_tc.cuh"
+#include "prof.h"
+
+#include <algorithm>
+#include <atomic>
+
+namespace mlb {
+
+constexpr int kFdThreads = 192;
+constexpr int kFdMaxStages = 8;
+constexpr int kFdPitch = 132;  // floats per token row of partial sums (128 features)
+
+struct FdParams {
+  const __nv_bfloat16* bias;
+  const __nv_bfloat16* residual;
+  __nv_bfloat16* y;
+  const __nv_bfloat16* z;
+  const __nv_bfloat16* lora_b;
+  const int32_t* row_adapter;
+  const uint64_t* tile_mask;
+  const uint64_t* bad;
+  int* status;
+  int T, K, h_out, n, r, act, gated, C, stages;
+  int clear_status;  // no shrink kernel ahead: this kernel's first thread clears the status
+};
+
+struct FdCore {
+  uint64_t full[kFdMaxStages], empty[kFdMaxStages], zgo[kFdMaxStages], zfull[kFdMaxStages], tfull;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+template <int BN>
+struct FdCfg {
+  static constexpr int kStageBytes = 128 * 128 + BN * 128;
+  static constexpr int kTmemCols = BN < 32 ? 32 : BN;
+  // two CTAs per SM up to 128 tokens (108 KB of ring each), one above
+  static constexpr int kBudget = BN <= 128 ? 108 * 1024 : 200 * 1024;
+  static constexpr int kStages = kBudget / kStageBytes < kFdMaxStages ? kBudget / kStageBytes : kFdMaxStages;
+  static constexpr int kPart = BN * kFdPitch * 4;
+  static constexpr int kRing = kStages * kStageBytes > kPart ? kStages * kStageBytes : kPart;
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
+    fused_decode_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmx,
+                        const __grid_constant__ CUtensorMap tmb, const FdParams p) {
+  using Cfg = FdCfg<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* part = reinterpret_cast<float*>(ring);  // [BN][kFdPitch], once the ring is idle
+  __shared__ FdCore sm;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int S = Cfg::kStages;
+  volatile int* abort_flag = &sm.abort_flag;
+  const int rank = static_cast<int>(blockIdx.x) % p.C;
+  const int tile = static_cast<int>(blockIdx.x) / p.C;
+  const int f0 = tile * (p.gated ? 64 : 128);
+  const int row1 = p.gated ? p.h_out + f0 : f0 + 64;  // the tile's second 64 weight rows
+  const int nkb = (p.K + 63) / 64;
+  const int kb0 = static_cast<int>(static_cast<long long>(nkb) * rank / p.C);
+  const int kb1 = static_cast<int>(static_cast<long long>(nkb) * (rank + 1) / p.C);
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.zgo[s], 1);
+      mbar_init(&sm.zfull[s], 128);
+    }
+    mbar_init(&sm.tfull, 1);
+    sm.abort_flag = 0;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&tmw);
+    tma_prefetch_desc(&tmx);
+    if (p.clear_status && blockIdx.x == 0) p.status[0] = 0;
+  }
+  if (warp == 1) tmem_alloc(&sm.tmem_base, Cfg::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  // the adapters of the (at most two 128-token) tiles, known once the shrink kernel is done
+  auto adapter_mask = [&]() -> uint64_t {
+    if (p.r == 0) return 0ull;
+    pdl_wait();
+    uint64_t m = *reinterpret_cast<const volatile uint64_t*>(p.tile_mask);
+    if (p.T > 128) m |= *reinterpret_cast<const volatile uint64_t*>(p.tile_mask + 1);
+    return m & ~*reinterpret_cast<const volatile uint64_t*>(p.bad);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, filled = 0, parity_of = 0;
+      bool ok = true;
+      auto advance = [&]() {
+        filled |= 1u << stage;
+        parity_of = (parity_of & ~(1u << stage)) | (phase << stage);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 50);
+        if (!ok) break;
+        uint8_t* s = ring + stage * Cfg::kStageBytes;
+        mbar_arrive_expect_tx(&sm.full[stage], Cfg::kStageBytes);
+        tma_load_2d(s, &tmw, &sm.full[stage], kb * 64, f0);
+        tma_load_2d(s + 64 * 128, &tmw, &sm.full[stage], kb * 64, row1);
+        tma_load_2d(s + 128 * 128, &tmx, &sm.full[stage], kb * 64, 0);
+        advance();
+      }
+      AdapterGroups g(ok ? adapter_mask() : 0ull, p.r);
+      for (int gi = 0; ok && g.next(); ++gi) {
+        if (gi % p.C != rank) continue;
+        ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 51);
+        if (!ok) break;
+        mbar_arrive(&sm.zgo[stage]);  // the z tile may be written
+        uint8_t* s = ring + stage * Cfg::kStageBytes;
+        const int rb = p.r < 64 ? p.r : 64;
+        // an odd adapter of rank 8 fills half an MMA step: its rows once more meet zeros of z
+        const int boxes = (p.r == 8 && (g.na & 1)) ? g.na + 1 : g.na;
+        mbar_arrive_expect_tx(&sm.full[stage], static_cast<uint32_t>(2 * boxes * rb) * 128u);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          if (q >= boxes) break;
+          const int id = (q > 0 && q >= g.na) ? g.ids[q > 0 ? q - 1 : 0] : g.ids[q];
+          tma_load_2d(s + q * rb * 128, &tmb, &sm.full[stage], f0, id * p.r + g.k0);
+          tma_load_2d(s + 64 * 128 + q * rb * 128, &tmb, &sm.full[stage], row1, id * p.r + g.k0);
+        }
+        advance();
+      }
+      if (*abort_flag)  // let our own copies land before the ring is reused
+        for (int s = 0; s < S; ++s)
+          if (filled & (1u << s)) {
+            volatile int dummy = 0;
+            mbar_wait(&sm.full[s], (parity_of >> s) & 1u, &dummy, nullptr, kFtWaitNs / 4, 0);
+          }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0, zi = 0;
+      uint32_t phase = 0;
+      bool ok = true, any = false;
+      const int n_mma = min(BN, (p.T + 15) & ~15);
+      const uint32_t idesc = umma_idesc_bf16(128, n_mma);
+      auto advance = [&]() {
+        umma_commit(&sm.empty[stage]);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 52);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t s = smem_u32(ring + stage * Cfg::kStageBytes);
+        const uint64_t ad = umma_desc_sw128(s), bd = umma_desc_sw128(s + 128 * 128);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          umma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, any ? 1u : 0u);
+          any = true;
+        }
+        advance();
+      }
+      // adapters: A = B_a^T, MN-major (64-feature blocks 8 KB apart), 16 rank rows per step
+      const uint32_t zdesc = umma_idesc_bf16_amn(128, n_mma);
+      AdapterGroups g(ok ? adapter_mask() : 0ull, p.r);
+      for (int gi = 0; ok && g.next(); ++gi) {
+        if (gi % p.C != rank) continue;
+        ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 53) &&
+             mbar_wait(&sm.zfull[stage], static_cast<uint32_t>(zi / S) & 1u, abort_flag, p.status, kFtWaitNs, 54);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t s = smem_u32(ring + stage * Cfg::kStageBytes);
+        const uint64_t ad = umma_desc_mn_sw128(s, 64 * 128), bd = umma_desc_sw128(s + 128 * 128);
+        const int steps = p.r > 64 ? 4 : (g.na * p.r + 15) / 16;
+        for (int k = 0; k < steps; ++k) {
+          umma_bf16(tmem, ad + 128 * k, bd + 2 * k, zdesc, any ? 1u : 0u);
+          any = true;
+        }
+        ++zi;
+        advance();
+      }
+      umma_commit(&sm.tfull);
+      volatile int dummy = 0;
+      mbar_wait(&sm.tfull, 0, &dummy, nullptr, kFtWaitNs, 0);  // the MMAs are done with the ring
+    }
+    __syncwarp();
+  } else {
+    // z tiles of this CTA's adapter groups, then the accumulator -> partial sums
+    const int e = tid - 64;
+    bool any = kb1 > kb0;
+    if (p.r) {
+      int stage = (kb1 - kb0) % S, zi = 0;
+      AdapterGroups g(adapter_mask(), p.r);
+      bool ok = true;
+      for (int gi = 0; ok && g.next(); ++gi) {
+        if (gi % p.C != rank) continue;
+        any = true;
+        ok = mbar_wait(&sm.zgo[stage], static_cast<uint32_t>(zi / S) & 1u, abort_flag, p.status, kFtWaitNs, 55);
+        if (!ok) break;
+        write_z_tile(ring + stage * Cfg::kStageBytes + 128 * 128, g, p.z, p.row_adapter, 0, BN, p.T, p.r, e, 128);
+        fence_proxy_async_smem();
+        mbar_arrive(&sm.zfull[stage]);
+        ++zi;
+        if (++stage == S) stage = 0;
+      }
+    }
+    bool got = mbar_wait(&sm.tfull, 0, abort_flag, p.status, kFtWaitNs, 56);
+    got = named_bar_and(1, 128, got);
+    if (got) {
+      tc_fence_after();
+      const int g4 = warp & 3, m = g4 * 32 + lane;
+      for (int c0 = 0; c0 < p.T; c0 += 32) {
+        float v[32];
+        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(g4 * 32) << 16) + c0, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (c0 + j < BN) part[(c0 + j) * kFdPitch + m] = any ? v[j] : 0.f;
+      }
+      tc_fence_before();
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();
+
+  // tokens rank, rank + C, ...: a warp per token, 4 features per lane (gated: lanes 0-15 the
+  // gate's 64 features, lanes 16-31 the up projection's)
+  if (p.r) pdl_wait();  // z and the adapter ids, where a broken adapter needs them
+  if (!*abort_flag) {
+    const int col = p.gated ? ((lane < 16 ? 0 : p.h_out) + f0 + 4 * (lane & 15)) : f0 + 4 * lane;  // row of W
+    const int feat = p.gated ? f0 + 4 * (lane & 15) : col;
+    const bool in = feat < p.h_out;
+    float b[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.bias != nullptr && in) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p.bias + col));
+      b[0] = __uint_as_float(v.x << 16);
+      b[1] = __uint_as_float(v.x & 0xFFFF0000u);
+      b[2] = __uint_as_float(v.y << 16);
+      b[3] = __uint_as_float(v.y & 0xFFFF0000u);
+    }
+    const uint64_t bad = p.r ? *reinterpret_cast<const volatile uint64_t*>(p.bad) : 0ull;
+    for (int t = rank + p.C * warp; t < p.T; t += p.C * (kFdThreads / 32)) {
+      const bool writer = in && (!p.gated || lane < 16);
+      uint2 res = make_uint2(0u, 0u);
+      if (p.residual != nullptr && writer)
+        res = *reinterpret_cast<const uint2*>(p.residual + static_cast<size_t>(t) * p.h_out + feat);
+      const uint32_t at = smem_u32(part + t * kFdPitch + 4 * lane);
+      float h[4] = {b[0], b[1], b[2], b[3]};
+      for (int c = 0; c < p.C; ++c) {
+        const float4 v = ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(c)));
+        h[0] += v.x;
+        h[1] += v.y;
+        h[2] += v.z;
+        h[3] += v.w;
+      }
+      if (bad != 0) {  // an adapter with values that are not finite: its own tokens only
+        const int ad = p.row_adapter[t];
+        if (ad >= 0 && (bad >> ad & 1ull) && in)
+          for (int i = 0; i < p.r; ++i) {
+            const float zi = __bfloat162float(p.z[static_cast<size_t>(t) * p.r + i]);
+            const __nv_bfloat16* br = p.lora_b + (static_cast<size_t>(ad) * p.r + i) * p.n + col;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = fmaf(zi, __bfloat162float(br[j]), h[j]);
+          }
+      }
+      float o[4];
+      if (p.gated) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = silu(h[j]) * __shfl_down_sync(0xffffffffu, h[j], 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = act_apply(p.act, h[j]);
+      }
+      o[0] += __uint_as_float(res.x << 16);
+      o[1] += __uint_as_float(res.x & 0xFFFF0000u);
+      o[2] += __uint_as_float(res.y << 16);
+      o[3] += __uint_as_float(res.y & 0xFFFF0000u);
+      if (writer)
+        *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(t) * p.h_out + feat) =
+            make_uint2(pack2_bf16(o[0], o[1]), pack2_bf16(o[2], o[3]));
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();  // the peers have read this CTA's partial sums
+  if (warp == 1) tmem_dealloc(tmem, Cfg::kTmemCols);
+}
+
+template <int BN>
+static cudaError_t launch_bn(const FusedTcArgs& f, cudaStream_t st) {
+  using Cfg = FdCfg<BN>;
+  const DenseFusedArgs& a = f.a;
+  CUtensorMap tmw, tmx, tmb;
+  if (encode_tmap_2d(&tmw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.w, a.h_in, a.n, static_cast<uint64_t>(a.h_in) * 2, 64,
+                     64, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+      encode_tmap_2d(&tmx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.h_in, a.T, static_cast<uint64_t>(a.h_in) * 2, 64,
+                     BN, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  tmb = tmx;
+  if (a.r && encode_tmap_2d(&tmb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.lora_b, a.n, static_cast<uint64_t>(a.L) * a.r,
+                            static_cast<uint64_t>(a.n) * 2, 64, a.r < 64 ? a.r : 64,
+                            CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  FdParams p{};
+  p.bias = static_cast<const __nv_bfloat16*>(a.bias);
+  p.residual = static_cast<const __nv_bfloat16*>(a.residual);
+  p.y = static_cast<__nv_bfloat16*>(a.y);
+  p.z = f.z;
+  p.lora_b = static_cast<const __nv_bfloat16*>(a.lora_b);
+  p.row_adapter = a.row_adapter;
+  p.tile_mask = f.tile_mask;
+  p.bad = f.bad;
+  p.status = a.status;
+  p.T = a.T;
+  p.K = a.h_in;
+  p.h_out = a.h_out;
+  p.n = a.n;
+  p.r = a.r;
+  p.act = a.act;
+  p.gated = a.act == ML_ACT_SILU_AND_MUL;
+  p.clear_status = a.r == 0;
+  const int tiles = p.gated ? (a.h_out + 63) / 64 : (a.h_out + 127) / 128;
+  // K splits: the smallest cluster that fills the slots of one wave best (a split must keep
+  // at least two K blocks)
+  const int slots = a.num_sms * (BN <= 128 ? 2 : 1), nkb = (a.h_in + 63) / 64;
+  double best = 0.0;
+  p.C = 1;
+  for (int c = 1; c <= 8 && (c == 1 || nkb / c >= 2); ++c) {
+    const long long n = static_cast<long long>(tiles) * c;
+    const double fill = static_cast<double>(n) / (static_cast<double>((n + slots - 1) / slots) * slots);
+    if (fill > best * 1.05) {
+      best = fill;
+      p.C = c;
+    }
+  }
+  const size_t smem = 1024 + Cfg::kRing;
+  static std::atomic<bool> attr_set[kMaxDevices];
+  const int dev = current_device_index();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(fused_decode_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  ProfScope ps(K_DENSE_FUSED, st);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(tiles * p.C);
+  cfg.blockDim = dim3(kFdThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.r ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fused_decode_kernel<BN>, tmw, tmx, tmb, p);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_fused_decode_tc(const FusedTcArgs& f, cudaStream_t st) {
+  const int T = f.a.T;
+  if (T <= 16) return launch_bn<16>(f, st);
+  if (T <= 32) return launch_bn<32>(f, st);
+  if (T <= 64) return launch_bn<64>(f, st);
+  if (T <= 128) return launch_bn<128>(f, st);
+  return launch_bn<256>(f, st);
+}
+
+}  // namespace mlb

@@ -1,0 +1,332 @@
+// Shrink of dense_lora_fused on the tensor cores: z_t = c x_t A_a(t), bf16
+// ([vLLM MoE-LoRA page], "O Papel da Multi-LoRA"; split-K, "Otimizações em Nível de Kernel").
+//
+// A tile of 128 tokens fills the MMA's M; its N takes the rank rows of 128 / r of the tile's
+// adapters at a time, so every token meets each of them and keeps the columns of its own.
+// A cluster of C CTAs splits h_in: each holds fp32 partial sums of all 128 tokens, then adds
+// up 128 / C tokens' partials in rank order from its peers' shared memory (no atomics: the
+// same bits every time).
+//
+// The launch's other clusters read the B rows of the adapters in use and record which hold
+// a value that is not finite: the projection keeps those out of its matrix product, where a
+// zero times an infinity would reach other tenants' tokens.  The rows read stay in L2, where
+// the projection finds them.
+#include "fused_tc.cuh"
+#include "prof.h"
+
+#include <algorithm>
+#include <atomic>
+
+namespace mlb {
+
+constexpr int kShThreads = 192;
+constexpr int kShStages = 4;
+constexpr int kShN = 128;
+constexpr int kShStageBytes = 2 * 128 * 128;
+
+struct ShParams {
+  const int32_t* seg_offsets;
+  const int32_t* seg_adapter;
+  int S, T, L, r, K, n;
+  float scale;
+  const __nv_bfloat16* lora_b;
+  __nv_bfloat16* z;
+  int32_t* row_adapter;
+  uint64_t* tile_mask;
+  unsigned long long* bad;
+  int* status;
+  int C, P, main_ctas, scan_ctas;
+};
+
+struct ShCore {
+  uint64_t full[kShStages], empty[kShStages], tfull, tempty;
+  uint32_t tmem_base;
+  int abort_flag;
+  unsigned mask[2];
+  int row_ad[128];
+};
+
+// adapters used by any segment that holds a token
+__device__ __forceinline__ void used_adapters(const ShParams& p, unsigned* mask, int tid, int n) {
+  for (int s = tid; s < p.S; s += n) {
+    const int a = p.seg_adapter[s];
+    if (a >= 0 && a < p.L && p.seg_offsets[s + 1] > p.seg_offsets[s]) atomicOr(&mask[a >> 5], 1u << (a & 31));
+  }
+}
+
+__global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_constant__ CUtensorMap tmx,
+                                                                 const __grid_constant__ CUtensorMap tma,
+                                                                 const ShParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* part = reinterpret_cast<float*>(ring + kShStages * kShStageBytes);  // [128][r + 4]
+  __shared__ ShCore sm;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();  // the projection streams its weights meanwhile
+
+  if (static_cast<int>(blockIdx.x) >= p.main_ctas) {
+    // ------------------------------------------------------------ B rows that are not finite
+    if (tid < 2) sm.mask[tid] = 0u;
+    __syncthreads();
+    used_adapters(p, sm.mask, tid, kShThreads);
+    __syncthreads();
+    uint64_t rem = sm.mask[0] | (static_cast<uint64_t>(sm.mask[1]) << 32);
+    const long long chunks = static_cast<long long>(p.r) * p.n / 8;  // 16 bytes each
+    const long long step = static_cast<long long>(p.scan_ctas) * kShThreads;
+    const long long first = static_cast<long long>(blockIdx.x - p.main_ctas) * kShThreads + tid;
+    while (rem != 0) {
+      const int a = __ffsll(static_cast<long long>(rem)) - 1;
+      rem &= rem - 1;
+      const uint4* b = reinterpret_cast<const uint4*>(p.lora_b) + static_cast<size_t>(a) * chunks;
+      bool hit = false;
+#pragma unroll 4
+      for (long long i = first; i < chunks; i += step) {
+        const uint4 v = __ldg(b + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // exponent bits all ones in either half
+          hit |= (w[j] & 0x7F80u) == 0x7F80u || (w[j] & 0x7F800000u) == 0x7F800000u;
+      }
+      if (hit) atomicOr(p.bad, 1ull << a);
+    }
+    return;
+  }
+
+  const int rank = static_cast<int>(blockIdx.x) % p.C;
+  const int group = static_cast<int>(blockIdx.x) / p.C;  // cluster index
+  const int tile = group / p.P, chunk0 = group % p.P;
+  const int t0 = tile * 128;
+  volatile int* abort_flag = &sm.abort_flag;
+  if (tid == 0) {
+    for (int s = 0; s < kShStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    mbar_init(&sm.tfull, 1);
+    mbar_init(&sm.tempty, 128);
+    sm.abort_flag = 0;
+    sm.mask[0] = sm.mask[1] = 0u;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) tmem_alloc(&sm.tmem_base, kShN);
+  __syncthreads();
+  // each token's adapter: the last segment that begins at or before it and ends behind it
+  if (tid < 128) {
+    const int t = t0 + tid;
+    int a = -1;
+    if (t < p.T) {
+      int lo = 0, hi = p.S;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.seg_offsets[mid] <= t) lo = mid;
+        else hi = mid;
+      }
+      if (p.seg_offsets[lo] <= t && t < p.seg_offsets[lo + 1]) a = p.seg_adapter[lo];
+      if (a >= p.L || a < 0) a = -1;
+      if (chunk0 == 0 && rank == 0) p.row_adapter[t] = a;
+    }
+    sm.row_ad[tid] = a;
+    if (a >= 0) atomicOr(&sm.mask[a >> 5], 1u << (a & 31));
+  }
+  if (group == 0 && rank == 0)  // segments that run backwards or leave [0, T], unknown adapters
+    for (int s = tid; s < p.S; s += kShThreads)
+      if (p.seg_offsets[s] > p.seg_offsets[s + 1] || p.seg_offsets[s] < 0 || p.seg_offsets[s + 1] > p.T ||
+          p.seg_adapter[s] < -1 || p.seg_adapter[s] >= p.L)
+        set_status(p.status, MOE_LORA_ERR_DEVICE_CHECK, s);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint64_t mask = sm.mask[0] | (static_cast<uint64_t>(sm.mask[1]) << 32);
+  if (tid == 0 && chunk0 == 0 && rank == 0) p.tile_mask[tile] = mask;
+  const uint32_t tmem = sm.tmem_base;
+  const int apc = kShN / p.r;  // adapters per chunk
+  const int cnt = __popcll(mask);
+  const int chunks = (cnt + apc - 1) / apc;
+  const int nkb = (p.K + 63) / 64;
+  const int kb0 = static_cast<int>(static_cast<long long>(nkb) * rank / p.C);
+  const int kb1 = static_cast<int>(static_cast<long long>(nkb) * (rank + 1) / p.C);
+  const int pitch = p.r + 4;  // floats per partial row: 16-byte aligned, rows on other banks
+  int stage = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  uint32_t filled = 0, parity_of = 0;
+
+  for (int ch = chunk0, it = 0; ch < chunks; ch += p.P, ++it) {
+    // the chunk's adapters: bits [ch apc, ch apc + na) of the mask
+    uint64_t rem = mask;
+    for (int i = 0; i < ch * apc; ++i) rem &= rem - 1;
+    const int na = min(apc, cnt - ch * apc);
+    if (warp == 0) {
+      if (lane == 0) {
+        for (int kb = kb0; ok && kb < kb1; ++kb) {
+          ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 40);
+          if (!ok) break;
+          uint8_t* s = ring + stage * kShStageBytes;
+          mbar_arrive_expect_tx(&sm.full[stage], 128u * 128u + static_cast<uint32_t>(na * p.r) * 128u);
+          tma_load_2d(s, &tmx, &sm.full[stage], kb * 64, t0);
+          uint64_t m = rem;
+          for (int q = 0; q < na; ++q, m &= m - 1) {
+            const int a = __ffsll(static_cast<long long>(m)) - 1;
+            tma_load_2d(s + 128 * 128 + q * p.r * 128, &tma, &sm.full[stage], kb * 64, a * p.r);
+          }
+          filled |= 1u << stage;
+          parity_of = (parity_of & ~(1u << stage)) | (phase << stage);
+          if (++stage == kShStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      if (lane == 0) {
+        const uint32_t idesc = umma_idesc_bf16(128, (na * p.r + 15) & ~15);
+        ok = ok && mbar_wait(&sm.tempty, (static_cast<uint32_t>(it) & 1u) ^ 1u, abort_flag, p.status, kFtWaitNs, 41);
+        tc_fence_after();
+        for (int kb = kb0; ok && kb < kb1; ++kb) {
+          ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 42);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t s = smem_u32(ring + stage * kShStageBytes);
+          const uint64_t ad = umma_desc_sw128(s), bd = umma_desc_sw128(s + 128 * 128);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) umma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
+          umma_commit(&sm.empty[stage]);
+          if (++stage == kShStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        umma_commit(&sm.tfull);
+      }
+      __syncwarp();
+    } else {
+      // this token's columns of its own adapter -> its partial row
+      const int g4 = warp & 3, row = g4 * 32 + lane;
+      bool got = mbar_wait(&sm.tfull, static_cast<uint32_t>(it) & 1u, abort_flag, p.status, kFtWaitNs, 43);
+      got = named_bar_and(1, 128, got);
+      if (got && kb1 > kb0) {
+        tc_fence_after();
+        const int a = sm.row_ad[row];
+        int mine = -1;  // this token's adapter among the chunk's
+        if (a >= 0 && (rem >> a & 1ull)) {
+          mine = __popcll(rem & ((1ull << a) - 1ull));
+          if (mine >= na) mine = -1;
+        }
+        for (int c0 = 0; c0 < na * p.r; c0 += 32) {
+          float v[32];
+          tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(g4 * 32) << 16) + c0, v);
+          // columns [c0, c0 + 32) against this token's [mine r, mine r + r)
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            const int i = c0 + j - mine * p.r;
+            if (mine >= 0 && i >= 0 && i < p.r) {
+              float4* d = reinterpret_cast<float4*>(part + row * pitch + i);
+              d[0] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+              d[1] = make_float4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
+            }
+          }
+        }
+        tc_fence_before();
+      } else if (got) {  // no K block of its own: its share of the sum is zero
+        for (int i = 0; i < p.r; ++i) part[row * pitch + i] = 0.f;
+      }
+      mbar_arrive(&sm.tempty);
+    }
+    cluster_sync_all();
+    // rows [rank 128 / C, ...): sum over the cluster in rank order
+    const int rows = 128 / p.C, q4 = p.r / 4;
+    for (int e = tid; e < rows * q4; e += kShThreads) {
+      const int row = rank * rows + e / q4, i = (e % q4) * 4;
+      const int a = sm.row_ad[row];
+      if (a < 0 || !(rem >> a & 1ull) || __popcll(rem & ((1ull << a) - 1ull)) >= na) continue;
+      const uint32_t at = smem_u32(part + row * pitch + i);
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < p.C; ++c) {
+        const float4 v = ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(c)));
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+      }
+      uint2 o;
+      o.x = pack2_bf16(p.scale * s.x, p.scale * s.y);
+      o.y = pack2_bf16(p.scale * s.z, p.scale * s.w);
+      *reinterpret_cast<uint2*>(p.z + static_cast<size_t>(t0 + row) * p.r + i) = o;
+    }
+    cluster_sync_all();  // the peers have read this CTA's partials
+  }
+  if (warp == 0 && lane == 0 && *abort_flag)  // let our own copies land before the CTA exits
+    for (int s = 0; s < kShStages; ++s)
+      if (filled & (1u << s)) {
+        volatile int dummy = 0;
+        mbar_wait(&sm.full[s], (parity_of >> s) & 1u, &dummy, nullptr, kFtWaitNs / 4, 0);
+      }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kShN);
+}
+
+cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, cudaStream_t st) {
+  const DenseFusedArgs& a = f.a;
+  CUtensorMap tmx, tma;
+  if (encode_tmap_2d(&tmx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.h_in, a.T, static_cast<uint64_t>(a.h_in) * 2, 64,
+                     128, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+      encode_tmap_2d(&tma, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.lora_a, a.h_in, static_cast<uint64_t>(a.L) * a.r,
+                     static_cast<uint64_t>(a.h_in) * 2, 64, a.r, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  ShParams p{};
+  p.seg_offsets = a.seg_offsets;
+  p.seg_adapter = a.seg_adapter;
+  p.S = a.S;
+  p.T = a.T;
+  p.L = a.L;
+  p.r = a.r;
+  p.K = a.h_in;
+  p.n = a.n;
+  p.scale = a.scale;
+  p.lora_b = static_cast<const __nv_bfloat16*>(a.lora_b);
+  p.z = f.z;
+  p.row_adapter = a.row_adapter;
+  p.tile_mask = f.tile_mask;
+  p.bad = reinterpret_cast<unsigned long long*>(f.bad);
+  p.status = a.status;
+  // K splits: as many as keep one wave of CTAs (one per SM: 128 KB of ring each)
+  const int tiles = (a.T + 127) / 128;
+  p.C = 8;
+  while (p.C > 1 && tiles * p.C > a.num_sms) p.C /= 2;
+  // chunks of a tile side by side while SMs are left
+  const int apc = kShN / a.r, most = (std::min(std::min(a.L, a.S), 128) + apc - 1) / apc;
+  p.P = std::max(1, std::min(most, a.num_sms / (tiles * p.C)));
+  p.main_ctas = tiles * p.P * p.C;
+  p.scan_ctas = std::max(8, a.num_sms / 2 / p.C * p.C);
+  const size_t smem = 1024 + kShStages * kShStageBytes + 128u * (a.r + 4) * 4;
+  static std::atomic<bool> attr_set[kMaxDevices];
+  const int dev = current_device_index();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(fused_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               1024 + kShStages * kShStageBytes + 128 * (128 + 4) * 4);
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  ProfScope ps(K_FUSED_SHRINK, st);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.main_ctas + p.scan_ctas);
+  cfg.blockDim = dim3(kShThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fused_shrink_kernel, tmx, tma, p);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace mlb

@@ -223,8 +223,9 @@ struct DenseFusedArgs {
   const void* residual;       // [T][h_out] or null (may be y)
   void* y;
   bool f32;
-  float* z;                   // workspace [T][r]: scale (x A), fp32
+  float* z;                   // workspace [T][r]: scale (x A), fp32 (bf16 projections: bf16)
   int32_t* row_adapter;       // workspace [T]
+  uint64_t* tile_mask;        // workspace: adapters of each 128-token tile (bf16)
   int* status;
   int num_sms;
 };
