@@ -271,6 +271,7 @@ struct FusedWs {
   float* z;
   int32_t* row_adapter;
   uint64_t* tile_mask;
+  uint64_t* bad_part;
   size_t bytes;
 };
 
@@ -287,6 +288,7 @@ FusedWs fused_layout(void* base, int T, int r) {
   w.z = reinterpret_cast<float*>(take(static_cast<size_t>(T) * r * 4));
   w.row_adapter = reinterpret_cast<int32_t*>(take(r ? static_cast<size_t>(T) * 4 : 0));
   w.tile_mask = reinterpret_cast<uint64_t*>(take(r ? (static_cast<size_t>(T) + 127) / 128 * 8 : 0));
+  w.bad_part = reinterpret_cast<uint64_t*>(take(r && T ? kFusedScanMax * 8 : 0));
   w.bytes = off;
   return w;
 }
@@ -1145,9 +1147,8 @@ moe_lora_status dense_lora_fused(const void* x, const void* w, const void* bias,
   const FusedWs ws = fused_layout(workspace, T, rr);
   if (dt == ML_BF16 && !tensor_map_encode_available())
     return fail(MOE_LORA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  // the status word, and (bf16) the mask of broken adapters beside it; without adapters the
-  // bf16 projection clears the word itself
-  if (dt == ML_F32 || rr > 0) ML_CUDA(cudaMemsetAsync(workspace, 0, kStatusBytes, cs), "status clear");
+  // the status word (the first kernel of a bf16 projection clears it itself)
+  if (dt == ML_F32) ML_CUDA(cudaMemsetAsync(workspace, 0, 8, cs), "status clear");
   DenseFusedArgs a{};
   a.x = x;
   a.w = w;
@@ -1171,6 +1172,7 @@ moe_lora_status dense_lora_fused(const void* x, const void* w, const void* bias,
   a.z = ws.z;
   a.row_adapter = ws.row_adapter;
   a.tile_mask = ws.tile_mask;
+  a.bad_part = ws.bad_part;
   a.status = ws.status;
   a.num_sms = num_sms();
   ML_CUDA(launch_dense_fused(a, cs), "dense_lora_fused launch");

@@ -105,7 +105,13 @@ __global__ void __launch_bounds__(256) fused_simt_kernel(const DenseFusedArgs a)
           for (int i = 0; i < a.r; ++i) v[h] = fmaf(zr[i], *(bp + static_cast<size_t>(i) * a.n), v[h]);
         }
       }
-      float o = GATED ? silu(v[0]) * v[NH - 1] : act_apply(a.act, v[0]);
+      float o;
+      if (GATED) {
+        o = silu(v[0]) * v[NH - 1];
+      } else {
+        act_apply<false>(a.act, v);
+        o = v[0];
+      }
       const size_t at = static_cast<size_t>(t) * a.h_out + f;
       if (a.residual != nullptr) o += *(static_cast<const float*>(a.residual) + at);
       static_cast<float*>(a.y)[at] = o;
@@ -139,7 +145,8 @@ cudaError_t launch_dense_fused(const DenseFusedArgs& a, cudaStream_t st) {
     f.a = a;
     f.z = reinterpret_cast<__nv_bfloat16*>(a.z);
     f.tile_mask = a.tile_mask;
-    f.bad = reinterpret_cast<uint64_t*>(a.status + 32);  // in the status block, cleared with it
+    f.bad = reinterpret_cast<uint64_t*>(a.status + 32);  // in the status block
+    f.bad_part = a.bad_part;
     if (a.r > 0) {
       const cudaError_t e = launch_fused_shrink_tc(f, st);
       if (e != cudaSuccess) return e;

@@ -214,13 +214,16 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
     if (p.r) {
       int stage = (kb1 - kb0) % S, zi = 0;
       AdapterGroups g(adapter_mask(), p.r);
+      ZTile<128, BN / 16> zt;
+      if (g.rem != 0) zt.rows(p.row_adapter, 0, p.T, e);
       bool ok = true;
       for (int gi = 0; ok && g.next(); ++gi) {
         if (gi % p.C != rank) continue;
         any = true;
+        zt.load(g, p.z, 0, p.r, e);
         ok = mbar_wait(&sm.zgo[stage], static_cast<uint32_t>(zi / S) & 1u, abort_flag, p.status, kFtWaitNs, 55);
         if (!ok) break;
-        write_z_tile(ring + stage * Cfg::kStageBytes + 128 * 128, g, p.z, p.row_adapter, 0, BN, p.T, p.r, e, 128);
+        zt.store(ring + stage * Cfg::kStageBytes + 128 * 128, e);
         fence_proxy_async_smem();
         mbar_arrive(&sm.zfull[stage]);
         ++zi;
@@ -285,21 +288,19 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
             for (int j = 0; j < 4; ++j) h[j] = fmaf(zi, __bfloat162float(br[j]), h[j]);
           }
       }
-      float o[4];
       if (p.gated) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = silu(h[j]) * __shfl_down_sync(0xffffffffu, h[j], 16);
+        for (int j = 0; j < 4; ++j) h[j] = sigmoid_of<true>(h[j], h[j]) * __shfl_down_sync(0xffffffffu, h[j], 16);
       } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = act_apply(p.act, h[j]);
+        act_apply<true>(p.act, h);
       }
-      o[0] += __uint_as_float(res.x << 16);
-      o[1] += __uint_as_float(res.x & 0xFFFF0000u);
-      o[2] += __uint_as_float(res.y << 16);
-      o[3] += __uint_as_float(res.y & 0xFFFF0000u);
+      h[0] += __uint_as_float(res.x << 16);
+      h[1] += __uint_as_float(res.x & 0xFFFF0000u);
+      h[2] += __uint_as_float(res.y << 16);
+      h[3] += __uint_as_float(res.y & 0xFFFF0000u);
       if (writer)
         *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(t) * p.h_out + feat) =
-            make_uint2(pack2_bf16(o[0], o[1]), pack2_bf16(o[2], o[3]));
+            make_uint2(pack2_bf16(h[0], h[1]), pack2_bf16(h[2], h[3]));
     }
   }
   __syncwarp();
@@ -341,19 +342,11 @@ static cudaError_t launch_bn(const FusedTcArgs& f, cudaStream_t st) {
   p.gated = a.act == ML_ACT_SILU_AND_MUL;
   p.clear_status = a.r == 0;
   const int tiles = p.gated ? (a.h_out + 63) / 64 : (a.h_out + 127) / 128;
-  // K splits: the smallest cluster that fills the slots of one wave best (a split must keep
-  // at least two K blocks)
+  // K splits: as many as keep one wave (a second wave starts its stream anew: 64 x 4096 ->
+  // 2 x 11008 in 41 us with C = 1, 172 CTAs for 296 slots, 47 us with C = 2; 4096 -> 11008 for
+  // one token 26, 21, 21 and 26 us with C = 1 to 4) and two K blocks per split
   const int slots = a.num_sms * (BN <= 128 ? 2 : 1), nkb = (a.h_in + 63) / 64;
-  double best = 0.0;
-  p.C = 1;
-  for (int c = 1; c <= 8 && (c == 1 || nkb / c >= 2); ++c) {
-    const long long n = static_cast<long long>(tiles) * c;
-    const double fill = static_cast<double>(n) / (static_cast<double>((n + slots - 1) / slots) * slots);
-    if (fill > best * 1.05) {
-      best = fill;
-      p.C = c;
-    }
-  }
+  p.C = std::max(1, std::min(std::min(8, slots / tiles), nkb / 2));
   const size_t smem = 1024 + Cfg::kRing;
   static std::atomic<bool> attr_set[kMaxDevices];
   const int dev = current_device_index();

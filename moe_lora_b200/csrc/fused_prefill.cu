@@ -277,34 +277,44 @@ __global__ void __launch_bounds__(kFpThreads, 1)
           }
         }
         const size_t at = static_cast<size_t>(tok) * p.h_out + f;
+        const int nq = min(4, (p.h_out - f) / 8);  // whole runs of 8 features (h_out is a multiple of 8)
+        if (p.bias != nullptr) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {  // features f + 8 q .. + 8 (h_out is a multiple of 8)
-          if (f + 8 * q >= p.h_out) break;
-          float b[8], o[8];
-          if (p.bias != nullptr) {
-            unpack8_bf16(__ldg(reinterpret_cast<const uint4*>(p.bias + f + 8 * q)), b);
+          for (int q = 0; q < 4; ++q) {
+            if (q >= nq) break;
+            float b[8];
+            unpack8_bf16(__ldg(reinterpret_cast<const uint4*>(p.bias + f) + q), b);
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[8 * q + j] += b[j];
-          }
-          if (p.gated) {
-            if (p.bias != nullptr) {
-              unpack8_bf16(__ldg(reinterpret_cast<const uint4*>(p.bias + p.h_out + f + 8 * q)), b);
+            if (p.gated) {
+              unpack8_bf16(__ldg(reinterpret_cast<const uint4*>(p.bias + p.h_out + f) + q), b);
 #pragma unroll
               for (int j = 0; j < 8; ++j) u[8 * q + j] += b[j];
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = silu(h[8 * q + j]) * u[8 * q + j];
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = act_apply(p.act, h[8 * q + j]);
           }
-          if (p.residual != nullptr) {
-            unpack8_bf16(*reinterpret_cast<const uint4*>(p.residual + at + 8 * q), b);
+        }
+        if (p.gated) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] += b[j];
+          for (int j = 0; j < 32; ++j) h[j] = sigmoid_of<true>(h[j], h[j]) * u[j];
+        } else {
+          act_apply<true>(p.act, h);
+        }
+        if (p.residual != nullptr) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (q >= nq) break;
+            float b[8];
+            unpack8_bf16(*(reinterpret_cast<const uint4*>(p.residual + at) + q), b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[8 * q + j] += b[j];
           }
-          *reinterpret_cast<uint4*>(p.y + at + 8 * q) = make_uint4(pack2_bf16(o[0], o[1]), pack2_bf16(o[2], o[3]),
-                                                                   pack2_bf16(o[4], o[5]), pack2_bf16(o[6], o[7]));
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (q >= nq) break;
+          reinterpret_cast<uint4*>(p.y + at)[q] =
+              make_uint4(pack2_bf16(h[8 * q], h[8 * q + 1]), pack2_bf16(h[8 * q + 2], h[8 * q + 3]),
+                         pack2_bf16(h[8 * q + 4], h[8 * q + 5]), pack2_bf16(h[8 * q + 6], h[8 * q + 7]));
         }
       }
     }
@@ -315,12 +325,16 @@ __global__ void __launch_bounds__(kFpThreads, 1)
     uint32_t used = 0;  // parity of each stage's uses by the z warps
     bool ok = true;
     pdl_wait();
+    ZTile<kFpZThreads, 128 * 8 / kFpZThreads> zt;
     for (int t = pair; ok && t < total; t += pairs) {
       int tt, ft;
       fp_tile(p, t, tt, ft);
       sc += nk;
       AdapterGroups g(adapter_mask(tt), p.r);
+      const int t0 = tt * 256 + static_cast<int>(rank) * 128;
+      if (g.rem != 0) zt.rows(p.row_adapter, t0, p.T, i);
       while (ok && g.next()) {
+        zt.load(g, p.z, t0, p.r, i);
         const int stage = static_cast<int>(sc % kFpStages);
         ok = mbar_wait(&sm.zgo[stage], used >> stage & 1u, abort_flag, p.status, kFtWaitNs, 67);
         used ^= 1u << stage;
@@ -328,8 +342,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
           ok = false;
           break;
         }
-        write_z_tile(ring + stage * kFpStageBytes, g, p.z, p.row_adapter, tt * 256 + static_cast<int>(rank) * 128, 128,
-                     p.T, p.r, i, kFpZThreads);
+        zt.store(ring + stage * kFpStageBytes, i);
         fence_proxy_async_smem();
         named_bar_sync(1, kFpZThreads);
         if (i == 0) mbar_arrive_cluster(leader(&sm.zfull[stage]));

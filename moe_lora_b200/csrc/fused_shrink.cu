@@ -7,10 +7,10 @@
 // up 128 / C tokens' partials in rank order from its peers' shared memory (no atomics: the
 // same bits every time).
 //
-// The launch's other clusters read the B rows of the adapters in use and record which hold
-// a value that is not finite: the projection keeps those out of its matrix product, where a
-// zero times an infinity would reach other tenants' tokens.  The rows read stay in L2, where
-// the projection finds them.
+// A launch ahead reads the B rows of the adapters in use and records which hold a value that
+// is not finite: the projection keeps those out of its matrix product, where a zero times an
+// infinity would reach other tenants' tokens.  The rows read stay in L2, where the projection
+// finds them.
 #include "fused_tc.cuh"
 #include "prof.h"
 
@@ -33,9 +33,10 @@ struct ShParams {
   __nv_bfloat16* z;
   int32_t* row_adapter;
   uint64_t* tile_mask;
-  unsigned long long* bad;
+  uint64_t* bad;
+  uint64_t* bad_part;
   int* status;
-  int C, P, main_ctas, scan_ctas;
+  int C, P, scan_ctas;
 };
 
 struct ShCore {
@@ -46,12 +47,58 @@ struct ShCore {
   int row_ad[128];
 };
 
-// adapters used by any segment that holds a token
-__device__ __forceinline__ void used_adapters(const ShParams& p, unsigned* mask, int tid, int n) {
-  for (int s = tid; s < p.S; s += n) {
-    const int a = p.seg_adapter[s];
-    if (a >= 0 && a < p.L && p.seg_offsets[s + 1] > p.seg_offsets[s]) atomicOr(&mask[a >> 5], 1u << (a & 31));
+// The adapters in use and whether their B rows are finite; the segments checked on the way.
+// First kernel of the call: it clears the status word (one thread writes it, whatever the
+// checks say) and lets the shrink kernel start at once.  Each CTA leaves the adapters that
+// it found broken in a word of its own, so that no counter has to be cleared.
+constexpr int kScanThreads = 256;
+
+__global__ void __launch_bounds__(kScanThreads) fused_scan_kernel(const ShParams p) {
+  __shared__ unsigned s_mask[2], s_bad[2];
+  __shared__ int s_wrong, s_ids[64];
+  const int tid = threadIdx.x;
+  pdl_trigger();
+  if (tid < 2) s_mask[tid] = s_bad[tid] = 0u;
+  if (tid == 0) s_wrong = 0x7fffffff;
+  __syncthreads();
+  for (int s = tid; s < p.S; s += kScanThreads) {
+    const int a = p.seg_adapter[s], lo = p.seg_offsets[s], hi = p.seg_offsets[s + 1];
+    if (a >= 0 && a < p.L && hi > lo) atomicOr(&s_mask[a >> 5], 1u << (a & 31));
+    if (blockIdx.x == 0 && (lo > hi || lo < 0 || hi > p.T || a < -1 || a >= p.L)) atomicMin(&s_wrong, s);
   }
+  __syncthreads();
+  const uint64_t mask = s_mask[0] | (static_cast<uint64_t>(s_mask[1]) << 32);
+  const int cnt = __popcll(mask);
+  if (tid < 64 && (mask >> tid & 1ull)) s_ids[__popcll(mask & ((1ull << tid) - 1ull))] = tid;
+  if (blockIdx.x == 0 && tid == 0) {
+    p.status[0] = s_wrong != 0x7fffffff ? MOE_LORA_ERR_DEVICE_CHECK : MOE_LORA_OK;
+    p.status[1] = s_wrong != 0x7fffffff ? s_wrong : 0;
+  }
+  __syncthreads();
+  const size_t chunks = static_cast<size_t>(p.r) * p.n / 8;  // 16 bytes each
+  const size_t step = static_cast<size_t>(gridDim.x) * kScanThreads;
+  const uint4* b = reinterpret_cast<const uint4*>(p.lora_b);
+  for (size_t i = static_cast<size_t>(blockIdx.x) * kScanThreads + tid; i < chunks; i += step) {
+    for (int q = 0; q < cnt; q += 8) {  // eight adapters' loads in flight
+      uint4 v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __ldg(b + s_ids[min(q + e, cnt - 1)] * chunks + i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+        bool hit = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // exponent bits all ones in either half
+          hit |= (w[j] & 0x7F80u) == 0x7F80u || (w[j] & 0x7F800000u) == 0x7F800000u;
+        if (hit) {
+          const int a = s_ids[min(q + e, cnt - 1)];
+          atomicOr(&s_bad[a >> 5], 1u << (a & 31));
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) p.bad_part[blockIdx.x] = s_bad[0] | (static_cast<uint64_t>(s_bad[1]) << 32);
 }
 
 __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_constant__ CUtensorMap tmx,
@@ -63,34 +110,6 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
   __shared__ ShCore sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();  // the projection streams its weights meanwhile
-
-  if (static_cast<int>(blockIdx.x) >= p.main_ctas) {
-    // ------------------------------------------------------------ B rows that are not finite
-    if (tid < 2) sm.mask[tid] = 0u;
-    __syncthreads();
-    used_adapters(p, sm.mask, tid, kShThreads);
-    __syncthreads();
-    uint64_t rem = sm.mask[0] | (static_cast<uint64_t>(sm.mask[1]) << 32);
-    const long long chunks = static_cast<long long>(p.r) * p.n / 8;  // 16 bytes each
-    const long long step = static_cast<long long>(p.scan_ctas) * kShThreads;
-    const long long first = static_cast<long long>(blockIdx.x - p.main_ctas) * kShThreads + tid;
-    while (rem != 0) {
-      const int a = __ffsll(static_cast<long long>(rem)) - 1;
-      rem &= rem - 1;
-      const uint4* b = reinterpret_cast<const uint4*>(p.lora_b) + static_cast<size_t>(a) * chunks;
-      bool hit = false;
-#pragma unroll 4
-      for (long long i = first; i < chunks; i += step) {
-        const uint4 v = __ldg(b + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)  // exponent bits all ones in either half
-          hit |= (w[j] & 0x7F80u) == 0x7F80u || (w[j] & 0x7F800000u) == 0x7F800000u;
-      }
-      if (hit) atomicOr(p.bad, 1ull << a);
-    }
-    return;
-  }
 
   const int rank = static_cast<int>(blockIdx.x) % p.C;
   const int group = static_cast<int>(blockIdx.x) / p.C;  // cluster index
@@ -128,11 +147,6 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
     sm.row_ad[tid] = a;
     if (a >= 0) atomicOr(&sm.mask[a >> 5], 1u << (a & 31));
   }
-  if (group == 0 && rank == 0)  // segments that run backwards or leave [0, T], unknown adapters
-    for (int s = tid; s < p.S; s += kShThreads)
-      if (p.seg_offsets[s] > p.seg_offsets[s + 1] || p.seg_offsets[s] < 0 || p.seg_offsets[s + 1] > p.T ||
-          p.seg_adapter[s] < -1 || p.seg_adapter[s] >= p.L)
-        set_status(p.status, MOE_LORA_ERR_DEVICE_CHECK, s);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -262,6 +276,14 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
         volatile int dummy = 0;
         mbar_wait(&sm.full[s], (parity_of >> s) & 1u, &dummy, nullptr, kFtWaitNs / 4, 0);
       }
+  if (blockIdx.x == 0 && warp == 2) {  // what the scan found; this launch ends behind it
+    pdl_wait();
+    uint64_t b = 0ull;
+    for (int i = lane; i < p.scan_ctas; i += 32) b |= *reinterpret_cast<const volatile uint64_t*>(p.bad_part + i);
+    const unsigned lo = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(b));
+    const unsigned hi = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(b >> 32));
+    if (lane == 0) *p.bad = lo | (static_cast<uint64_t>(hi) << 32);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -290,7 +312,8 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, cudaStream_t st) {
   p.z = f.z;
   p.row_adapter = a.row_adapter;
   p.tile_mask = f.tile_mask;
-  p.bad = reinterpret_cast<unsigned long long*>(f.bad);
+  p.bad = f.bad;
+  p.bad_part = f.bad_part;
   p.status = a.status;
   // K splits: as many as keep one wave of CTAs (one per SM: 128 KB of ring each)
   const int tiles = (a.T + 127) / 128;
@@ -299,8 +322,7 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, cudaStream_t st) {
   // chunks of a tile side by side while SMs are left
   const int apc = kShN / a.r, most = (std::min(std::min(a.L, a.S), 128) + apc - 1) / apc;
   p.P = std::max(1, std::min(most, a.num_sms / (tiles * p.C)));
-  p.main_ctas = tiles * p.P * p.C;
-  p.scan_ctas = std::max(8, a.num_sms / 2 / p.C * p.C);
+  p.scan_ctas = std::min(kFusedScanMax, kScanCtasPerSm * a.num_sms);
   const size_t smem = 1024 + kShStages * kShStageBytes + 128u * (a.r + 4) * 4;
   static std::atomic<bool> attr_set[kMaxDevices];
   const int dev = current_device_index();
@@ -312,18 +334,22 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, cudaStream_t st) {
     attr_set[dev].store(true, std::memory_order_release);
   }
   ProfScope ps(K_FUSED_SHRINK, st);
+  fused_scan_kernel<<<p.scan_ctas, kScanThreads, 0, st>>>(p);
+  count_launch();
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.main_ctas + p.scan_ctas);
+  cfg.gridDim = dim3(tiles * p.P * p.C);
   cfg.blockDim = dim3(kShThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = p.C;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, fused_shrink_kernel, tmx, tma, p);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();

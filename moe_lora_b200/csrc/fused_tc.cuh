@@ -9,16 +9,36 @@ namespace mlb {
 
 constexpr uint64_t kFtWaitNs = 2000000000ull;  // limit of every bounded wait: 2 s
 
-__device__ __forceinline__ float act_apply(int act, float v) {
+// Activations behind a projection.  Fp32 outputs take expf, erff and IEEE divisions.  Bf16
+// outputs (FAST) are rounded to 2^-8 behind them, so the sigmoid forms use the hardware
+// exponential and reciprocal, off by a few 2^-22 of the result.
+template <bool FAST>
+__device__ __forceinline__ float sigmoid_of(float x, float v) {  // v / (1 + exp(-x))
+  if constexpr (FAST) return __fdividef(v, 1.f + __expf(-x));
+  return v / (1.f + expf(-x));
+}
+
+template <bool FAST, int N>
+__device__ __forceinline__ void act_apply(int act, float (&h)[N]) {
   switch (act) {
-    case ML_ACT_RELU: return v > 0.f ? v : (v != v ? v : 0.f);
-    case ML_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    case ML_ACT_GELU_TANH: {
-      const float u = 0.79788456080286536f * (v + 0.044715f * v * v * v);
-      return 0.5f * v * (1.f + tanhf(u));
-    }
-    case ML_ACT_SILU: return silu(v);
-    default: return v;
+    case ML_ACT_RELU:
+#pragma unroll
+      for (int j = 0; j < N; ++j) h[j] = h[j] > 0.f ? h[j] : (h[j] != h[j] ? h[j] : 0.f);
+      break;
+    case ML_ACT_GELU:
+#pragma unroll
+      for (int j = 0; j < N; ++j) h[j] = 0.5f * h[j] * (1.f + erff(h[j] * 0.70710678118654752f));
+      break;
+    case ML_ACT_GELU_TANH:  // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        h[j] = sigmoid_of<FAST>(1.5957691216057308f * (h[j] + 0.044715f * h[j] * h[j] * h[j]), h[j]);
+      break;
+    case ML_ACT_SILU:
+#pragma unroll
+      for (int j = 0; j < N; ++j) h[j] = sigmoid_of<FAST>(h[j], h[j]);
+      break;
+    default: break;
   }
 }
 
@@ -115,28 +135,41 @@ struct AdapterGroups {
   int k0 = 0;  // first rank row of the group's adapter (r = 128)
 };
 
-// z rows [t0, t0 + rows) as the group's K-major tile (128-byte swizzle): row of 64 K columns,
-// 16-byte chunk c at c ^ (row & 7).  Thread i of n.
-__device__ __forceinline__ void write_z_tile(uint8_t* dst, const AdapterGroups& g, const __nv_bfloat16* z,
-                                             const int32_t* row_adapter, int t0, int rows, int T, int r, int i, int n) {
-  const int per = r >= 64 ? 64 : r;
-  for (int e = i; e < rows * 8; e += n) {
-    const int row = e >> 3, c = e & 7;
-    const int t = t0 + row;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (t < T) {
-      const int ad = row_adapter[t];
-      const int q = (8 * c) / per;
-      int want = -2;
+// z rows [t0, t0 + N NT / 8) as a group's K-major tile (128-byte swizzle): a row
+// holds 64 K columns, its 16-byte chunk c at c ^ (row & 7).  Thread i of NT takes chunk i & 7
+// of rows i / 8 + j NT / 8, j < N: the rows' adapters once per tile, the z values ahead of
+// the stage that takes them, so that only the shared-memory stores wait for it.
+template <int NT, int N>
+struct ZTile {
+  int ad[N];
+  uint4 v[N];
+  __device__ __forceinline__ void rows(const int32_t* row_adapter, int t0, int T, int i) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j == q) want = g.ids[j];
-      if (ad >= 0 && ad == want)
-        v = *reinterpret_cast<const uint4*>(z + static_cast<size_t>(t) * r + g.k0 + (8 * c) % per);
+    for (int j = 0; j < N; ++j) {
+      const int t = t0 + (i >> 3) + j * (NT / 8);
+      ad[j] = t < T ? row_adapter[t] : -1;
     }
-    *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = v;
   }
-}
+  __device__ __forceinline__ void load(const AdapterGroups& g, const __nv_bfloat16* z, int t0, int r, int i) {
+    const int per = r >= 64 ? 64 : r, k = 8 * (i & 7), q = k / per;
+    int want = -2;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e == q) want = g.ids[e];
+    const __nv_bfloat16* zp = z + static_cast<size_t>(t0 + (i >> 3)) * r + g.k0 + k - q * per;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      v[j] = (ad[j] >= 0 && ad[j] == want) ? *reinterpret_cast<const uint4*>(zp + static_cast<size_t>(j) * (NT / 8) * r)
+                                           : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void store(uint8_t* dst, int i) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int row = (i >> 3) + j * (NT / 8);
+      *reinterpret_cast<uint4*>(dst + row * 128 + (((i & 7) ^ (row & 7)) << 4)) = v[j];
+    }
+  }
+};
 
 // Host side: launches of the tensor-core projection.
 struct FusedTcArgs {
@@ -144,7 +177,9 @@ struct FusedTcArgs {
   __nv_bfloat16* z;        // [T][r]
   uint64_t* tile_mask;     // adapters of each 128-token tile
   uint64_t* bad;           // adapters whose B holds a value that is not finite
+  uint64_t* bad_part;      // ... found by each CTA of the scan
 };
+constexpr int kScanCtasPerSm = 2;
 cudaError_t launch_fused_shrink_tc(const FusedTcArgs& p, cudaStream_t st);
 cudaError_t launch_fused_decode_tc(const FusedTcArgs& p, cudaStream_t st);
 cudaError_t launch_fused_prefill_tc(const FusedTcArgs& p, cudaStream_t st);

@@ -225,10 +225,12 @@ struct DenseFusedArgs {
   bool f32;
   float* z;                   // workspace [T][r]: scale (x A), fp32 (bf16 projections: bf16)
   int32_t* row_adapter;       // workspace [T]
-  uint64_t* tile_mask;        // workspace: adapters of each 128-token tile (bf16)
+  uint64_t* tile_mask;        // workspace (bf16): adapters of each 128-token tile
+  uint64_t* bad_part;         // workspace (bf16): kFusedScanMax words
   int* status;
   int num_sms;
 };
+constexpr int kFusedScanMax = 512;  // CTAs of the adapters' scan at most
 cudaError_t launch_dense_fused(const DenseFusedArgs& a, cudaStream_t st);
 
 // Tensor-core grouped GEMM with operand swap: the weight rows fill the 128-row MMA
