@@ -137,6 +137,8 @@ static cudaError_t launch_simt(const DenseFusedArgs& a, cudaStream_t st) {
 // Token counts up to here take the weight-streaming kernel (all tokens in the MMA's N), more
 // the tiled one.
 constexpr int kDecodeTokens = 256;
+// ... and up to here the adapters' shrink runs on CUDA cores
+constexpr int kSmallTokens = 64;
 
 cudaError_t launch_dense_fused(const DenseFusedArgs& a, cudaStream_t st) {
   if (a.T <= 0) return cudaSuccess;
@@ -148,7 +150,8 @@ cudaError_t launch_dense_fused(const DenseFusedArgs& a, cudaStream_t st) {
     f.bad = reinterpret_cast<uint64_t*>(a.status + 32);  // in the status block
     f.bad_part = a.bad_part;
     if (a.r > 0) {
-      const cudaError_t e = launch_fused_shrink_tc(f, st);
+      const cudaError_t e = a.T <= kSmallTokens ? launch_fused_shrink_simt(f, st)
+                                                : launch_fused_shrink_tc(f, a.T > kDecodeTokens, st);
       if (e != cudaSuccess) return e;
     }
     return a.T <= kDecodeTokens ? launch_fused_decode_tc(f, st) : launch_fused_prefill_tc(f, st);

@@ -31,18 +31,21 @@ struct FdParams {
   __nv_bfloat16* y;
   const __nv_bfloat16* z;
   const __nv_bfloat16* lora_b;
-  const int32_t* row_adapter;
-  const uint64_t* tile_mask;
-  const uint64_t* bad;
+  const int32_t* seg_offsets;
+  const int32_t* seg_adapter;
   int* status;
-  int T, K, h_out, n, r, act, gated, C, stages;
+  int S, T, K, h_out, n, r, L, act, gated, C;
   int clear_status;  // no shrink kernel ahead: this kernel's first thread clears the status
 };
 
 struct FdCore {
-  uint64_t full[kFdMaxStages], empty[kFdMaxStages], zgo[kFdMaxStages], zfull[kFdMaxStages], tfull;
+  uint64_t full[kFdMaxStages], empty[kFdMaxStages], zgo[kFdMaxStages], zfull[kFdMaxStages], tfull, rows;
   uint32_t tmem_base;
   int abort_flag;
+  alignas(8) unsigned mask[2];    // adapters of the tokens
+  // ... whose B rows of this tile hold a value that is not finite ([2, 4): rank rows 64 to 127)
+  alignas(8) unsigned broken[4];
+  int row_ad[256];
 };
 
 template <int BN>
@@ -84,7 +87,10 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
       mbar_init(&sm.zfull[s], 128);
     }
     mbar_init(&sm.tfull, 1);
+    mbar_init(&sm.rows, 128);
     sm.abort_flag = 0;
+    sm.mask[0] = sm.mask[1] = 0u;
+    sm.broken[0] = sm.broken[1] = sm.broken[2] = sm.broken[3] = 0u;
     fence_mbarrier_init();
     tma_prefetch_desc(&tmw);
     tma_prefetch_desc(&tmx);
@@ -96,14 +102,14 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
-  // the adapters of the (at most two 128-token) tiles, known once the shrink kernel is done
+  // the tokens' adapters, looked up by the epilogue warps while the stream starts
   auto adapter_mask = [&]() -> uint64_t {
-    if (p.r == 0) return 0ull;
-    pdl_wait();
-    uint64_t m = *reinterpret_cast<const volatile uint64_t*>(p.tile_mask);
-    if (p.T > 128) m |= *reinterpret_cast<const volatile uint64_t*>(p.tile_mask + 1);
-    return m & ~*reinterpret_cast<const volatile uint64_t*>(p.bad);
+    if (p.r == 0 || !mbar_wait(&sm.rows, 0, abort_flag, p.status, kFtWaitNs, 57)) return 0ull;
+    return sm.mask[0] | (static_cast<uint64_t>(sm.mask[1]) << 32);
   };
+  // the adapters' K columns come after three quarters of the CTA's K blocks: late enough for
+  // the shrink kernel to be done, early enough to hide behind the rest of the stream
+  const int kbz = kb0 + (kb1 - kb0) * 3 / 4;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
           phase ^= 1u;
         }
       };
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = kb0; ok && kb < kb1; ++kb) {
         ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 50);
         if (!ok) break;
         uint8_t* s = ring + stage * Cfg::kStageBytes;
@@ -127,26 +133,25 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
         tma_load_2d(s + 64 * 128, &tmw, &sm.full[stage], kb * 64, row1);
         tma_load_2d(s + 128 * 128, &tmx, &sm.full[stage], kb * 64, 0);
         advance();
-      }
-      AdapterGroups g(ok ? adapter_mask() : 0ull, p.r);
-      for (int gi = 0; ok && g.next(); ++gi) {
-        if (gi % p.C != rank) continue;
-        ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 51);
-        if (!ok) break;
-        mbar_arrive(&sm.zgo[stage]);  // the z tile may be written
-        uint8_t* s = ring + stage * Cfg::kStageBytes;
-        const int rb = p.r < 64 ? p.r : 64;
-        // an odd adapter of rank 8 fills half an MMA step: its rows once more meet zeros of z
-        const int boxes = (p.r == 8 && (g.na & 1)) ? g.na + 1 : g.na;
-        mbar_arrive_expect_tx(&sm.full[stage], static_cast<uint32_t>(2 * boxes * rb) * 128u);
+        if (kb != kbz) continue;
+        AdapterGroups g(adapter_mask(), p.r);
+        for (int gi = 0; ok && g.next(); ++gi) {
+          if (gi % p.C != rank) continue;
+          ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 51);
+          if (!ok) break;
+          mbar_arrive(&sm.zgo[stage]);  // the z tile may be written
+          uint8_t* zs = ring + stage * Cfg::kStageBytes;
+          const int rb = p.r < 64 ? p.r : 64, boxes = g.boxes();
+          mbar_arrive_expect_tx(&sm.full[stage], static_cast<uint32_t>(2 * boxes * rb) * 128u);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          if (q >= boxes) break;
-          const int id = (q > 0 && q >= g.na) ? g.ids[q > 0 ? q - 1 : 0] : g.ids[q];
-          tma_load_2d(s + q * rb * 128, &tmb, &sm.full[stage], f0, id * p.r + g.k0);
-          tma_load_2d(s + 64 * 128 + q * rb * 128, &tmb, &sm.full[stage], row1, id * p.r + g.k0);
+          for (int q = 0; q < 8; ++q) {
+            if (q >= boxes) break;
+            const int id = (q > 0 && q >= g.na) ? g.ids[q > 0 ? q - 1 : 0] : g.ids[q];
+            tma_load_2d(zs + q * rb * 128, &tmb, &sm.full[stage], f0, id * p.r + g.k0);
+            tma_load_2d(zs + 64 * 128 + q * rb * 128, &tmb, &sm.full[stage], row1, id * p.r + g.k0);
+          }
+          advance();
         }
-        advance();
       }
       if (*abort_flag)  // let our own copies land before the ring is reused
         for (int s = 0; s < S; ++s)
@@ -158,9 +163,9 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      int stage = 0, zi = 0;
-      uint32_t phase = 0;
-      bool ok = true, any = false;
+      int stage = 0;
+      uint32_t phase = 0, zi = 0;
+      bool ok = true;
       const int n_mma = min(BN, (p.T + 15) & ~15);
       const uint32_t idesc = umma_idesc_bf16(128, n_mma);
       auto advance = [&]() {
@@ -170,37 +175,32 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
           phase ^= 1u;
         }
       };
-      for (int kb = kb0; kb < kb1; ++kb) {
+      const uint32_t zdesc = umma_idesc_bf16_amn(128, n_mma);
+      for (int kb = kb0; ok && kb < kb1; ++kb) {
         ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 52);
         if (!ok) break;
         tc_fence_after();
         const uint32_t s = smem_u32(ring + stage * Cfg::kStageBytes);
         const uint64_t ad = umma_desc_sw128(s), bd = umma_desc_sw128(s + 128 * 128);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          umma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, any ? 1u : 0u);
-          any = true;
-        }
+        for (int k = 0; k < 4; ++k) umma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
         advance();
-      }
-      // adapters: A = B_a^T, MN-major (64-feature blocks 8 KB apart), 16 rank rows per step
-      const uint32_t zdesc = umma_idesc_bf16_amn(128, n_mma);
-      AdapterGroups g(ok ? adapter_mask() : 0ull, p.r);
-      for (int gi = 0; ok && g.next(); ++gi) {
-        if (gi % p.C != rank) continue;
-        ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 53) &&
-             mbar_wait(&sm.zfull[stage], static_cast<uint32_t>(zi / S) & 1u, abort_flag, p.status, kFtWaitNs, 54);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t s = smem_u32(ring + stage * Cfg::kStageBytes);
-        const uint64_t ad = umma_desc_mn_sw128(s, 64 * 128), bd = umma_desc_sw128(s + 128 * 128);
-        const int steps = p.r > 64 ? 4 : (g.na * p.r + 15) / 16;
-        for (int k = 0; k < steps; ++k) {
-          umma_bf16(tmem, ad + 128 * k, bd + 2 * k, zdesc, any ? 1u : 0u);
-          any = true;
+        if (kb != kbz) continue;
+        // adapters: A = B_a^T, MN-major (64-feature blocks 8 KB apart), 16 rank rows per step
+        AdapterGroups g(adapter_mask(), p.r);
+        for (int gi = 0; ok && g.next(); ++gi) {
+          if (gi % p.C != rank) continue;
+          ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 53) &&
+               mbar_wait(&sm.zfull[stage], static_cast<uint32_t>(zi >> stage) & 1u, abort_flag, p.status, kFtWaitNs, 54);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t zs = smem_u32(ring + stage * Cfg::kStageBytes);
+          const uint64_t zad = umma_desc_mn_sw128(zs, 64 * 128), zbd = umma_desc_sw128(zs + 128 * 128);
+          const int steps = g.steps();
+          for (int k = 0; k < steps; ++k) umma_bf16(tmem, zad + 128 * k, zbd + 2 * k, zdesc, 1u);
+          zi ^= 1u << stage;  // parity of the stage's uses for adapters
+          advance();
         }
-        ++zi;
-        advance();
       }
       umma_commit(&sm.tfull);
       volatile int dummy = 0;
@@ -208,26 +208,77 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
     }
     __syncwarp();
   } else {
-    // z tiles of this CTA's adapter groups, then the accumulator -> partial sums
+    // the tokens' adapters, z tiles of this CTA's groups, then the accumulator -> partial sums
     const int e = tid - 64;
-    bool any = kb1 > kb0;
     if (p.r) {
-      int stage = (kb1 - kb0) % S, zi = 0;
+      for (int t = e; t < BN; t += 128) {
+        int a = -1;
+        if (t < p.T) {
+          const int s = segment_of(p.seg_offsets, p.S, t);
+          if (s >= 0) a = p.seg_adapter[s];
+          if (a < 0 || a >= p.L) a = -1;
+          if (a >= 0) atomicOr(&sm.mask[a >> 5], 1u << (a & 31));
+        }
+        sm.row_ad[t] = a;
+      }
+      mbar_arrive(&sm.rows);
+      // the stage and lap that follow the K blocks up to kbz
+      int stage = (kbz + 1 - kb0) % S;
+      uint32_t lap = static_cast<uint32_t>((kbz + 1 - kb0) / S) & 1u, zi = 0;
       AdapterGroups g(adapter_mask(), p.r);
       ZTile<128, BN / 16> zt;
-      if (g.rem != 0) zt.rows(p.row_adapter, 0, p.T, e);
-      bool ok = true;
+      zt.rows(sm.row_ad, 0, BN, e);
+      bool ok = true, waited = false;
       for (int gi = 0; ok && g.next(); ++gi) {
         if (gi % p.C != rank) continue;
-        any = true;
+        if (!waited) pdl_wait();  // z comes from the shrink kernel
+        waited = true;
         zt.load(g, p.z, 0, p.r, e);
-        ok = mbar_wait(&sm.zgo[stage], static_cast<uint32_t>(zi / S) & 1u, abort_flag, p.status, kFtWaitNs, 55);
-        if (!ok) break;
-        zt.store(ring + stage * Cfg::kStageBytes + 128 * 128, e);
+        // (after zgo the barrier `full` is in this lap's phase)
+        ok = mbar_wait(&sm.zgo[stage], zi >> stage & 1u, abort_flag, p.status, kFtWaitNs, 55) &&
+             mbar_wait(&sm.full[stage], lap, abort_flag, p.status, kFtWaitNs, 58);
+        if (!named_bar_and(1, 128, ok)) {
+          ok = false;
+          break;
+        }
+        zi ^= 1u << stage;
+        uint8_t* zs = ring + stage * Cfg::kStageBytes;
+        zt.store(zs + 128 * 128, e);
+        // B rows that are not finite would reach every token through its zeros: their adapter
+        // leaves the product, the final rows add it for its own tokens alone
+        const int per = p.r < 64 ? p.r : 64, used = g.boxes() * per * 8;  // 16-byte chunks of a block
+        unsigned* broken = sm.broken + (g.k0 != 0 ? 2 : 0);
+        uint32_t hit = 0u;  // adapters of the group
+        for (int c = e; c < used; c += 128) {
+          const uint4* b = reinterpret_cast<const uint4*>(zs) + c;
+          if (not_finite8(b[0]) || not_finite8(b[512])) hit |= 1u << min(c / 8 / per, g.na - 1);
+        }
+        hit = __reduce_or_sync(0xffffffffu, hit);
+        if (!named_bar_and(1, 128, hit == 0u)) {
+          if (hit != 0u && lane == 0) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (hit >> q & 1u) atomicOr(&broken[g.ids[q] >> 5], 1u << (g.ids[q] & 31));
+          }
+          named_bar_sync(1, 128);
+          for (int c = e; c < used; c += 128) {
+            const int q = min(c / 8 / per, g.na - 1);
+            int id = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j == q) id = g.ids[j];
+            if (broken[id >> 5] >> (id & 31) & 1u) {
+              uint4* b = reinterpret_cast<uint4*>(zs) + c;
+              b[0] = b[512] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+        }
         fence_proxy_async_smem();
         mbar_arrive(&sm.zfull[stage]);
-        ++zi;
-        if (++stage == S) stage = 0;
+        if (++stage == S) {
+          stage = 0;
+          lap ^= 1u;
+        }
       }
     }
     bool got = mbar_wait(&sm.tfull, 0, abort_flag, p.status, kFtWaitNs, 56);
@@ -240,7 +291,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
         tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(g4 * 32) << 16) + c0, v);
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          if (c0 + j < BN) part[(c0 + j) * kFdPitch + m] = any ? v[j] : 0.f;
+          if (c0 + j < BN) part[(c0 + j) * kFdPitch + m] = v[j];
       }
       tc_fence_before();
     }
@@ -250,7 +301,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
 
   // tokens rank, rank + C, ...: a warp per token, 4 features per lane (gated: lanes 0-15 the
   // gate's 64 features, lanes 16-31 the up projection's)
-  if (p.r) pdl_wait();  // z and the adapter ids, where a broken adapter needs them
+  if (p.r) pdl_wait();  // the call ends behind the shrink kernel, whatever the tokens need of it
   if (!*abort_flag) {
     const int col = p.gated ? ((lane < 16 ? 0 : p.h_out) + f0 + 4 * (lane & 15)) : f0 + 4 * lane;  // row of W
     const int feat = p.gated ? f0 + 4 * (lane & 15) : col;
@@ -263,7 +314,13 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
       b[2] = __uint_as_float(v.y << 16);
       b[3] = __uint_as_float(v.y & 0xFFFF0000u);
     }
-    const uint64_t bad = p.r ? *reinterpret_cast<const volatile uint64_t*>(p.bad) : 0ull;
+    // the tile's broken adapters, whichever CTA met them (rank rows below 64, and from there)
+    uint64_t bad = 0ull, bad_up = 0ull;
+    if (p.r)
+      for (int c = 0; c < p.C; ++c) {
+        bad |= ld_cluster_u64(mapa_shared(smem_u32(sm.broken), static_cast<uint32_t>(c)));
+        bad_up |= ld_cluster_u64(mapa_shared(smem_u32(sm.broken + 2), static_cast<uint32_t>(c)));
+      }
     for (int t = rank + p.C * warp; t < p.T; t += p.C * (kFdThreads / 32)) {
       const bool writer = in && (!p.gated || lane < 16);
       uint2 res = make_uint2(0u, 0u);
@@ -278,10 +335,11 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
         h[2] += v.z;
         h[3] += v.w;
       }
-      if (bad != 0) {  // an adapter with values that are not finite: its own tokens only
-        const int ad = p.row_adapter[t];
-        if (ad >= 0 && (bad >> ad & 1ull) && in)
-          for (int i = 0; i < p.r; ++i) {
+      if ((bad | bad_up) != 0) {  // an adapter with values that are not finite: its own tokens only
+        const int ad = sm.row_ad[t];
+        const bool lo = ad >= 0 && (bad >> ad & 1ull), up = ad >= 0 && (bad_up >> ad & 1ull);
+        if ((lo || up) && in)  // the rank rows that left the product
+          for (int i = lo ? 0 : 64; i < (up ? p.r : min(p.r, 64)); ++i) {
             const float zi = __bfloat162float(p.z[static_cast<size_t>(t) * p.r + i]);
             const __nv_bfloat16* br = p.lora_b + (static_cast<size_t>(ad) * p.r + i) * p.n + col;
 #pragma unroll
@@ -329,9 +387,10 @@ static cudaError_t launch_bn(const FusedTcArgs& f, cudaStream_t st) {
   p.y = static_cast<__nv_bfloat16*>(a.y);
   p.z = f.z;
   p.lora_b = static_cast<const __nv_bfloat16*>(a.lora_b);
-  p.row_adapter = a.row_adapter;
-  p.tile_mask = f.tile_mask;
-  p.bad = f.bad;
+  p.seg_offsets = a.seg_offsets;
+  p.seg_adapter = a.seg_adapter;
+  p.S = a.S;
+  p.L = a.L;
   p.status = a.status;
   p.T = a.T;
   p.K = a.h_in;

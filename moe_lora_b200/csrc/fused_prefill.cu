@@ -143,8 +143,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
           uint8_t* s = ring + stage * kFpStageBytes + 128 * 128;
           const uint32_t fb = leader(&sm.full[stage]);
           const int rb = p.r < 64 ? p.r : 64;
-          // an odd adapter of rank 8 fills half an MMA step: its rows once more meet zeros of z
-          const int boxes = (p.r == 8 && (g.na & 1)) ? g.na + 1 : g.na;
+          const int boxes = g.boxes();
           if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], static_cast<uint32_t>(4 * boxes * rb) * 128u);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
@@ -216,7 +215,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
             tc_fence_after();
             const uint32_t s = smem_u32(ring + stage * kFpStageBytes);
             const uint64_t ad = umma_desc_sw128(s), bd = umma_desc_mn_sw128(s + 128 * 128, 64 * 128);
-            const int steps = p.r > 64 ? 4 : (g.na * p.r + 15) / 16;
+            const int steps = g.steps();
             for (int k = 0; k < steps; ++k) umma_bf16_pair(d, ad + 2 * k, bd + 128 * k, zidesc, 1u);
             advance();
           }

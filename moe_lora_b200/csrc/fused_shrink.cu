@@ -37,6 +37,7 @@ struct ShParams {
   uint64_t* bad_part;
   int* status;
   int C, P, scan_ctas;
+  int validate;  // no scan ahead: the first CTA checks the segments and clears the status
 };
 
 struct ShCore {
@@ -44,6 +45,7 @@ struct ShCore {
   uint32_t tmem_base;
   int abort_flag;
   unsigned mask[2];
+  int wrong;
   int row_ad[128];
 };
 
@@ -64,7 +66,7 @@ __global__ void __launch_bounds__(kScanThreads) fused_scan_kernel(const ShParams
   for (int s = tid; s < p.S; s += kScanThreads) {
     const int a = p.seg_adapter[s], lo = p.seg_offsets[s], hi = p.seg_offsets[s + 1];
     if (a >= 0 && a < p.L && hi > lo) atomicOr(&s_mask[a >> 5], 1u << (a & 31));
-    if (blockIdx.x == 0 && (lo > hi || lo < 0 || hi > p.T || a < -1 || a >= p.L)) atomicMin(&s_wrong, s);
+    if (blockIdx.x == 0 && segment_wrong(lo, hi, a, p.T, p.L)) atomicMin(&s_wrong, s);
   }
   __syncthreads();
   const uint64_t mask = s_mask[0] | (static_cast<uint64_t>(s_mask[1]) << 32);
@@ -85,12 +87,7 @@ __global__ void __launch_bounds__(kScanThreads) fused_scan_kernel(const ShParams
       for (int e = 0; e < 8; ++e) v[e] = __ldg(b + s_ids[min(q + e, cnt - 1)] * chunks + i);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
-        bool hit = false;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)  // exponent bits all ones in either half
-          hit |= (w[j] & 0x7F80u) == 0x7F80u || (w[j] & 0x7F800000u) == 0x7F800000u;
-        if (hit) {
+        if (not_finite8(v[e])) {
           const int a = s_ids[min(q + e, cnt - 1)];
           atomicOr(&s_bad[a >> 5], 1u << (a & 31));
         }
@@ -125,22 +122,28 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
     mbar_init(&sm.tempty, 128);
     sm.abort_flag = 0;
     sm.mask[0] = sm.mask[1] = 0u;
+    sm.wrong = 0x7fffffff;
     fence_mbarrier_init();
   }
   if (warp == 1) tmem_alloc(&sm.tmem_base, kShN);
   __syncthreads();
-  // each token's adapter: the last segment that begins at or before it and ends behind it
+  if (p.validate && blockIdx.x == 0) {  // the call's first kernel: its status word
+    int wrong = 0x7fffffff;
+    for (int s = tid; s < p.S; s += kShThreads)
+      if (segment_wrong(p.seg_offsets[s], p.seg_offsets[s + 1], p.seg_adapter[s], p.T, p.L)) wrong = min(wrong, s);
+    atomicMin(&sm.wrong, wrong);
+    __syncthreads();
+    if (tid == 0) {
+      p.status[0] = sm.wrong != 0x7fffffff ? MOE_LORA_ERR_DEVICE_CHECK : MOE_LORA_OK;
+      p.status[1] = sm.wrong != 0x7fffffff ? sm.wrong : 0;
+    }
+  }
   if (tid < 128) {
     const int t = t0 + tid;
     int a = -1;
     if (t < p.T) {
-      int lo = 0, hi = p.S;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.seg_offsets[mid] <= t) lo = mid;
-        else hi = mid;
-      }
-      if (p.seg_offsets[lo] <= t && t < p.seg_offsets[lo + 1]) a = p.seg_adapter[lo];
+      const int s = segment_of(p.seg_offsets, p.S, t);
+      if (s >= 0) a = p.seg_adapter[s];
       if (a >= p.L || a < 0) a = -1;
       if (chunk0 == 0 && rank == 0) p.row_adapter[t] = a;
     }
@@ -276,7 +279,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
         volatile int dummy = 0;
         mbar_wait(&sm.full[s], (parity_of >> s) & 1u, &dummy, nullptr, kFtWaitNs / 4, 0);
       }
-  if (blockIdx.x == 0 && warp == 2) {  // what the scan found; this launch ends behind it
+  if (p.scan_ctas > 0 && blockIdx.x == 0 && warp == 2) {  // what the scan found; this launch ends behind it
     pdl_wait();
     uint64_t b = 0ull;
     for (int i = lane; i < p.scan_ctas; i += 32) b |= *reinterpret_cast<const volatile uint64_t*>(p.bad_part + i);
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
   if (warp == 1) tmem_dealloc(tmem, kShN);
 }
 
-cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, cudaStream_t st) {
+cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool scan, cudaStream_t st) {
   const DenseFusedArgs& a = f.a;
   CUtensorMap tmx, tma;
   if (encode_tmap_2d(&tmx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.h_in, a.T, static_cast<uint64_t>(a.h_in) * 2, 64,
@@ -322,7 +325,8 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, cudaStream_t st) {
   // chunks of a tile side by side while SMs are left
   const int apc = kShN / a.r, most = (std::min(std::min(a.L, a.S), 128) + apc - 1) / apc;
   p.P = std::max(1, std::min(most, a.num_sms / (tiles * p.C)));
-  p.scan_ctas = std::min(kFusedScanMax, kScanCtasPerSm * a.num_sms);
+  p.validate = !scan;
+  p.scan_ctas = !scan ? 0 : std::min(kFusedScanMax, kScanCtasPerSm * a.num_sms);
   const size_t smem = 1024 + kShStages * kShStageBytes + 128u * (a.r + 4) * 4;
   static std::atomic<bool> attr_set[kMaxDevices];
   const int dev = current_device_index();
@@ -334,8 +338,10 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, cudaStream_t st) {
     attr_set[dev].store(true, std::memory_order_release);
   }
   ProfScope ps(K_FUSED_SHRINK, st);
-  fused_scan_kernel<<<p.scan_ctas, kScanThreads, 0, st>>>(p);
-  count_launch();
+  if (scan) {
+    fused_scan_kernel<<<p.scan_ctas, kScanThreads, 0, st>>>(p);
+    count_launch();
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(tiles * p.P * p.C);
   cfg.blockDim = dim3(kShThreads);
@@ -349,10 +355,131 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, cudaStream_t st) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = scan ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, fused_shrink_kernel, tmx, tma, p);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- few tokens
+// z of a small batch on CUDA cores: latency counts, and CTAs that need no shared memory run
+// beside the projection's, which starts meanwhile.  An item is up to 4 tokens of a segment; a
+// CTA takes 4 rank rows of an item, its 8 warps split h_in.
+constexpr int kSsTok = 4, kSsRank = 4, kSsThreads = 256;
+
+__global__ void __launch_bounds__(kSsThreads) fused_shrink_small_kernel(const ShParams p, const __nv_bfloat16* __restrict__ x,
+                                                                       const __nv_bfloat16* __restrict__ lora_a) {
+  __shared__ float s_red[8][kSsTok * kSsRank];
+  __shared__ int s_item[4];  // segment, first token, tokens (0: no such item), any segment wrong
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();
+  const int i0 = blockIdx.y * kSsRank;
+  for (int item = blockIdx.x;; item += gridDim.x) {
+    if (warp == 0) {
+      int base = 0, first_wrong = 0x7fffffff;
+      if (lane == 0) s_item[2] = 0;
+      __syncwarp();
+      for (int s0 = 0; s0 < p.S; s0 += 32) {
+        const int s = s0 + lane;
+        int lo = 0, hi = 0, a = -1;
+        if (s < p.S) {
+          lo = p.seg_offsets[s];
+          hi = p.seg_offsets[s + 1];
+          a = p.seg_adapter[s];
+          if (segment_wrong(lo, hi, a, p.T, p.L)) first_wrong = min(first_wrong, s);
+          lo = max(lo, 0);
+          hi = min(hi, p.T);
+        }
+        const int n = (a >= 0 && a < p.L && hi > lo) ? (hi - lo + kSsTok - 1) / kSsTok : 0;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        const int at = item - base - (incl - n);
+        if (at >= 0 && at < n) {
+          s_item[0] = s;
+          s_item[1] = lo + at * kSsTok;
+          s_item[2] = min(kSsTok, hi - lo - at * kSsTok);
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      first_wrong = __reduce_min_sync(0xffffffffu, first_wrong);
+      if (lane == 0) {
+        s_item[3] = first_wrong != 0x7fffffff;
+        if (blockIdx.x == 0 && blockIdx.y == 0 && item == 0) {  // the call's first kernel: its status word
+          p.status[0] = s_item[3] ? MOE_LORA_ERR_DEVICE_CHECK : MOE_LORA_OK;
+          p.status[1] = s_item[3] ? first_wrong : 0;
+        }
+      }
+    }
+    __syncthreads();
+    const int seg = s_item[0], t0 = s_item[1], nt = s_item[2];
+    const bool wrong = s_item[3];
+    if (nt == 0) return;
+    const int a = p.seg_adapter[seg];
+    float acc[kSsRank][kSsTok] = {};
+    const int h8 = p.K / 8;
+    const uint4* A = reinterpret_cast<const uint4*>(lora_a) + (static_cast<size_t>(a) * p.r + i0) * h8;
+    const uint4* X = reinterpret_cast<const uint4*>(x) + static_cast<size_t>(t0) * h8;
+#pragma unroll 2
+    for (int c = tid; c < h8; c += kSsThreads) {
+      uint4 av[kSsRank], xv[kSsTok];
+#pragma unroll
+      for (int i = 0; i < kSsRank; ++i) av[i] = __ldg(A + static_cast<size_t>(i) * h8 + c);
+#pragma unroll
+      for (int t = 0; t < kSsTok; ++t) xv[t] = __ldg(X + static_cast<size_t>(t < nt ? t : 0) * h8 + c);
+#pragma unroll
+      for (int t = 0; t < kSsTok; ++t)
+        if (t < nt) {
+#pragma unroll
+          for (int i = 0; i < kSsRank; ++i) acc[i][t] += dot8_bf16(av[i], xv[t]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kSsRank; ++i)
+#pragma unroll
+      for (int t = 0; t < kSsTok; ++t) {
+        const float v = warp_sum(acc[i][t]);
+        if (lane == 0) s_red[warp][t * kSsRank + i] = v;
+      }
+    __syncthreads();
+    if (tid < nt) {
+      const int t = t0 + tid;
+      if (!wrong || segment_of(p.seg_offsets, p.S, t) == seg) {
+        float s[kSsRank] = {};
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+#pragma unroll
+          for (int i = 0; i < kSsRank; ++i) s[i] += s_red[w][tid * kSsRank + i];
+        *reinterpret_cast<uint2*>(p.z + static_cast<size_t>(t) * p.r + i0) =
+            make_uint2(pack2_bf16(p.scale * s[0], p.scale * s[1]), pack2_bf16(p.scale * s[2], p.scale * s[3]));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+cudaError_t launch_fused_shrink_simt(const FusedTcArgs& f, cudaStream_t st) {
+  const DenseFusedArgs& a = f.a;
+  ShParams p{};
+  p.seg_offsets = a.seg_offsets;
+  p.seg_adapter = a.seg_adapter;
+  p.S = a.S;
+  p.T = a.T;
+  p.L = a.L;
+  p.r = a.r;
+  p.K = a.h_in;
+  p.scale = a.scale;
+  p.z = f.z;
+  p.status = a.status;
+  ProfScope ps(K_FUSED_SHRINK, st);
+  const int items = std::min(a.S, a.T) + a.T / kSsTok;  // one per segment and one per 4 more tokens
+  fused_shrink_small_kernel<<<dim3(items, a.r / kSsRank), kSsThreads, 0, st>>>(
+      p, static_cast<const __nv_bfloat16*>(a.x), static_cast<const __nv_bfloat16*>(a.lora_a));
+  count_launch();
+  return cudaGetLastError();
 }
 
 }  // namespace mlb

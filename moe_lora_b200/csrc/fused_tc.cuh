@@ -51,6 +51,12 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
   return v;
 }
 
+__device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t cluster_addr) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
 // arrive / wait whose release and acquire reach the whole cluster: for data that one CTA's
 // threads wrote to its shared memory and the leader's MMA reads there
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
@@ -95,10 +101,11 @@ struct AdapterGroups {
   int ids[8];  // adapters of the current group (-2: none)
   int na;      // how many
   __device__ __forceinline__ AdapterGroups(uint64_t mask, int rank) : rem(mask), r(rank), half(0), na(0) {}
-  __device__ __forceinline__ static int count(uint64_t mask, int r) {
-    const int n = __popcll(mask);
-    return r > 64 ? 2 * n : (n * r + 63) / 64;
-  }
+  // B boxes per 64 features: an odd adapter of rank 8 fills half an MMA step, so its rows come
+  // once more and meet zeros of z
+  __device__ __forceinline__ int boxes() const { return (r == 8 && (na & 1)) ? na + 1 : na; }
+  // MMA steps of 16 K columns
+  __device__ __forceinline__ int steps() const { return r > 64 ? 4 : (na * r + 15) / 16; }
   __device__ __forceinline__ bool next() {
     if (r > 64) {
       if (half == 0) {
@@ -134,6 +141,31 @@ struct AdapterGroups {
   }
   int k0 = 0;  // first rank row of the group's adapter (r = 128)
 };
+
+// Token t's segment: the last one that begins at or before it, if it ends behind it (-1: none).
+// Every kernel of a call asks here, so that they agree even on segments out of order.
+__device__ __forceinline__ int segment_of(const int32_t* off, int S, int t) {
+  int lo = 0, hi = S;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return (off[lo] <= t && t < off[lo + 1]) ? lo : -1;
+}
+
+__device__ __forceinline__ bool segment_wrong(int lo, int hi, int a, int T, int L) {
+  return lo > hi || lo < 0 || hi > T || a < -1 || a >= L;
+}
+
+// true if a bf16 of the eight is an infinity or NaN (exponent bits all ones)
+__device__ __forceinline__ bool not_finite8(uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool hit = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) hit |= (w[j] & 0x7F80u) == 0x7F80u || (w[j] & 0x7F800000u) == 0x7F800000u;
+  return hit;
+}
 
 // z rows [t0, t0 + N NT / 8) as a group's K-major tile (128-byte swizzle): a row
 // holds 64 K columns, its 16-byte chunk c at c ^ (row & 7).  Thread i of NT takes chunk i & 7
@@ -180,7 +212,9 @@ struct FusedTcArgs {
   uint64_t* bad_part;      // ... found by each CTA of the scan
 };
 constexpr int kScanCtasPerSm = 2;
-cudaError_t launch_fused_shrink_tc(const FusedTcArgs& p, cudaStream_t st);
+cudaError_t launch_fused_shrink_simt(const FusedTcArgs& p, cudaStream_t st);
+// scan: also record the adapters that are not finite (launch_fused_prefill_tc asks for them)
+cudaError_t launch_fused_shrink_tc(const FusedTcArgs& p, bool scan, cudaStream_t st);
 cudaError_t launch_fused_decode_tc(const FusedTcArgs& p, cudaStream_t st);
 cudaError_t launch_fused_prefill_tc(const FusedTcArgs& p, cudaStream_t st);
 

@@ -130,6 +130,22 @@ def test_a_broken_adapter_stays_with_its_tenant(T):
         check_dense(good, torch.from_numpy(y), where=rest)
 
 
+@pytest.mark.parametrize("row", [3, 64, 127])
+@pytest.mark.parametrize("T", [12, 40, 150, 300])
+def test_a_broken_half_of_a_wide_adapter(T, row):
+    """Rank 128, one infinity in either half of the rank rows: the tenant's features beside it
+    still get every rank row once."""
+    d = dense_inputs(T, 520, 328, 5, 128, BF16, "none", True, True, 11, none_frac=0.1)
+    good = dict(d, b=d["b"].clone())
+    rows = fr.row_adapters(T, d["offs"].numpy(), d["segs"].numpy())
+    assert (rows == 2).any()
+    d["b"][2, row, 17], good["b"][2, row, 17] = float("inf"), 0.0
+    y = run_dense(d).float().cpu()
+    assert not torch.isfinite(y[torch.from_numpy(rows == 2), 17]).any()
+    check_dense(good, y, where=np.ix_(np.arange(T), np.flatnonzero(np.arange(328) != 17)))
+    check_dense(good, y, where=np.flatnonzero(rows != 2))
+
+
 @pytest.mark.parametrize("T", [5, 300])
 def test_a_token_that_is_not_finite_stays_alone(T):
     d = dense_inputs(T, 264, 328, 3, 16, BF16, "gelu", True, True, 2)
