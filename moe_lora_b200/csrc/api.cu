@@ -264,7 +264,32 @@ RouteWs route_layout(void* base, int M, int E, int L) {
   return w;
 }
 
-RouteWs scored_layout(void* base, int M, int E, int L) { return route_layout(base, M, E, L); }
+struct ScoredWs {
+  int* status;
+  uint16_t* bitmap;
+  int32_t* before;
+  int32_t* flags;
+  size_t bytes;
+};
+
+ScoredWs scored_layout(void* base, int M, int E) {
+  size_t off = kStatusBytes;
+  ScoredWs w{};
+  uint8_t* b = static_cast<uint8_t*>(base);
+  auto take = [&](size_t bytes) {
+    uint8_t* p = b ? b + off : nullptr;
+    off += align256(bytes);
+    return p;
+  };
+  size_t bitmap, before, flags;
+  route_scored_scratch(M, E, &bitmap, &before, &flags);
+  w.status = reinterpret_cast<int*>(b);
+  w.bitmap = reinterpret_cast<uint16_t*>(take(bitmap));
+  w.before = reinterpret_cast<int32_t*>(take(before));
+  w.flags = reinterpret_cast<int32_t*>(take(flags));
+  w.bytes = off;
+  return w;
+}
 
 struct FusedWs {
   int* status;
@@ -416,7 +441,7 @@ size_t moe_lora_workspace_size(int op, int M, int H, int I, int E, int k, int L,
     case MOE_LORA_OP_FORWARD_BF16:
       return forward_layout(nullptr, M, H, I, k, L > 0 ? r : 0, false, lora_place(1LL * M * k, E), E * (L + 1))
           .bytes;
-    case MOE_LORA_OP_ROUTE_SCORED: return scored_layout(nullptr, M, E, L).bytes;
+    case MOE_LORA_OP_ROUTE_SCORED: return scored_layout(nullptr, M, E).bytes;
     case MOE_LORA_OP_DENSE_FUSED: return fused_layout(nullptr, M, L > 0 ? r : 0).bytes;
     case MOE_LORA_OP_SGMV_SHRINK:
     case MOE_LORA_OP_SGMV_EXPAND: return kStatusBytes;
@@ -536,7 +561,7 @@ moe_lora_status moe_lora_route_scored(const void* x, const void* w_router, const
   ML_REQUIRE(k <= fmt.topk_group * (E / fmt.n_group), MOE_LORA_ERR_INVALID_ARG,
              "the topk_group groups hold fewer than k experts");
   ML_PTR(seg_offsets);
-  const RouteWs need = scored_layout(nullptr, M, E, L);
+  const ScoredWs need = scored_layout(nullptr, M, E);
   moe_lora_status st = check_ws(workspace, workspace_bytes, need.bytes);
   if (st != MOE_LORA_OK) return st;
   if (score_bias) ML_PTR(score_bias);
@@ -558,30 +583,31 @@ moe_lora_status moe_lora_route_scored(const void* x, const void* w_router, const
   st = check_device();
   if (st != MOE_LORA_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  const RouteWs w = scored_layout(workspace, M, E, L);
-  ML_CUDA(cudaMemsetAsync(workspace, 0, 8, cs), "status clear");
-  RouteArgs a{};
+  const ScoredWs w = scored_layout(workspace, M, E);
+  if (M > 0 && logits_in == nullptr && !tensor_map_encode_available())
+    return fail(MOE_LORA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  RouteScoredArgs a{};
   a.x = static_cast<const __nv_bfloat16*>(x);
   a.w_router = static_cast<const __nv_bfloat16*>(w_router);
   a.bias = bias;
   a.logits_in = logits_in;
+  a.score_bias = score_bias;
   a.adapter_ids = adapter_ids;
   a.M = M;
   a.H = H;
   a.E = E;
   a.k = k;
   a.L = L;
-  a.logits = logits_out ? logits_out : w.logits;
   a.logits_out = logits_out;
   a.topk_ids = topk_ids;
   a.topk_w = topk_w;
   a.sorted_pairs = sorted_pairs;
   a.seg_offsets = seg_offsets;
-  a.key_count = w.key_count;
-  a.a_key = w.a_key;
+  a.bitmap = w.bitmap;
+  a.before = w.before;
+  a.flags = w.flags;
   a.status = w.status;
-  a.num_sms = num_sms();
-  ScoreFormat f{};
+  ScoreFormat& f = a.f;
   f.sigmoid = fmt.score == ML_SCORE_SIGMOID;
   f.n_group = fmt.n_group;
   f.topk_group = fmt.topk_group;
@@ -590,7 +616,7 @@ moe_lora_status moe_lora_route_scored(const void* x, const void* w_router, const
   f.renorm = fmt.renormalize;
   f.by_logit = score_bias == nullptr && !(fmt.n_group > 1 && f.top2);
   f.scale = fmt.scale;
-  ML_CUDA(launch_route_scored(a, f, score_bias, cs), "moe_lora_route_scored launch");
+  ML_CUDA(launch_route_scored(a, cs), "moe_lora_route_scored launch");
   return MOE_LORA_OK;
 }
 

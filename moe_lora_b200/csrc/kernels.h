@@ -31,11 +31,6 @@ struct RouteArgs {
   int tickets_zeroed = 0;  // the caller's status clear already zeroed the tickets
 };
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t st);
-// The logits of a routing call on their own: a.logits_in (copied to a.logits_out if set) or
-// x W_r^T + bias into a.logits; *lg is where they are.
-cudaError_t launch_router_logits(const RouteArgs& a, const float** lg, cudaStream_t st);
-// seg_offsets and sorted_pairs from topk_ids, the tokens' adapter keys and the key counts.
-cudaError_t launch_sort_scatter(const RouteArgs& a, cudaStream_t st);
 // Tickets (ints at a_key) of the one-launch routing for M tokens of k pairs, or 0 when the
 // routing takes the multi-kernel path.
 int route_fused_tickets(int M, int k);
@@ -49,7 +44,28 @@ struct ScoreFormat {
   int by_logit;    // the selection compares logits (no score_bias, no sums of scores)
   float scale;
 };
-cudaError_t launch_route_scored(const RouteArgs& a, const ScoreFormat& f, const float* score_bias, cudaStream_t st);
+struct RouteScoredArgs {
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* w_router;
+  const float* bias;
+  const float* logits_in;
+  const float* score_bias;
+  const int32_t* adapter_ids;
+  int M, H, E, k, L;
+  ScoreFormat f;
+  float* logits_out;      // may be null
+  int32_t* topk_ids;
+  float* topk_w;
+  int32_t* sorted_pairs;
+  int32_t* seg_offsets;
+  uint16_t* bitmap;       // workspace: see route_scored_scratch
+  int32_t* before;
+  int32_t* flags;
+  int* status;
+};
+// Bytes of the three scratch arrays of M tokens and E experts.
+void route_scored_scratch(int M, int E, size_t* bitmap, size_t* before, size_t* flags);
+cudaError_t launch_route_scored(const RouteScoredArgs& a, cudaStream_t st);
 
 // Segmented shrink z[s] = src_row(s) . A_seg(s)^T (SIMT: 128-bit loads, warp-shuffle
 // split-K reduction).  Segments come either from a dense (offsets, adapter) table or

@@ -508,8 +508,39 @@ int route_fused_tickets(int M, int k) {
   return (M > 0 && static_cast<long long>(M) * k <= RF_MAX_PAIRS) ? (M + RF_TB - 1) / RF_TB + 1 : 0;
 }
 
-cudaError_t launch_router_logits(const RouteArgs& a, const float** out, cudaStream_t st) {
-  cudaError_t err = cudaSuccess;
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
+  const int nk = a.E * (a.L + 1);
+  if (a.M == 0) return cudaMemsetAsync(a.seg_offsets, 0, sizeof(int32_t) * (nk + 1), st);
+  if (static_cast<long long>(a.M) * a.k <= RF_MAX_PAIRS) {
+    // one launch; a_key[0, n_tb] holds the tickets (zeroed here unless the caller's
+    // status clear covered them)
+    const int n_tb = (a.M + RF_TB - 1) / RF_TB;
+    cudaError_t err = a.tickets_zeroed ? cudaSuccess : cudaMemsetAsync(a.a_key, 0, sizeof(int32_t) * (n_tb + 1), st);
+    if (err != cudaSuccess) return err;
+    const size_t smem = route_fused_smem(a.E, a.L, a.M, a.k);
+    // the raised shared-memory limit is a per-device function attribute
+    static std::atomic<bool> attr_set[kMaxDevices];
+    const int dev = current_device_index();
+    if (dev < 0) return cudaErrorInvalidDevice;
+    if (!attr_set[dev].load(std::memory_order_acquire)) {
+      const int most = static_cast<int>(route_fused_smem(256, 64, 1, RF_MAX_PAIRS));  // E = 256, L = 64, caps
+      err = cudaFuncSetAttribute(route_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+      if (err != cudaSuccess) return err;
+      attr_set[dev].store(true, std::memory_order_release);
+    }
+    if (a.logits_in != nullptr && a.logits_out != nullptr) {
+      err = cudaMemcpyAsync(a.logits_out, a.logits_in, sizeof(float) * a.M * a.E, cudaMemcpyDeviceToDevice, st);
+      if (err != cudaSuccess) return err;
+    }
+    const int n_eb = (a.E + RF_EB - 1) / RF_EB;
+    const int grid = a.logits_in ? n_tb : n_eb * n_tb;
+    ProfScope ps(K_ROUTE, st);
+    route_fused_kernel<<<grid, 256, smem, st>>>(a, a.logits_in, n_eb);
+    count_launch();
+    return cudaGetLastError();
+  }
+  cudaError_t err = cudaMemsetAsync(a.key_count, 0, sizeof(int32_t) * nk, st);
+  if (err != cudaSuccess) return err;
   const float* lg = a.logits_in;
   if (lg == nullptr && a.M >= 256 && tensor_map_encode_available()) {
     // large batches: logits on the tensor cores (the grouped GEMM with one group, W_r
@@ -548,61 +579,19 @@ cudaError_t launch_router_logits(const RouteArgs& a, const float** out, cudaStre
                           cudaMemcpyDeviceToDevice, st);
     if (err != cudaSuccess) return err;
   }
-  *out = lg;
-  return cudaGetLastError();
-}
-
-cudaError_t launch_sort_scatter(const RouteArgs& a, cudaStream_t st) {
-  ProfScope ps(K_SORT, st);
-  sort_scatter_kernel<<<a.E, 512, 0, st>>>(a.topk_ids, a.a_key, a.key_count, a.M, a.k, a.E, a.L, a.sorted_pairs,
-                                           a.seg_offsets);
-  count_launch();
-  return cudaGetLastError();
-}
-
-cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
-  const int nk = a.E * (a.L + 1);
-  if (a.M == 0) return cudaMemsetAsync(a.seg_offsets, 0, sizeof(int32_t) * (nk + 1), st);
-  if (static_cast<long long>(a.M) * a.k <= RF_MAX_PAIRS) {
-    // one launch; a_key[0, n_tb] holds the tickets (zeroed here unless the caller's
-    // status clear covered them)
-    const int n_tb = (a.M + RF_TB - 1) / RF_TB;
-    cudaError_t err = a.tickets_zeroed ? cudaSuccess : cudaMemsetAsync(a.a_key, 0, sizeof(int32_t) * (n_tb + 1), st);
-    if (err != cudaSuccess) return err;
-    const size_t smem = route_fused_smem(a.E, a.L, a.M, a.k);
-    // the raised shared-memory limit is a per-device function attribute
-    static std::atomic<bool> attr_set[kMaxDevices];
-    const int dev = current_device_index();
-    if (dev < 0) return cudaErrorInvalidDevice;
-    if (!attr_set[dev].load(std::memory_order_acquire)) {
-      const int most = static_cast<int>(route_fused_smem(256, 64, 1, RF_MAX_PAIRS));  // E = 256, L = 64, caps
-      err = cudaFuncSetAttribute(route_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-      if (err != cudaSuccess) return err;
-      attr_set[dev].store(true, std::memory_order_release);
-    }
-    if (a.logits_in != nullptr && a.logits_out != nullptr) {
-      err = cudaMemcpyAsync(a.logits_out, a.logits_in, sizeof(float) * a.M * a.E, cudaMemcpyDeviceToDevice, st);
-      if (err != cudaSuccess) return err;
-    }
-    const int n_eb = (a.E + RF_EB - 1) / RF_EB;
-    const int grid = a.logits_in ? n_tb : n_eb * n_tb;
-    ProfScope ps(K_ROUTE, st);
-    route_fused_kernel<<<grid, 256, smem, st>>>(a, a.logits_in, n_eb);
-    count_launch();
-    return cudaGetLastError();
-  }
-  cudaError_t err = cudaMemsetAsync(a.key_count, 0, sizeof(int32_t) * nk, st);
-  if (err != cudaSuccess) return err;
-  const float* lg = nullptr;
-  err = launch_router_logits(a, &lg, st);
-  if (err != cudaSuccess) return err;
   {
     ProfScope ps(K_TOPK, st);
     topk_kernel<<<(a.M + 7) / 8, 256, 0, st>>>(lg, a.adapter_ids, a.M, a.E, a.k, a.L, a.topk_ids,
                                                a.topk_w, a.key_count, a.a_key, a.status);
     count_launch();
   }
-  return launch_sort_scatter(a, st);
+  {
+    ProfScope ps(K_SORT, st);
+    sort_scatter_kernel<<<a.E, 512, 0, st>>>(a.topk_ids, a.a_key, a.key_count, a.M, a.k, a.E, a.L,
+                                             a.sorted_pairs, a.seg_offsets);
+    count_launch();
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace mlb

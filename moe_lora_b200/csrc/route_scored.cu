@@ -4,24 +4,82 @@
 // A router sends each token to its most relevant experts ([vLLM MoE-LoRA page],
 // "Entendendo os Modelos MoE"); scores, bias, groups and scaling are the generic forms of
 // that choice.
-#include "common.cuh"
-#include "kernels.h"
+//
+// One kernel makes logits, choice and weights: a cluster of C CTAs takes 128 tokens x all E
+// experts (one tcgen05 tile: tokens in M, experts in N), splits H, and each CTA adds up the
+// partial logits of 128 / C tokens from its peers' shared memory in rank order; its warps
+// then choose those tokens' experts, a warp per token, the logits never leaving the SM.  x
+// is read once, W_r once per 128 tokens (from L2).
+//
+// The sort needs no atomics on global memory: a CTA leaves one bit per (expert, token) and
+// the running count of its pairs by expert.  Up to 128 tokens the cluster itself sorts (a
+// warp per expert); above, a second kernel does, a CTA per expert.
+#include "fused_tc.cuh"
 #include "prof.h"
 
+#include <algorithm>
+#include <atomic>
 #include <cfloat>
+#include <climits>
 
 namespace mlb {
 
-// One warp chooses the experts of one token.  Lane l holds experts l, l + 32, ... (E <= 256,
-// eight at most), its selection scores in c[8] (-inf for a NaN: below every number, since
-// infinite logits and biases are clamped to the largest finite float first).
-//
-// The scores are computed in 64 bits: two experts whose 32-bit scores are equal or off by a
-// rounding would otherwise be ordered by the rounding.
+constexpr int kRsThreads = 512;
+constexpr int kRsWarps = kRsThreads / 32;
+constexpr int kRsMaxStages = 8;
+constexpr int kRsRing = 196608;  // bytes of the ring at most
 
-constexpr int kScWarps = 8;
+struct RsParams {
+  const float* logits_in;
+  const float* bias;
+  const float* score_bias;
+  const int32_t* adapter_ids;
+  float* logits_out;
+  int32_t* topk_ids;
+  float* topk_w;
+  int32_t* sorted_pairs;
+  int32_t* seg_offsets;
+  uint16_t* bitmap;  // [E][8 tiles]: bit t % 16 of word t / 16: token t chose the expert
+  int32_t* before;   // [E][chunks]: the chunk's pairs of lower experts
+  int32_t* flags;    // [chunks]: what the chunk has to report (kRsClean: nothing)
+  int* status;
+  int M, H, E, k, L, C, tiles, epad, stages;
+  ScoreFormat f;
+};
 
-__device__ __forceinline__ float clamp_finite(float v) { return fminf(fmaxf(v, -FLT_MAX), FLT_MAX); }  // NaN: FLT_MAX or -FLT_MAX, checked apart
+constexpr int kRsClean = INT_MAX;  // a token that failed a check: its index; a wait that ran out: < 0
+
+struct RsCore {
+  uint64_t full[kRsMaxStages], empty[kRsMaxStages], tfull;
+  uint32_t tmem_base;
+  int abort_flag;
+  int flag;
+  int scan[kRsWarps];
+  alignas(16) uint4 map[256];  // tokens of the tile (this CTA's: 128 / C of them) by expert
+  uint8_t ids[kRsWarps][256];  // a token's choice
+};
+
+// ------------------------------------------------------------------ the choice of one token
+__device__ __forceinline__ float clamp_finite(float v) { return fminf(fmaxf(v, -FLT_MAX), FLT_MAX); }
+
+// Order-preserving unsigned key of a finite float, at least 0x00800000; both zeros alike.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
+}
+constexpr uint32_t kNanKey = 1u;  // below every number, above "not a candidate" (0)
+
+// True if fp32 selection scores prove a > b.  A score is off by at most 2^-20 (exponential:
+// 2 + 1.17 |d| steps of 2^-23 of a value e^-|d| at most; the sum's and the quotient's roundings), a sum
+// of two by 2^-19; the add of a bias rounds to 2^-24 of the result.
+__device__ __forceinline__ bool surely_above(uint32_t a, uint32_t b) {
+  if (b <= kNanKey) return a > b;
+  const float x = key_value(a), y = key_value(b);
+  return x - y > 0x1p-18f + 0x1p-21f * (fabsf(x) + fabsf(y));
+}
 
 __device__ __forceinline__ void warp_argmax(double& v, int& e) {
 #pragma unroll
@@ -35,76 +93,55 @@ __device__ __forceinline__ void warp_argmax(double& v, int& e) {
   }
 }
 
-__global__ void __launch_bounds__(kScWarps * 32) score_topk_kernel(const float* __restrict__ logits,
-                                                                  const float* __restrict__ score_bias,
-                                                                  const RouteArgs a, const ScoreFormat f) {
-  __shared__ double s_c[kScWarps][256];
-  __shared__ double s_s[kScWarps][256];
-  __shared__ int s_id[kScWarps][256];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kScWarps + warp;
-  if (t >= a.M) return;
-  const int E = a.E, k = a.k;
-  float l[8];
-  bool bad = false;
-  unsigned nan_mask = 0u, alive = 0u;
+// The definition in 64 bits: for tokens whose 32-bit scores lie too close to prove an order.
+// Lane l holds experts l, l + 32, ...; c: 256 doubles of the warp.
+template <int NI>
+__device__ __noinline__ void choose_exact(const float* row, const RsParams& p, double* c_of, uint8_t* ids) {
+  const int lane = threadIdx.x & 31;
+  const int E = p.E;
+  const ScoreFormat& f = p.f;
+  unsigned alive = 0u;
   float mx = -FLT_MAX;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < NI; ++i) {
     const int e = lane + 32 * i;
-    l[i] = -FLT_MAX;
     if (e < E) {
       alive |= 1u << i;
-      const float v = logits[static_cast<size_t>(t) * E + e];
-      if (v != v) nan_mask |= 1u << i;
-      else l[i] = clamp_finite(v);
-      mx = fmaxf(mx, l[i]);
+      if (row[e] == row[e]) mx = fmaxf(mx, clamp_finite(row[e]));
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  double s[8], sum = 0.0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    s[i] = 0.0;
-    if (!((alive & ~nan_mask) >> i & 1u)) continue;
-    s[i] = f.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l[i]))) : exp(static_cast<double>(l[i]) - mx);
-    sum += s[i];
-  }
+  double sum = 1.0;
   if (!f.sigmoid) {
+    sum = 0.0;
+    for (int i = 0; i < NI; ++i) {
+      const int e = lane + 32 * i;
+      if (e < E && row[e] == row[e]) sum += exp(static_cast<double>(clamp_finite(row[e])) - mx);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if ((alive & ~nan_mask) >> i & 1u) s[i] /= sum;
   }
-  double c[8];
+  auto score = [&](int e) -> double {
+    const double l = clamp_finite(row[e]);
+    return f.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - mx) / sum;
+  };
+  auto bias = [&](int e) -> double { return p.score_bias ? static_cast<double>(clamp_finite(p.score_bias[e])) : 0.0; };
+  double c[NI];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < NI; ++i) {
     const int e = lane + 32 * i;
     c[i] = -INFINITY;
     if (e >= E) continue;
-    const float b = score_bias ? score_bias[e] : 0.f;
-    if ((nan_mask >> i & 1u) || b != b) {
-      bad = true;
-      continue;
-    }
-    c[i] = f.by_logit ? static_cast<double>(l[i]) : s[i] + static_cast<double>(clamp_finite(b));
+    const bool nan = row[e] != row[e] || (p.score_bias && p.score_bias[e] != p.score_bias[e]);
+    if (!nan) c[i] = f.by_logit ? static_cast<double>(clamp_finite(row[e])) : score(e) + bias(e);
+    c_of[e] = c[i];
   }
-
+  __syncwarp();
   if (f.n_group > 1) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (lane + 32 * i < E) {
-        s_c[warp][lane + 32 * i] = c[i];
-        s_s[warp][lane + 32 * i] = s[i];
-      }
-    __syncwarp();
-    // group scores: lane g holds groups g, g + 32, ...
-    double gs[8];
+    double gs[NI];  // lane g holds groups g, g + 32, ...
     unsigned galive = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < NI; ++i) {
       const int g = lane + 32 * i;
       gs[i] = -INFINITY;
       if (g >= f.n_group) continue;
@@ -113,7 +150,7 @@ __global__ void __launch_bounds__(kScWarps * 32) score_topk_kernel(const float* 
       int e1 = g * f.group_size, e2 = e1;
       for (int j = 0; j < f.group_size; ++j) {
         const int e = g * f.group_size + j;
-        const double v = s_c[warp][e];
+        const double v = c_of[e];
         if (v > m1) {
           m2 = m1;
           e2 = e1;
@@ -128,18 +165,14 @@ __global__ void __launch_bounds__(kScWarps * 32) score_topk_kernel(const float* 
       // scores and biases summed apart, so that groups whose two best have the same scores
       // and the same sum of biases tie, whatever the roundings
       if (f.top2 && f.group_size > 1)
-        gs[i] = m2 == -INFINITY ? m2
-                                : (s_s[warp][e1] + s_s[warp][e2]) +
-                                      (score_bias ? static_cast<double>(clamp_finite(score_bias[e1])) +
-                                                        static_cast<double>(clamp_finite(score_bias[e2]))
-                                                  : 0.0);
+        gs[i] = m2 == -INFINITY ? m2 : (score(e1) + score(e2)) + (bias(e1) + bias(e2));
     }
     unsigned keep = 0u;  // this lane's experts in a kept group
     for (int j = 0; j < f.topk_group; ++j) {
       double bv = -INFINITY;
       int bg = 0x7fffffff;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < NI; ++i)
         if ((galive >> i & 1u) && (bg == 0x7fffffff || gs[i] > bv)) {
           bv = gs[i];
           bg = lane + 32 * i;
@@ -147,85 +180,748 @@ __global__ void __launch_bounds__(kScWarps * 32) score_topk_kernel(const float* 
       warp_argmax(bv, bg);
       if ((bg & 31) == lane) galive &= ~(1u << (bg >> 5));
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < NI; ++i)
         if ((lane + 32 * i) / f.group_size == bg) keep |= 1u << i;
     }
     alive &= keep;
   }
-
-  for (int j = 0; j < k; ++j) {
+  for (int j = 0; j < p.k; ++j) {
     double bv = -INFINITY;
     int be = 0x7fffffff;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < NI; ++i)
       if ((alive >> i & 1u) && (be == 0x7fffffff || c[i] > bv)) {
         bv = c[i];
         be = lane + 32 * i;
       }
     warp_argmax(bv, be);
     if ((be & 31) == lane) alive &= ~(1u << (be >> 5));
-    if (lane == 0) s_id[warp][j] = be;
+    if (lane == 0) ids[j] = static_cast<uint8_t>(be);
   }
   __syncwarp();
-
-  // weights of the chosen, in 32 bits.  Renormalised: relative to the largest chosen logit
-  // (at most 0 for sigmoids), so that scores below the smallest float keep their ratio.
-  int ad = a.adapter_ids[t];
-  if (ad < -1 || ad >= a.L) {
-    bad = true;
-    ad = -1;
-  }
-  const int ap = ad >= 0 ? ad : a.L;
-  float top = -FLT_MAX;
-  if (f.renorm) {
-    for (int j = lane; j < k; j += 32) {
-      const float v = logits[static_cast<size_t>(t) * E + s_id[warp][j]];
-      if (v == v) top = fmaxf(top, clamp_finite(v));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (f.sigmoid) top = fminf(top, 0.f);
-  } else {
-    top = f.sigmoid ? 0.f : mx;
-  }
-  float wsum = 0.f;
-  for (int j = lane; j < k; j += 32) {
-    const int e = s_id[warp][j];
-    const float raw = logits[static_cast<size_t>(t) * E + e];
-    const float v = clamp_finite(raw);
-    float w = 0.f;
-    if (raw == raw) {
-      if (!f.sigmoid) w = expf(v - top);
-      else w = v > 0.f ? 1.f / (1.f + expf(-v)) : expf(v - top) / (1.f + expf(v));
-    }
-    wsum += w;
-    a.topk_ids[static_cast<size_t>(t) * k + j] = e;
-    a.topk_w[static_cast<size_t>(t) * k + j] = w;
-    atomicAdd(a.key_count + e * (a.L + 1) + ap, 1);
-  }
-  wsum = warp_sum(wsum);
-  float mul = f.scale;
-  if (f.renorm) mul = wsum > 0.f ? f.scale / wsum : 0.f;
-  else if (!f.sigmoid) mul = f.scale / static_cast<float>(sum);
-  for (int j = lane; j < k; j += 32) a.topk_w[static_cast<size_t>(t) * k + j] *= mul;
-  if (lane == 0) a.a_key[t] = ap;
-  if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(a.status, MOE_LORA_ERR_DEVICE_CHECK, t);
 }
 
-cudaError_t launch_route_scored(const RouteArgs& a, const ScoreFormat& f, const float* score_bias, cudaStream_t st) {
-  const int nk = a.E * (a.L + 1);
-  if (a.M == 0) return cudaMemsetAsync(a.seg_offsets, 0, sizeof(int32_t) * (nk + 1), st);
-  cudaError_t err = cudaMemsetAsync(a.key_count, 0, sizeof(int32_t) * nk, st);
-  if (err != cudaSuccess) return err;
-  const float* lg = nullptr;
-  err = launch_router_logits(a, &lg, st);
-  if (err != cudaSuccess) return err;
-  {
-    ProfScope ps(K_ROUTE_SCORED, st);
-    score_topk_kernel<<<(a.M + kScWarps - 1) / kScWarps, kScWarps * 32, 0, st>>>(lg, score_bias, a, f);
-    count_launch();
+// The k experts of the token whose logits are row[0, E), in order, into ids; returns whether
+// a NaN was met.  Selection scores in fp32 as order-preserving keys; every order that decides
+// (between the chosen, to the first one left out, between kept and dropped groups) has to be
+// wider than the scores' error, else the token is done again in 64 bits.  Logits compared as
+// such need no proof.  scratch: a double of the warp per expert.
+template <int NI>
+__device__ __forceinline__ bool choose(const float* row, const RsParams& p, const float (&sb)[NI], double* scratch,
+                                       uint8_t* ids, float& mx_out, float& sum_out) {
+  const int lane = threadIdx.x & 31;
+  const int E = p.E;
+  const ScoreFormat& f = p.f;
+  float l[NI];
+  uint32_t key[NI];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int e = lane + 32 * i;
+    const float v = e < E ? row[e] : -FLT_MAX;
+    const bool nan = v != v;
+    bad |= nan || sb[i] != sb[i];
+    l[i] = nan ? -FLT_MAX : clamp_finite(v);
+    key[i] = e < E ? (nan || sb[i] != sb[i] ? kNanKey : order_key(l[i])) : 0u;
   }
-  return launch_sort_scatter(a, st);
+  const bool need_sum = !f.sigmoid && !(f.by_logit && f.renorm);
+  float mx = -FLT_MAX, sum = 1.f;
+  if (!f.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) mx = fmaxf(mx, l[i]);
+    mx = key_value(__reduce_max_sync(0xffffffffu, order_key(mx)));
+  }
+  float s[NI];
+  if (need_sum) {
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int e = lane + 32 * i;
+      s[i] = e < E && row[e] == row[e] ? expf(l[i] - mx) : 0.f;
+      sum += s[i];
+    }
+    sum = warp_sum(sum);
+  }
+  mx_out = mx;
+  sum_out = sum;
+  bool exact = f.n_group > 32;
+  if (!f.by_logit) {
+    const float inv = 1.f / sum;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const float v = f.sigmoid ? __fdividef(1.f, 1.f + __expf(-l[i])) : s[i] * inv;
+      if (key[i] > kNanKey) key[i] = order_key(clamp_finite(v + clamp_finite(sb[i])));
+    }
+  }
+  if (f.n_group > 1 && !exact) {
+    uint32_t* keys = reinterpret_cast<uint32_t*>(scratch);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (lane + 32 * i < E) keys[lane + 32 * i] = key[i];
+    __syncwarp();
+    // `per` lanes per group walk its experts, starting at different places so that the lanes
+    // stay on different banks, and join their two largest
+    int per = 32;
+    while (per * f.n_group > 32) per >>= 1;
+    const int g = lane / per, sub = lane % per;
+    uint32_t m1 = 0u, m2 = 0u;
+    if (g < f.n_group) {
+      const int cnt = (f.group_size - sub + per - 1) / per;
+      int j = cnt > 0 ? g % cnt : 0;
+      for (int n = 0; n < cnt; ++n) {
+        const uint32_t v = keys[g * f.group_size + sub + j * per];
+        m2 = max(m2, min(m1, v));
+        m1 = max(m1, v);
+        j = j + 1 == cnt ? 0 : j + 1;
+      }
+    }
+    for (int o = 1; o < per; o <<= 1) {
+      const uint32_t a1 = __shfl_xor_sync(0xffffffffu, m1, o), a2 = __shfl_xor_sync(0xffffffffu, m2, o);
+      m2 = max(max(m2, a2), min(m1, a1));
+      m1 = max(m1, a1);
+    }
+    uint32_t gk = m1;
+    if (f.top2 && f.group_size > 1) {
+      if (m2 <= kNanKey) {
+        gk = kNanKey;
+      } else {
+        const float a = key_value(m1), b = key_value(m2);
+        exact |= g < f.n_group && fabsf(a) + fabsf(b) > 0x1p20f;  // (its error is that of the terms)
+        gk = order_key(clamp_finite(a + b));
+      }
+    }
+    // rank among the groups: how many are larger, or as large and before
+    int rank = 0;
+    for (int h = 0; h < f.n_group; ++h) {
+      const uint32_t o = __shfl_sync(0xffffffffu, gk, h * per);
+      rank += (o > gk || (o == gk && h < g)) ? 1 : 0;
+    }
+    const bool in = g < f.n_group, kept = in && rank < f.topk_group;
+    if (!f.by_logit) {
+      const uint32_t lo = __reduce_min_sync(0xffffffffu, kept ? gk : 0xffffffffu);
+      const uint32_t hi = __reduce_max_sync(0xffffffffu, in && !kept ? gk : 0u);
+      exact |= !surely_above(lo, hi);
+    }
+    const unsigned keep = __ballot_sync(0xffffffffu, kept);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int e = lane + 32 * i;
+      if (e < E && !(keep >> (e / f.group_size * per) & 1u)) key[i] = 0u;
+    }
+    exact = __any_sync(0xffffffffu, exact);
+  }
+  if (!exact) {
+    uint32_t prev = 0u;
+    // one more than k, to see the first one left out
+    const int rounds = f.by_logit ? p.k : p.k + 1;
+    for (int j = 0; j < rounds; ++j) {
+      uint32_t best = key[0], at = 0u;
+#pragma unroll
+      for (int i = 1; i < NI; ++i)
+        if (key[i] > best) {
+          best = key[i];
+          at = i;
+        }
+      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+      if (!f.by_logit && j > 0 && !surely_above(prev, top)) {
+        exact = true;
+        break;
+      }
+      if (j == p.k) break;
+      prev = top;
+      const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? lane + 32u * at : 0xffffffffu);
+      if ((e & 31u) == static_cast<uint32_t>(lane)) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          if (e >> 5 == static_cast<uint32_t>(i)) key[i] = 0u;
+      }
+      if (lane == 0) ids[j] = static_cast<uint8_t>(e);
+    }
+    __syncwarp();
+  }
+  if (exact) {
+    __syncwarp();
+    choose_exact<NI>(row, p, scratch, ids);
+  }
+  return __any_sync(0xffffffffu, bad);
+}
+
+// Weights of the chosen, in 32 bits.  Renormalised: relative to the largest chosen logit (at
+// most 0 for sigmoids), so that scores below the smallest float keep their ratio.
+__device__ __forceinline__ void weigh(const float* row, const RsParams& p, const uint8_t* ids, int t, float mx,
+                                      float sum) {
+  const int lane = threadIdx.x & 31;
+  const ScoreFormat& f = p.f;
+  float top = f.sigmoid ? 0.f : mx;
+  if (f.renorm) {
+    top = -FLT_MAX;
+    for (int j = lane; j < p.k; j += 32) {
+      const float v = row[ids[j]];
+      if (v == v) top = fmaxf(top, clamp_finite(v));
+    }
+    top = key_value(__reduce_max_sync(0xffffffffu, order_key(top)));
+    if (f.sigmoid) top = fminf(top, 0.f);
+  }
+  auto weight = [&](int e) -> float {
+    const float raw = row[e], v = clamp_finite(raw);
+    if (raw != raw) return 0.f;
+    if (!f.sigmoid) return expf(v - top);
+    return v > 0.f ? 1.f / (1.f + expf(-v)) : expf(v - top) / (1.f + expf(v));
+  };
+  float mul = f.scale;
+  if (f.renorm) {
+    float wsum = 0.f;
+    for (int j = lane; j < p.k; j += 32) wsum += weight(ids[j]);
+    wsum = warp_sum(wsum);
+    mul = wsum > 0.f ? f.scale / wsum : 0.f;
+  } else if (!f.sigmoid) {
+    mul = sum > 0.f ? f.scale / sum : 0.f;
+  }
+  for (int j = lane; j < p.k; j += 32) {
+    p.topk_ids[static_cast<size_t>(t) * p.k + j] = ids[j];
+    p.topk_w[static_cast<size_t>(t) * p.k + j] = weight(ids[j]) * mul;
+  }
+}
+
+// ------------------------------------------------------------------ the stable sort
+// Slot of expert e among token t's k choices (the token chose it); written by this kernel's
+// peers or the kernel ahead.
+__device__ __forceinline__ int slot_of_expert(const int32_t* topk_ids, int t, int k, int e) {
+  const int32_t* row = topk_ids + static_cast<size_t>(t) * k;
+  if ((k & 3) == 0) {
+    for (int q = 0; q < k; q += 4) {
+      const int4 v = __ldcg(reinterpret_cast<const int4*>(row + q));
+      if (v.x == e) return q;
+      if (v.y == e) return q + 1;
+      if (v.z == e) return q + 2;
+      if (v.w == e) return q + 3;
+    }
+    return 0;
+  }
+  for (int j = 0; j < k; ++j)
+    if (__ldcg(row + j) == e) return j;
+  return 0;
+}
+
+__device__ __forceinline__ uint4 ld_cluster_u32x4(uint32_t cluster_addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ int ld_cluster_s32(uint32_t cluster_addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+// exclusive prefix sum over the CTA's 512 threads
+__device__ __forceinline__ int block_prefix(int v, int* s_scan) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  int base = 0;
+#pragma unroll
+  for (int w = 0; w < kRsWarps; ++w) base += w < warp ? s_scan[w] : 0;
+  return base + incl - v;
+}
+
+// One warp's exclusive prefix over n <= 96 counters, in place; each result plus `base` also to
+// off[i].  (run and off: shared and global.)
+__device__ __forceinline__ void warp_offsets(int* run, int n, int base, int32_t* off) {
+  const int lane = threadIdx.x & 31;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + lane;
+    const int v = i < n ? run[i] : 0;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (i < n) {
+      run[i] = base + incl - v;
+      off[i] = base + incl - v;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  __syncwarp();
+}
+
+// Places one warp's pairs of up to 32 tokens in token order (lane = token; chosen: it chose
+// the expert): run[a] is the next free place of adapter a.
+__device__ __forceinline__ void place32(const RsParams& p, bool chosen, int t, int a, int e, int* run) {
+  const int lane = threadIdx.x & 31;
+  const unsigned peers = __match_any_sync(0xffffffffu, chosen ? a : 128 + lane);
+  const unsigned before = peers & ((1u << lane) - 1u);
+  if (chosen) p.sorted_pairs[run[a] + __popc(before)] = t * p.k + slot_of_expert(p.topk_ids, t, p.k, e);
+  __syncwarp();
+  if (chosen && before == 0u) run[a] += __popc(peers);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ logits, choice, weights
+template <int NI>
+__global__ void __launch_bounds__(kRsThreads, 1)
+    route_scored_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw,
+                        const RsParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ RsCore sm;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = p.C, TC = 128 / C;
+  const int rank = static_cast<int>(blockIdx.x) % C, tile = static_cast<int>(blockIdx.x) / C;
+  const int t0 = tile * 128, own0 = rank * TC;
+  const int pitch = p.epad + 4;  // floats: rows 16-byte aligned, neighbours 4 banks apart
+  const bool given = p.logits_in != nullptr;
+  // logits: the tile's partial sums [128][pitch], or a row per warp of given ones
+  float* part = reinterpret_cast<float*>(ring);
+  double* scratch = reinterpret_cast<double*>(ring + static_cast<size_t>(given ? kRsWarps : 128) * pitch * 4) +
+                    warp * p.epad;
+  volatile int* abort_flag = &sm.abort_flag;
+  pdl_trigger();  // the sort of a large batch may be launched
+
+  if (tid == 0) {
+    sm.abort_flag = 0;
+    sm.flag = kRsClean;
+    if (!given) {
+      for (int s = 0; s < p.stages; ++s) {
+        mbar_init(&sm.full[s], 1);
+        mbar_init(&sm.empty[s], 1);
+      }
+      mbar_init(&sm.tfull, 1);
+      fence_mbarrier_init();
+      tma_prefetch_desc(&tmx);
+      tma_prefetch_desc(&tmw);
+    }
+  }
+  for (int i = tid; i < 256; i += kRsThreads) sm.map[i] = make_uint4(0u, 0u, 0u, 0u);
+  uint32_t cols = 32;
+  while (cols < static_cast<uint32_t>(p.epad)) cols <<= 1;
+  if (!given && warp == 1) tmem_alloc(&sm.tmem_base, cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  if (!given) {
+    const uint32_t tmem = sm.tmem_base;
+    const int nkb = (p.H + 63) / 64;
+    const int kb0 = static_cast<int>(static_cast<long long>(nkb) * rank / C);
+    const int kb1 = static_cast<int>(static_cast<long long>(nkb) * (rank + 1) / C);
+    const int stage_bytes = (128 + p.epad) * 128;
+    if (warp == 0) {
+      if (lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0, filled = 0, parity_of = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, nullptr, kFtWaitNs, 70)) break;
+          uint8_t* s = ring + stage * stage_bytes;
+          mbar_arrive_expect_tx(&sm.full[stage], static_cast<uint32_t>(stage_bytes));
+          tma_load_2d(s, &tmx, &sm.full[stage], kb * 64, t0);
+          tma_load_2d(s + 128 * 128, &tmw, &sm.full[stage], kb * 64, 0);
+          filled |= 1u << stage;
+          parity_of = (parity_of & ~(1u << stage)) | (phase << stage);
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (*abort_flag)  // let our own copies land before the ring is reused
+          for (int s = 0; s < p.stages; ++s)
+            if (filled & (1u << s)) {
+              volatile int dummy = 0;
+              mbar_wait(&sm.full[s], (parity_of >> s) & 1u, &dummy, nullptr, kFtWaitNs / 4, 0);
+            }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      if (lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        const uint32_t idesc = umma_idesc_bf16(128, p.epad);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&sm.full[stage], phase, abort_flag, nullptr, kFtWaitNs, 71)) break;
+          tc_fence_after();
+          const uint32_t s = smem_u32(ring + stage * stage_bytes);
+          const uint64_t ad = umma_desc_sw128(s), bd = umma_desc_sw128(s + 128 * 128);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) umma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
+          umma_commit(&sm.empty[stage]);
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        umma_commit(&sm.tfull);
+        volatile int dummy = 0;
+        mbar_wait(&sm.tfull, 0, &dummy, nullptr, kFtWaitNs, 0);
+      }
+      __syncwarp();
+    }
+    __syncthreads();  // the ring is idle
+    tc_fence_after();
+    // accumulator -> partial sums: warps of a lane quarter take every fourth run of 32 experts
+    const int q4 = warp & 3, m = q4 * 32 + lane;
+    for (int c0 = (warp >> 2) * 32; c0 < p.epad; c0 += kRsWarps / 4 * 32) {
+      float v[32];
+      tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q4 * 32) << 16) + c0, v);
+      if (kb1 == kb0) {  // no K block of its own: nothing was accumulated
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        if (c0 + j < p.epad)
+          *reinterpret_cast<float4*>(part + m * pitch + c0 + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    }
+    tc_fence_before();
+    if (C > 1) cluster_sync_all();
+    else __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, cols);
+    // own tokens: the sum over the cluster in rank order, in place (no peer reads these rows)
+    const int e4 = p.epad / 4;
+    if (C > 1 || p.bias != nullptr || p.logits_out != nullptr)
+      for (int i = tid; i < TC * e4; i += kRsThreads) {
+        const int row = own0 + i / e4, e = (i % e4) * 4;
+        float* at = part + row * pitch + e;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < C; ++c) {
+          const float4 v = ld_cluster_f4(mapa_shared(smem_u32(at), static_cast<uint32_t>(c)));
+          s.x += v.x;
+          s.y += v.y;
+          s.z += v.z;
+          s.w += v.w;
+        }
+        const float o[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (e + j >= p.E) break;
+          const float l = o[j] + (p.bias != nullptr ? p.bias[e + j] : 0.f);
+          at[j] = l;
+          if (p.logits_out != nullptr && t0 + row < p.M) p.logits_out[static_cast<size_t>(t0 + row) * p.E + e + j] = l;
+        }
+      }
+    __syncthreads();
+  }
+
+  // ---- a warp per token
+  float sb[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+    sb[i] = p.score_bias != nullptr && lane + 32 * i < p.E ? p.score_bias[lane + 32 * i] : 0.f;
+  for (int i = warp; i < TC; i += kRsWarps) {
+    const int t = t0 + own0 + i;
+    if (t >= p.M) break;
+    const float* row = part + (own0 + i) * pitch;
+    if (given) {
+      float* mine = part + warp * pitch;
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+        if (lane + 32 * j < p.E) {
+          const float v = p.logits_in[static_cast<size_t>(t) * p.E + lane + 32 * j];
+          mine[lane + 32 * j] = v;
+          if (p.logits_out != nullptr) p.logits_out[static_cast<size_t>(t) * p.E + lane + 32 * j] = v;
+        }
+      row = mine;
+      __syncwarp();
+    }
+    float mx, sum;
+    bool bad = choose<NI>(row, p, sb, scratch, sm.ids[warp], mx, sum);
+    weigh(row, p, sm.ids[warp], t, mx, sum);
+    const int a = p.adapter_ids[t];
+    bad |= a < -1 || a >= p.L;
+    if (bad && lane == 0) atomicMin(&sm.flag, t);
+    const int b = own0 + i;  // the token's bit
+    for (int j = lane; j < p.k; j += 32)
+      atomicOr(reinterpret_cast<unsigned*>(sm.map + sm.ids[warp][j]) + (b >> 5), 1u << (b & 31));
+    __syncwarp();
+  }
+  __syncthreads();
+  if (tid == 0 && *abort_flag) sm.flag = -1;
+
+  if (p.tiles > 1) {
+    // ---- for the sort: the chunk's bits and its pairs of lower experts
+    const int chunks = p.tiles * C, chunk = static_cast<int>(blockIdx.x);
+    int n = 0;
+    uint4 m = make_uint4(0u, 0u, 0u, 0u);
+    if (tid < p.E) {
+      m = sm.map[tid];
+      n = __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
+    }
+    const int before = block_prefix(n, sm.scan);
+    if (tid < p.E) {
+      p.before[static_cast<size_t>(tid) * chunks + chunk] = before;
+      uint16_t* dst = p.bitmap + static_cast<size_t>(tid) * p.tiles * 8 + tile * 8 + own0 / 16;
+      const uint32_t w[4] = {m.x, m.y, m.z, m.w};
+      if (TC == 128) {
+        *reinterpret_cast<uint4*>(dst) = m;
+      } else if (TC == 64) {
+        *reinterpret_cast<uint2*>(dst) = rank == 0 ? make_uint2(m.x, m.y) : make_uint2(m.z, m.w);
+      } else if (TC == 32) {
+        *reinterpret_cast<uint32_t*>(dst) = w[0] | w[1] | w[2] | w[3];  // one of them is this CTA's
+      } else {
+        const uint32_t v = w[0] | w[1] | w[2] | w[3];
+        *dst = static_cast<uint16_t>(v | v >> 16);
+      }
+    }
+    if (tid == 0) p.flags[chunk] = sm.flag;
+    if (C > 1) cluster_sync_all();  // the peers have read this CTA's partial sums
+    return;
+  }
+
+  // ---- up to 128 tokens: the cluster sorts, a warp per expert
+  int* run = reinterpret_cast<int*>(scratch);            // next place by adapter, of this warp
+  int* s_base = reinterpret_cast<int*>(sm.ids);          // pairs of lower experts (the ids are done)
+  uint8_t* s_ad = reinterpret_cast<uint8_t*>(sm.ids) + 1024;  // adapters of the tokens
+  cluster_sync_all();
+  uint4 m = make_uint4(0u, 0u, 0u, 0u);
+  int n = 0;
+  if (tid < p.E) {
+    for (int c = 0; c < C; ++c) {
+      const uint4 v = ld_cluster_u32x4(mapa_shared(smem_u32(sm.map + tid), static_cast<uint32_t>(c)));
+      m = make_uint4(m.x | v.x, m.y | v.y, m.z | v.z, m.w | v.w);
+    }
+    n = __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
+  }
+  if (rank == 0 && tid == 0) {  // the call's status word
+    int flag = kRsClean;
+    for (int c = 0; c < C; ++c)
+      flag = min(flag, ld_cluster_s32(mapa_shared(smem_u32(&sm.flag), static_cast<uint32_t>(c))));
+    p.status[0] = flag == kRsClean ? MOE_LORA_OK : flag < 0 ? MOE_LORA_ERR_TIMEOUT : MOE_LORA_ERR_DEVICE_CHECK;
+    p.status[1] = flag == kRsClean || flag < 0 ? 0 : flag;
+  }
+  cluster_sync_all();  // every peer has read the maps
+  const int base = block_prefix(n, sm.scan);
+  if (tid < 256) {
+    s_base[tid] = base;
+    sm.map[tid] = m;
+  }
+  if (tid < 128) {
+    const int a = tid < p.M ? p.adapter_ids[tid] : -1;
+    s_ad[tid] = static_cast<uint8_t>(a >= 0 && a < p.L ? a : p.L);
+  }
+  __syncthreads();
+  const int LA = p.L + 1;
+  for (int e = rank * kRsWarps + warp; e < p.E; e += C * kRsWarps) {
+    const unsigned* w = reinterpret_cast<const unsigned*>(sm.map + e);
+    for (int a = lane; a < LA; a += 32) run[a] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (w[q] >> lane & 1u) atomicAdd(run + s_ad[q * 32 + lane], 1);
+    __syncwarp();
+    warp_offsets(run, LA, s_base[e], p.seg_offsets + e * LA);
+    for (int q = 0; q < 4; ++q)
+      if (w[q] != 0u) place32(p, w[q] >> lane & 1u, q * 32 + lane, s_ad[q * 32 + lane], e, run);
+  }
+  if (rank == 0 && tid == 0) p.seg_offsets[p.E * LA] = p.M * p.k;
+}
+
+// ------------------------------------------------------------------ sort of large batches
+// A CTA per expert; its warps split the expert's words of 32 tokens and compact the set bits
+// of 32 words at a time into a list, so that sparse experts cost loads for their own pairs
+// only.  Two walks: count by adapter, then place in token order.
+__global__ void __launch_bounds__(kRsThreads) route_scored_sort_kernel(const RsParams p) {
+  __shared__ int s_scan[kRsWarps];
+  __shared__ int s_run[kRsWarps][65];
+  __shared__ int s_off[65];
+  __shared__ uint16_t s_list[kRsWarps][1024];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int e = blockIdx.x, LA = p.L + 1;
+  const int words = p.tiles * 4, chunks = p.tiles * p.C;
+  for (int i = tid; i < kRsWarps * 65; i += kRsThreads) (&s_run[0][0])[i] = 0;
+  pdl_wait();
+  // pairs of lower experts
+  int part = 0;
+  for (int c = tid; c < chunks; c += kRsThreads) part += p.before[static_cast<size_t>(e) * chunks + c];
+  part = __reduce_add_sync(0xffffffffu, part);
+  if (lane == 0) s_scan[warp] = part;
+  if (e == 0 && warp == 0) {  // the call's status word
+    int flag = kRsClean;
+    for (int c = lane; c < chunks; c += 32) flag = min(flag, p.flags[c]);
+    flag = __reduce_min_sync(0xffffffffu, flag);
+    if (lane == 0) {
+      p.status[0] = flag == kRsClean ? MOE_LORA_OK : flag < 0 ? MOE_LORA_ERR_TIMEOUT : MOE_LORA_ERR_DEVICE_CHECK;
+      p.status[1] = flag == kRsClean || flag < 0 ? 0 : flag;
+    }
+  }
+  const uint32_t* map = reinterpret_cast<const uint32_t*>(p.bitmap) + static_cast<size_t>(e) * words;
+  // each warp's words, whole runs of 32
+  const int runs = (words + 31) / 32;
+  const int r0 = static_cast<int>(static_cast<long long>(runs) * warp / kRsWarps);
+  const int r1 = static_cast<int>(static_cast<long long>(runs) * (warp + 1) / kRsWarps);
+  uint16_t* list = s_list[warp];
+  int n = 0;
+  auto compact = [&](int r) {  // the run's tokens, relative to its first, in order
+    uint32_t w = r * 32 + lane < words ? map[r * 32 + lane] : 0u;
+    const int c = __popc(w);
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    n = __shfl_sync(0xffffffffu, incl, 31);
+    __syncwarp();
+    for (int at = incl - c; w != 0u; ++at, w &= w - 1u) list[at] = static_cast<uint16_t>(lane * 32 + __ffs(w) - 1);
+    __syncwarp();
+  };
+  auto adapter = [&](int t) -> int {
+    const int a = p.adapter_ids[t];
+    return a >= 0 && a < p.L ? a : p.L;
+  };
+  __syncthreads();
+  int base = 0;
+#pragma unroll
+  for (int w = 0; w < kRsWarps; ++w) base += s_scan[w];
+  for (int r = r0; r < r1; ++r) {
+    compact(r);
+    for (int i = lane; i < n; i += 32) atomicAdd(&s_run[warp][adapter(r * 1024 + list[i])], 1);
+  }
+  __syncthreads();
+  if (tid < LA) {  // counts of the expert by adapter; s_run: the warps' exclusive prefix
+    int acc = 0;
+#pragma unroll
+    for (int w = 0; w < kRsWarps; ++w) {
+      const int c = s_run[w][tid];
+      s_run[w][tid] = acc;
+      acc += c;
+    }
+    s_off[tid] = acc;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    warp_offsets(s_off, LA, base, p.seg_offsets + e * LA);
+    if (e == p.E - 1 && lane == 0) p.seg_offsets[p.E * LA] = p.M * p.k;
+  }
+  __syncthreads();
+  for (int a = lane; a < LA; a += 32) s_run[warp][a] += s_off[a];
+  __syncwarp();
+  for (int r = r0; r < r1; ++r) {
+    if (r1 - r0 > 1) compact(r);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const bool in = i0 + lane < n;
+      const int t = in ? r * 1024 + list[i0 + lane] : 0;
+      place32(p, in, t, in ? adapter(t) : 0, e, s_run[warp]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host
+// CTAs per tile of 128 tokens: as many as keep one CTA per SM, 8 at most.
+constexpr int kRsSms = 148;
+
+static int scored_split(int M) {
+  const int tiles = (M + 127) / 128;
+  int C = 8;
+  while (C > 1 && tiles * C > kRsSms) C /= 2;
+  return C;
+}
+
+void route_scored_scratch(int M, int E, size_t* bitmap, size_t* before, size_t* flags) {
+  const size_t tiles = (static_cast<size_t>(M) + 127) / 128;
+  const size_t chunks = std::max<size_t>(tiles, std::min<size_t>(8 * tiles, kRsSms));  // or more: grows with M
+  *bitmap = tiles > 1 ? E * tiles * 16 : 0;
+  *before = tiles > 1 ? E * chunks * 4 : 0;
+  *flags = tiles > 1 ? chunks * 4 : 0;
+}
+
+template <int NI>
+static cudaError_t launch_choice(const RsParams& p, const CUtensorMap& tmx, const CUtensorMap& tmw, cudaStream_t st) {
+  const int pitch = p.epad + 4;
+  const size_t rows = p.logits_in ? kRsWarps : 128;
+  size_t body = rows * pitch * 4 + static_cast<size_t>(kRsWarps) * p.epad * 8;
+  if (!p.logits_in) body = std::max(body, static_cast<size_t>(p.stages) * (128 + p.epad) * 128);
+  static std::atomic<bool> attr_set[kMaxDevices];
+  const int dev = current_device_index();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(route_scored_kernel<NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               1024 + kRsRing);
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  ProfScope ps(K_ROUTE_SCORED, st);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.tiles * p.C);
+  cfg.blockDim = dim3(kRsThreads);
+  cfg.dynamicSmemBytes = 1024 + body;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, route_scored_kernel<NI>, tmx, tmw, p);
+  count_launch();
+  return e;
+}
+
+cudaError_t launch_route_scored(const RouteScoredArgs& a, cudaStream_t st) {
+  if (a.M == 0) {
+    const cudaError_t e = cudaMemsetAsync(a.status, 0, 8, st);
+    return e != cudaSuccess ? e : cudaMemsetAsync(a.seg_offsets, 0, sizeof(int32_t) * (a.E * (a.L + 1) + 1), st);
+  }
+  RsParams p{};
+  p.logits_in = a.logits_in;
+  p.bias = a.bias;
+  p.score_bias = a.score_bias;
+  p.adapter_ids = a.adapter_ids;
+  p.logits_out = a.logits_out;
+  p.topk_ids = a.topk_ids;
+  p.topk_w = a.topk_w;
+  p.sorted_pairs = a.sorted_pairs;
+  p.seg_offsets = a.seg_offsets;
+  p.bitmap = a.bitmap;
+  p.before = a.before;
+  p.flags = a.flags;
+  p.status = a.status;
+  p.M = a.M;
+  p.H = a.H;
+  p.E = a.E;
+  p.k = a.k;
+  p.L = a.L;
+  p.C = scored_split(a.M);
+  p.tiles = (a.M + 127) / 128;
+  p.epad = std::max(48, (a.E + 15) / 16 * 16);  // (the sort's 65 counters fit a warp's doubles)
+  p.stages = std::min(kRsMaxStages, kRsRing / ((128 + p.epad) * 128));
+  p.f = a.f;
+  CUtensorMap tmx{}, tmw{};
+  if (a.logits_in == nullptr &&
+      (encode_tmap_2d(&tmx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.H, a.M, static_cast<uint64_t>(a.H) * 2, 64, 128,
+                      CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+       encode_tmap_2d(&tmw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.w_router, a.H, a.E, static_cast<uint64_t>(a.H) * 2, 64,
+                      p.epad, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS))
+    return cudaErrorInvalidValue;
+  cudaError_t e = a.E <= 64    ? launch_choice<2>(p, tmx, tmw, st)
+                  : a.E <= 128 ? launch_choice<4>(p, tmx, tmw, st)
+                               : launch_choice<8>(p, tmx, tmw, st);
+  if (e != cudaSuccess || p.tiles == 1) return e != cudaSuccess ? e : cudaGetLastError();
+  ProfScope ps(K_SORT, st);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.E);
+  cfg.blockDim = dim3(kRsThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, route_scored_sort_kernel, p);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace mlb

@@ -73,12 +73,12 @@ def test_dense_no_tokens_is_ok():
 
 
 def test_workspace_sizes():
-    assert ml.workspace_size(ml.OP_ROUTE_SCORED, 64, 0, 0, 64, 8, 8, 0) >= 256 + 64 * 4
+    assert ml.workspace_size(ml.OP_ROUTE_SCORED, 1000, 0, 0, 64, 8, 8, 0) >= 256 + 64 * 1000 // 8
     assert ml.workspace_size(ml.OP_DENSE_FUSED, 64, 4096, 512, 1, 1, 4, 16) >= 256 + 64 * 16 * 2
     assert ml.workspace_size(ml.OP_DENSE_FUSED, -1) == 0
     # grows with the batch, so a workspace made for the largest batch serves every smaller one
     for op, args in ((ml.OP_ROUTE_SCORED, (1024, 0, 128, 8, 16, 0)), (ml.OP_DENSE_FUSED, (1024, 512, 1, 1, 4, 16))):
-        sizes = [ml.workspace_size(op, M, *args) for M in (1, 2, 63, 64, 65, 128, 129, 1000, 4096)]
+        sizes = [ml.workspace_size(op, M, *args) for M in (1, 2, 63, 64, 65, 128, 129, 1000, 2304, 2305, 4096, 9472, 9473)]
         assert sizes == sorted(sizes)
 
 

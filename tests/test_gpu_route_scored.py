@@ -247,3 +247,33 @@ def test_every_token_on_one_expert():
     lg = np.random.default_rng(2).standard_normal((M, E)).astype(np.float32)
     lg[:, 17] = 9
     _check(M, E, k, L, 3, lg=lg, score="sigmoid")
+
+
+@pytest.mark.parametrize("M", [1, 16, 127, 128, 129, 2049])
+@pytest.mark.parametrize("E,L", [(3, 64), (33, 64), (256, 64), (256, 0)])
+def test_every_adapter_and_expert_count(M, E, L):
+    """Both sides of the one-launch limit, with as many adapters as there can be."""
+    _check(M, E, min(E, 3), L, M + E + L, score="sigmoid",
+           score_bias=np.random.default_rng(E).standard_normal(E).astype(np.float32) * 0.05)
+
+
+def test_rows_of_nan_without_renormalisation():
+    lg = np.random.default_rng(1).standard_normal((200, 12)).astype(np.float32)
+    lg[7] = np.nan
+    for M in (20, 200):
+        for score in ("softmax", "sigmoid"):
+            res = _check(M, 12, 3, 2, 1, lg=lg[:M], score=score, renormalize=False, status=False)
+            with pytest.raises(ml.MoELoRAError):
+                ml.check_status(res["workspace"])
+
+
+@pytest.mark.parametrize("M", [40, 700])
+def test_huge_biases_of_both_signs(M):
+    """Group sums whose terms cancel, and experts a bias rules out or forces."""
+    g = np.random.default_rng(5)
+    lg = g.standard_normal((M, 32)).astype(np.float32)
+    b = (g.standard_normal(32) * 0.05).astype(np.float32)
+    b[[1, 9, 17]], b[[2, 10, 30]] = 3e6, -3e6
+    for rule in ("max", "top2"):
+        _check(M, 32, 5, 3, 2, lg=lg, score="sigmoid", score_bias=b, n_group=4, topk_group=3, group_rule=rule)
+        _check(M, 32, 5, 3, 2, lg=lg, score="softmax", score_bias=b, n_group=8, topk_group=3, group_rule=rule)
