@@ -8,8 +8,9 @@
 // One kernel makes logits, choice and weights: a cluster of C CTAs takes 128 tokens x all E
 // experts (one tcgen05 tile: tokens in M, experts in N), splits H, and each CTA adds up the
 // partial logits of 128 / C tokens from its peers' shared memory in rank order; its warps
-// then choose those tokens' experts, a warp per token, the logits never leaving the SM.  x
-// is read once, W_r once per 128 tokens (from L2).
+// then choose those tokens' experts, a warp per token, the logits never leaving the SM.
+// Batches that fill the SMs with 128 tokens each are bound by what the SMs read (x once, W_r
+// once per tile): there two CTAs share 256 tokens, each over half of H.
 //
 // The sort needs no atomics on global memory: a CTA leaves one bit per (expert, token) and
 // the running count of its pairs by expert.  Up to 128 tokens the cluster itself sorts (a
@@ -43,7 +44,11 @@ struct RsParams {
   int32_t* before;   // [E][chunks]: the chunk's pairs of lower experts
   int32_t* flags;    // [chunks]: what the chunk has to report (kRsClean: nothing)
   int* status;
-  int M, H, E, k, L, C, tiles, epad, stages;
+  int M, H, E, k, L;
+  int tiles;  // of 128 tokens
+  int C;      // CTAs that share a tile's tokens
+  int wide;   // two CTAs make the logits of two tiles, then take one each (C = 1)
+  int epad, stages;
   ScoreFormat f;
 };
 
@@ -62,7 +67,7 @@ struct RsCore {
 // ------------------------------------------------------------------ the choice of one token
 __device__ __forceinline__ float clamp_finite(float v) { return fminf(fmaxf(v, -FLT_MAX), FLT_MAX); }
 
-// Order-preserving unsigned key of a finite float, at least 0x00800000; both zeros alike.
+// Order-preserving unsigned key of a finite float; both zeros alike.
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t b = __float_as_uint(v + 0.f);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
@@ -70,16 +75,69 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 __device__ __forceinline__ float key_value(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
 }
-constexpr uint32_t kNanKey = 1u;  // below every number, above "not a candidate" (0)
+__device__ __forceinline__ float warp_max(float v) { return key_value(__reduce_max_sync(0xffffffffu, order_key(v))); }
 
-// True if fp32 selection scores prove a > b.  A score is off by at most 2^-20 (exponential:
-// 2 + 1.17 |d| steps of 2^-23 of a value e^-|d| at most; the sum's and the quotient's roundings), a sum
-// of two by 2^-19; the add of a bias rounds to 2^-24 of the result.
-__device__ __forceinline__ bool surely_above(uint32_t a, uint32_t b) {
-  if (b <= kNanKey) return a > b;
-  const float x = key_value(a), y = key_value(b);
-  return x - y > 0x1p-18f + 0x1p-21f * (fabsf(x) + fabsf(y));
+// Selection scores as 24-bit fixed point q, so that q and the expert fit one word whose
+// warp-wide maximum is one instruction, equal q going to the lower expert.
+//   0 not a candidate, kQNan NaN, kQLow / kQHigh beyond the range, else kQMin + (v - lo) scale
+// An order is proved where q differs by more than `slack` (or the lower one is NaN); what is
+// not proved is decided in 64 bits.  Logits compared as such: every step is monotone, so any
+// difference of q is a proof.
+constexpr uint32_t kQNan = 1u, kQLow = 2u, kQHigh = (1u << 24) - 2u, kQMin = 8u;
+constexpr float kQSpan = 16777200.f;  // 2^24 - 16
+constexpr float kBiasMost = 1024.f;   // larger biases leave the fixed-point range
+constexpr float kLogitSpan = 32.f;    // logits further below the largest are kQLow
+
+__device__ __forceinline__ bool proved(uint32_t above, uint32_t below, uint32_t slack) {
+  return below <= kQNan || above > below + slack;
 }
+
+// What the choice needs of the call, by lane (experts lane, lane + 32, ...).
+template <int NI>
+struct ChoiceSetup {
+  float sb[NI];        // selection bias
+  int group_lane[NI];  // first lane of the expert's group (groups take `per` lanes each)
+  int per;
+  float lo, scale;     // of fixed-point scores
+  uint32_t slack;      // difference of q that proves an order of scores
+  bool exact;          // every token in 64 bits
+
+  __device__ __forceinline__ void make(const RsParams& p) {
+    const int lane = threadIdx.x & 31;
+    per = 32;
+    while (per > 1 && per * p.f.n_group > 32) per >>= 1;
+    exact = p.f.n_group > 32;
+    float bmin = FLT_MAX, bmax = -FLT_MAX;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int e = lane + 32 * i;
+      const bool in = e < p.E;
+      sb[i] = in && p.score_bias != nullptr ? p.score_bias[e] : 0.f;
+      group_lane[i] = in && !exact ? e / p.f.group_size * per : 0;
+      const float b = fabsf(sb[i]);
+      if (in && b <= kBiasMost) {
+        bmin = fminf(bmin, sb[i]);
+        bmax = fmaxf(bmax, sb[i]);
+      }
+      // (a score is at most 1: a bias between the range and 2 beyond it might cross over)
+      exact |= in && b > kBiasMost && b < kBiasMost + 2.f;
+    }
+    exact = __any_sync(0xffffffffu, exact);
+    bmin = -warp_max(-bmin);
+    bmax = warp_max(bmax);
+    if (bmin > bmax) bmin = bmax = 0.f;
+    lo = bmin;
+    const float range = 1.f + (bmax - bmin);
+    scale = kQSpan / range;
+    // Error of a selection score in 2^-24: a sigmoid's exponential (2 ulp), sum and quotient 3;
+    // a softmax's exponential and its argument 5, the sum of up to 256 of them (4 each, 13
+    // roundings) 17, quotient and product 3; the add of the bias |c|; then (c - lo) scale and
+    // its floor, the range each.  Two scores, in units of range 2^-24.
+    const float most = fmaxf(fabsf(bmin), fabsf(bmax + 1.f));
+    slack = static_cast<uint32_t>(2.f * ((p.f.sigmoid ? 3.f : 25.f) + most + 3.f * range) / range) + 2u;
+    if (p.f.by_logit) slack = 0u;
+  }
+};
 
 __device__ __forceinline__ void warp_argmax(double& v, int& e) {
 #pragma unroll
@@ -93,6 +151,52 @@ __device__ __forceinline__ void warp_argmax(double& v, int& e) {
   }
 }
 
+// Scores in 64 bits.
+__device__ __forceinline__ float row_max(const float* row, int E) {
+  float mx = -FLT_MAX;
+  for (int e = threadIdx.x & 31; e < E; e += 32)
+    if (row[e] == row[e]) mx = fmaxf(mx, clamp_finite(row[e]));
+  return warp_max(mx);
+}
+
+__device__ __forceinline__ double exact_sum(const float* row, int E, float mx) {
+  double sum = 0.0;
+  for (int e = threadIdx.x & 31; e < E; e += 32)
+    if (row[e] == row[e]) sum += exp(static_cast<double>(clamp_finite(row[e])) - mx);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+__device__ __forceinline__ double exact_score(float logit, int sigmoid, float mx, double sum) {
+  const double l = clamp_finite(logit);
+  const double x = exp(sigmoid ? -l : l - mx);
+  return sigmoid ? 1.0 / (1.0 + x) : x / sum;
+}
+
+__device__ __forceinline__ double exact_selection(const float* row, const RsParams& p, int e, float mx, double sum) {
+  const float b = p.score_bias ? p.score_bias[e] : 0.f;
+  if (row[e] != row[e] || b != b) return -INFINITY;
+  if (p.f.by_logit) return static_cast<double>(clamp_finite(row[e]));
+  return exact_score(row[e], p.f.sigmoid, mx, sum) + static_cast<double>(clamp_finite(b));
+}
+
+// Up to 32 candidates, lane j holding expert e of the j-th (n of them): the first k in 64 bits.
+__device__ __noinline__ void order_candidates(const float* row, const RsParams& p, int e, int n, uint8_t* ids) {
+  const int lane = threadIdx.x & 31;
+  const float mx = p.f.sigmoid || p.f.by_logit ? 0.f : row_max(row, p.E);
+  const double sum = p.f.sigmoid || p.f.by_logit ? 1.0 : exact_sum(row, p.E, mx);
+  const double c = lane < n ? exact_selection(row, p, e, mx, sum) : 0.0;
+  int rank = 0;
+  for (int i = 0; i < n; ++i) {
+    const double o = __shfl_sync(0xffffffffu, c, i);
+    const int oe = __shfl_sync(0xffffffffu, e, i);
+    rank += (o > c || (o == c && oe < e)) ? 1 : 0;
+  }
+  if (lane < n && rank < p.k) ids[rank] = static_cast<uint8_t>(e);
+  __syncwarp();
+}
+
 // The definition in 64 bits: for tokens whose 32-bit scores lie too close to prove an order.
 // Lane l holds experts l, l + 32, ...; c: 256 doubles of the warp.
 template <int NI>
@@ -102,29 +206,9 @@ __device__ __noinline__ void choose_exact(const float* row, const RsParams& p, d
   const ScoreFormat& f = p.f;
   unsigned alive = 0u;
   float mx = -FLT_MAX;
-  for (int i = 0; i < NI; ++i) {
-    const int e = lane + 32 * i;
-    if (e < E) {
-      alive |= 1u << i;
-      if (row[e] == row[e]) mx = fmaxf(mx, clamp_finite(row[e]));
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  double sum = 1.0;
-  if (!f.sigmoid) {
-    sum = 0.0;
-    for (int i = 0; i < NI; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E && row[e] == row[e]) sum += exp(static_cast<double>(clamp_finite(row[e])) - mx);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  }
-  auto score = [&](int e) -> double {
-    const double l = clamp_finite(row[e]);
-    return f.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - mx) / sum;
-  };
+  if (!f.sigmoid) mx = row_max(row, E);
+  const double sum = f.sigmoid ? 1.0 : exact_sum(row, E, mx);
+  auto score = [&](int e) -> double { return exact_score(row[e], f.sigmoid, mx, sum); };
   auto bias = [&](int e) -> double { return p.score_bias ? static_cast<double>(clamp_finite(p.score_bias[e])) : 0.0; };
   double c[NI];
 #pragma unroll
@@ -132,8 +216,8 @@ __device__ __noinline__ void choose_exact(const float* row, const RsParams& p, d
     const int e = lane + 32 * i;
     c[i] = -INFINITY;
     if (e >= E) continue;
-    const bool nan = row[e] != row[e] || (p.score_bias && p.score_bias[e] != p.score_bias[e]);
-    if (!nan) c[i] = f.by_logit ? static_cast<double>(clamp_finite(row[e])) : score(e) + bias(e);
+    alive |= 1u << i;
+    c[i] = exact_selection(row, p, e, mx, sum);
     c_of[e] = c[i];
   }
   __syncwarp();
@@ -202,37 +286,36 @@ __device__ __noinline__ void choose_exact(const float* row, const RsParams& p, d
 }
 
 // The k experts of the token whose logits are row[0, E), in order, into ids; returns whether
-// a NaN was met.  Selection scores in fp32 as order-preserving keys; every order that decides
-// (between the chosen, to the first one left out, between kept and dropped groups) has to be
-// wider than the scores' error, else the token is done again in 64 bits.  Logits compared as
-// such need no proof.  scratch: a double of the warp per expert.
+// a NaN was met.  Also the row's largest logit and the sum of its exponentials (softmax).
+// scratch: a double of the warp per expert.
 template <int NI>
-__device__ __forceinline__ bool choose(const float* row, const RsParams& p, const float (&sb)[NI], double* scratch,
-                                       uint8_t* ids, float& mx_out, float& sum_out) {
+__device__ __forceinline__ bool choose(const float* row, const RsParams& p, const ChoiceSetup<NI>& cs, float* copy_to,
+                                       double* scratch, uint8_t* ids, float& mx, float& sum) {
   const int lane = threadIdx.x & 31;
   const int E = p.E;
   const ScoreFormat& f = p.f;
   float l[NI];
-  uint32_t key[NI];
-  bool bad = false;
+  uint32_t key[NI];  // q and 255 - expert
+  bool nan[NI], bad = false;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int e = lane + 32 * i;
     const float v = e < E ? row[e] : -FLT_MAX;
-    const bool nan = v != v;
-    bad |= nan || sb[i] != sb[i];
-    l[i] = nan ? -FLT_MAX : clamp_finite(v);
-    key[i] = e < E ? (nan || sb[i] != sb[i] ? kNanKey : order_key(l[i])) : 0u;
+    if (copy_to != nullptr && e < E) copy_to[e] = v;
+    nan[i] = v != v;
+    l[i] = nan[i] ? -FLT_MAX : clamp_finite(v);
+    nan[i] |= cs.sb[i] != cs.sb[i];
+    bad |= nan[i];
   }
-  const bool need_sum = !f.sigmoid && !(f.by_logit && f.renorm);
-  float mx = -FLT_MAX, sum = 1.f;
-  if (!f.sigmoid) {
+  mx = -FLT_MAX;
+  sum = 1.f;
+  if (!f.sigmoid || f.by_logit) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) mx = fmaxf(mx, l[i]);
-    mx = key_value(__reduce_max_sync(0xffffffffu, order_key(mx)));
+    mx = warp_max(mx);
   }
-  float s[NI];
-  if (need_sum) {
+  if (!f.sigmoid && !(f.by_logit && f.renorm)) {
+    float s[NI];
     sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -241,35 +324,48 @@ __device__ __forceinline__ bool choose(const float* row, const RsParams& p, cons
       sum += s[i];
     }
     sum = warp_sum(sum);
-  }
-  mx_out = mx;
-  sum_out = sum;
-  bool exact = f.n_group > 32;
-  if (!f.by_logit) {
-    const float inv = 1.f / sum;
+    if (!f.by_logit) {
+      const float inv = 1.f / sum;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const float v = f.sigmoid ? __fdividef(1.f, 1.f + __expf(-l[i])) : s[i] * inv;
-      if (key[i] > kNanKey) key[i] = order_key(clamp_finite(v + clamp_finite(sb[i])));
+      for (int i = 0; i < NI; ++i) l[i] = s[i] * inv;
     }
+  } else if (!f.by_logit) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) l[i] = 1.f / (1.f + expf(-l[i]));
   }
+  // (l: the logits, or the scores)
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int e = lane + 32 * i;
+    uint32_t q;
+    if (f.by_logit) {
+      const float d = l[i] - (mx - kLogitSpan);
+      q = d < 0.f ? kQLow : kQMin + static_cast<uint32_t>(d * (kQSpan / kLogitSpan));
+    } else {
+      q = kQMin + static_cast<uint32_t>(fmaxf(l[i] + cs.sb[i] - cs.lo, 0.f) * cs.scale);
+      if (fabsf(cs.sb[i]) > kBiasMost) q = cs.sb[i] < 0.f ? kQLow : kQHigh;
+    }
+    if (nan[i]) q = kQNan;
+    key[i] = e < E ? min(q, kQHigh) << 8 | static_cast<uint32_t>(255 - e) : 0u;
+  }
+  bool exact = cs.exact;
   if (f.n_group > 1 && !exact) {
     uint32_t* keys = reinterpret_cast<uint32_t*>(scratch);
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-      if (lane + 32 * i < E) keys[lane + 32 * i] = key[i];
+      if (lane + 32 * i < E) keys[lane + 32 * i] = key[i] >> 8;
     __syncwarp();
     // `per` lanes per group walk its experts, starting at different places so that the lanes
     // stay on different banks, and join their two largest
-    int per = 32;
-    while (per * f.n_group > 32) per >>= 1;
-    const int g = lane / per, sub = lane % per;
+    const int per = cs.per, g = lane / per, sub = lane & (per - 1);
     uint32_t m1 = 0u, m2 = 0u;
     if (g < f.n_group) {
       const int cnt = (f.group_size - sub + per - 1) / per;
+      const uint32_t* mine = keys + g * f.group_size + sub;
       int j = cnt > 0 ? g % cnt : 0;
+#pragma unroll 4
       for (int n = 0; n < cnt; ++n) {
-        const uint32_t v = keys[g * f.group_size + sub + j * per];
+        const uint32_t v = mine[j * per];
         m2 = max(m2, min(m1, v));
         m1 = max(m1, v);
         j = j + 1 == cnt ? 0 : j + 1;
@@ -280,62 +376,59 @@ __device__ __forceinline__ bool choose(const float* row, const RsParams& p, cons
       m2 = max(max(m2, a2), min(m1, a1));
       m1 = max(m1, a1);
     }
-    uint32_t gk = m1;
+    uint32_t gk = m1, slack = cs.slack;
     if (f.top2 && f.group_size > 1) {
-      if (m2 <= kNanKey) {
-        gk = kNanKey;
-      } else {
-        const float a = key_value(m1), b = key_value(m2);
-        exact |= g < f.n_group && fabsf(a) + fabsf(b) > 0x1p20f;  // (its error is that of the terms)
-        gk = order_key(clamp_finite(a + b));
-      }
+      // (sums with a member beyond the range say nothing)
+      exact = __any_sync(0xffffffffu, g < f.n_group && (m1 >= kQHigh || m2 == kQLow));
+      gk = m2 <= kQNan ? kQNan : m1 + m2;
+      slack *= 2u;
     }
-    // rank among the groups: how many are larger, or as large and before
+    gk = gk << 5 | static_cast<uint32_t>(31 - g);
+    const bool in = g < f.n_group;
     int rank = 0;
-    for (int h = 0; h < f.n_group; ++h) {
-      const uint32_t o = __shfl_sync(0xffffffffu, gk, h * per);
-      rank += (o > gk || (o == gk && h < g)) ? 1 : 0;
-    }
-    const bool in = g < f.n_group, kept = in && rank < f.topk_group;
-    if (!f.by_logit) {
-      const uint32_t lo = __reduce_min_sync(0xffffffffu, kept ? gk : 0xffffffffu);
-      const uint32_t hi = __reduce_max_sync(0xffffffffu, in && !kept ? gk : 0u);
-      exact |= !surely_above(lo, hi);
-    }
+#pragma unroll 4
+    for (int h = 0; h < f.n_group; ++h) rank += __shfl_sync(0xffffffffu, gk, h * per) > gk ? 1 : 0;
+    const bool kept = in && rank < f.topk_group;
+    const uint32_t last = __reduce_min_sync(0xffffffffu, kept ? gk : 0xffffffffu);
+    const uint32_t first = __reduce_max_sync(0xffffffffu, in && !kept ? gk : 0u);
+    exact |= !proved(last >> 5, first >> 5, slack);
     const unsigned keep = __ballot_sync(0xffffffffu, kept);
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E && !(keep >> (e / f.group_size * per) & 1u)) key[i] = 0u;
-    }
-    exact = __any_sync(0xffffffffu, exact);
+    for (int i = 0; i < NI; ++i)
+      if (!(keep >> cs.group_lane[i] & 1u)) key[i] = 0u;
   }
   if (!exact) {
     uint32_t prev = 0u;
-    // one more than k, to see the first one left out
-    const int rounds = f.by_logit ? p.k : p.k + 1;
-    for (int j = 0; j < rounds; ++j) {
-      uint32_t best = key[0], at = 0u;
+    int mine = 0;
+    bool open = false;  // an order that is not proved
+    auto next = [&]() -> uint32_t {
+      uint32_t m = key[0];
 #pragma unroll
-      for (int i = 1; i < NI; ++i)
-        if (key[i] > best) {
-          best = key[i];
-          at = i;
-        }
-      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-      if (!f.by_logit && j > 0 && !surely_above(prev, top)) {
-        exact = true;
-        break;
-      }
-      if (j == p.k) break;
+      for (int i = 1; i < NI; ++i) m = max(m, key[i]);
+      m = __reduce_max_sync(0xffffffffu, m);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) key[i] = key[i] == m ? 0u : key[i];
+      return m;
+    };
+    for (int j = 0; j < p.k; ++j) {
+      const uint32_t top = next();
+      open |= j > 0 && !proved(prev >> 8, top >> 8, cs.slack);
       prev = top;
-      const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? lane + 32u * at : 0xffffffffu);
-      if ((e & 31u) == static_cast<uint32_t>(lane)) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-          if (e >> 5 == static_cast<uint32_t>(i)) key[i] = 0u;
-      }
+      const int e = 255 - static_cast<int>(top & 255u);
+      mine = lane == j ? e : mine;
       if (lane == 0) ids[j] = static_cast<uint8_t>(e);
+    }
+    uint32_t top = next();  // the first one left out
+    open |= !proved(prev >> 8, top >> 8, cs.slack);
+    if (open) {  // with every expert that may belong to the first k
+      int n = p.k;
+      for (; n < 32 && !proved(prev >> 8, top >> 8, cs.slack); ++n) {
+        mine = lane == n ? 255 - static_cast<int>(top & 255u) : mine;
+        top = next();
+      }
+      exact = n > 32 || !proved(prev >> 8, top >> 8, cs.slack);
+      __syncwarp();
+      if (!exact) order_candidates(row, p, mine, n, ids);
     }
     __syncwarp();
   }
@@ -389,17 +482,28 @@ __device__ __forceinline__ void weigh(const float* row, const RsParams& p, const
 __device__ __forceinline__ int slot_of_expert(const int32_t* topk_ids, int t, int k, int e) {
   const int32_t* row = topk_ids + static_cast<size_t>(t) * k;
   if ((k & 3) == 0) {
-    for (int q = 0; q < k; q += 4) {
-      const int4 v = __ldcg(reinterpret_cast<const int4*>(row + q));
-      if (v.x == e) return q;
-      if (v.y == e) return q + 1;
-      if (v.z == e) return q + 2;
-      if (v.w == e) return q + 3;
+    for (int q0 = 0; q0 < k; q0 += 16) {
+      int4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q0 + 4 * q < k) v[q] = __ldcg(reinterpret_cast<const int4*>(row + q0) + q);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q0 + 4 * q < k) {
+          const int at = v[q].x == e ? 0 : v[q].y == e ? 1 : v[q].z == e ? 2 : v[q].w == e ? 3 : -1;
+          if (at >= 0) return q0 + 4 * q + at;
+        }
     }
     return 0;
   }
-  for (int j = 0; j < k; ++j)
-    if (__ldcg(row + j) == e) return j;
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    int v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __ldcg(row + min(j0 + j, k - 1));
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (v[j] == e) return min(j0 + j, k - 1);
+  }
   return 0;
 }
 
@@ -481,6 +585,7 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   const int C = p.C, TC = 128 / C;
   const int rank = static_cast<int>(blockIdx.x) % C, tile = static_cast<int>(blockIdx.x) / C;
   const int t0 = tile * 128, own0 = rank * TC;
+  const int splits = p.wide ? 2 : C, split = p.wide ? static_cast<int>(blockIdx.x) & 1 : rank;  // of H
   const int pitch = p.epad + 4;  // floats: rows 16-byte aligned, neighbours 4 banks apart
   const bool given = p.logits_in != nullptr;
   // logits: the tile's partial sums [128][pitch], or a row per warp of given ones
@@ -507,6 +612,8 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   for (int i = tid; i < 256; i += kRsThreads) sm.map[i] = make_uint4(0u, 0u, 0u, 0u);
   uint32_t cols = 32;
   while (cols < static_cast<uint32_t>(p.epad)) cols <<= 1;
+  const uint32_t second = cols;  // the other tile's accumulator
+  if (p.wide) cols <<= 1;
   if (!given && warp == 1) tmem_alloc(&sm.tmem_base, cols);
   tc_fence_before();
   __syncthreads();
@@ -515,9 +622,9 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   if (!given) {
     const uint32_t tmem = sm.tmem_base;
     const int nkb = (p.H + 63) / 64;
-    const int kb0 = static_cast<int>(static_cast<long long>(nkb) * rank / C);
-    const int kb1 = static_cast<int>(static_cast<long long>(nkb) * (rank + 1) / C);
-    const int stage_bytes = (128 + p.epad) * 128;
+    const int kb0 = static_cast<int>(static_cast<long long>(nkb) * split / splits);
+    const int kb1 = static_cast<int>(static_cast<long long>(nkb) * (split + 1) / splits);
+    const int x_bytes = (p.wide ? 256 : 128) * 128, stage_bytes = x_bytes + p.epad * 128;
     if (warp == 0) {
       if (lane == 0) {
         int stage = 0;
@@ -526,8 +633,9 @@ __global__ void __launch_bounds__(kRsThreads, 1)
           if (!mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, nullptr, kFtWaitNs, 70)) break;
           uint8_t* s = ring + stage * stage_bytes;
           mbar_arrive_expect_tx(&sm.full[stage], static_cast<uint32_t>(stage_bytes));
-          tma_load_2d(s, &tmx, &sm.full[stage], kb * 64, t0);
-          tma_load_2d(s + 128 * 128, &tmw, &sm.full[stage], kb * 64, 0);
+          tma_load_2d(s, &tmx, &sm.full[stage], kb * 64, p.wide ? (tile & ~1) * 128 : t0);
+          if (p.wide) tma_load_2d(s + 128 * 128, &tmx, &sm.full[stage], kb * 64, (tile | 1) * 128);
+          tma_load_2d(s + x_bytes, &tmw, &sm.full[stage], kb * 64, 0);
           filled |= 1u << stage;
           parity_of = (parity_of & ~(1u << stage)) | (phase << stage);
           if (++stage == p.stages) {
@@ -552,9 +660,15 @@ __global__ void __launch_bounds__(kRsThreads, 1)
           if (!mbar_wait(&sm.full[stage], phase, abort_flag, nullptr, kFtWaitNs, 71)) break;
           tc_fence_after();
           const uint32_t s = smem_u32(ring + stage * stage_bytes);
-          const uint64_t ad = umma_desc_sw128(s), bd = umma_desc_sw128(s + 128 * 128);
+          const uint64_t ad = umma_desc_sw128(s), bd = umma_desc_sw128(s + x_bytes);
 #pragma unroll
           for (int k = 0; k < 4; ++k) umma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
+          if (p.wide) {
+            const uint64_t od = umma_desc_sw128(s + 128 * 128);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_bf16(tmem + second, od + 2 * k, bd + 2 * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
+          }
           umma_commit(&sm.empty[stage]);
           if (++stage == p.stages) {
             stage = 0;
@@ -569,56 +683,94 @@ __global__ void __launch_bounds__(kRsThreads, 1)
     }
     __syncthreads();  // the ring is idle
     tc_fence_after();
-    // accumulator -> partial sums: warps of a lane quarter take every fourth run of 32 experts
+    // accumulator (the peer's tile of the two) -> partial sums: warps of a lane quarter take
+    // every fourth run of 32 experts
     const int q4 = warp & 3, m = q4 * 32 + lane;
-    for (int c0 = (warp >> 2) * 32; c0 < p.epad; c0 += kRsWarps / 4 * 32) {
-      float v[32];
-      tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q4 * 32) << 16) + c0, v);
-      if (kb1 == kb0) {  // no K block of its own: nothing was accumulated
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = 0.f;
-      }
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
+    auto store32 = [&](int c0, const float* v) {
 #pragma unroll
       for (int j = 0; j < 32; j += 4)
         if (c0 + j < p.epad)
           *reinterpret_cast<float4*>(part + m * pitch + c0 + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-    }
-    tc_fence_before();
-    if (C > 1) cluster_sync_all();
-    else __syncthreads();
-    tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, cols);
-    // own tokens: the sum over the cluster in rank order, in place (no peer reads these rows)
-    const int e4 = p.epad / 4;
-    if (C > 1 || p.bias != nullptr || p.logits_out != nullptr)
-      for (int i = tid; i < TC * e4; i += kRsThreads) {
-        const int row = own0 + i / e4, e = (i % e4) * 4;
-        float* at = part + row * pitch + e;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = 0; c < C; ++c) {
-          const float4 v = ld_cluster_f4(mapa_shared(smem_u32(at), static_cast<uint32_t>(c)));
-          s.x += v.x;
-          s.y += v.y;
-          s.z += v.z;
-          s.w += v.w;
-        }
-        const float o[4] = {s.x, s.y, s.z, s.w};
+    };
+    for (int c0 = (warp >> 2) * 32; c0 < p.epad; c0 += kRsWarps / 4 * 32) {
+      float v[32];
+      tmem_ld_32x32b_x32(lanes + (p.wide && split == 0 ? second : 0u) + c0, v);
+      if (kb1 == kb0) {  // no K block of its own: nothing was accumulated
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (e + j >= p.E) break;
-          const float l = o[j] + (p.bias != nullptr ? p.bias[e + j] : 0.f);
-          at[j] = l;
-          if (p.logits_out != nullptr && t0 + row < p.M) p.logits_out[static_cast<size_t>(t0 + row) * p.E + e + j] = l;
+        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+      }
+      store32(c0, v);
+    }
+    if (p.wide) {  // the other half of the sum comes from the peer; its rows then take the logits
+      float v[2][32];
+      cluster_sync_all();
+      const uint32_t other = mapa_shared(smem_u32(part + m * pitch), static_cast<uint32_t>(split ^ 1));
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int c0 = (warp >> 2) * 32 + u * (kRsWarps / 4 * 32);
+        if (c0 < p.epad) {
+          float4 o[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            o[j] = c0 + 4 * j < p.epad ? ld_cluster_f4(other + (c0 + 4 * j) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+          tmem_ld_32x32b_x32(lanes + (split == 0 ? 0u : second) + c0, v[u]);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float4 w = o[j / 4];
+            if (kb1 == kb0) v[u][j] = 0.f;
+            v[u][j] += j % 4 == 0 ? w.x : j % 4 == 1 ? w.y : j % 4 == 2 ? w.z : w.w;
+            if (p.bias != nullptr && c0 + j < p.E) v[u][j] += p.bias[c0 + j];
+          }
         }
       }
+      tc_fence_before();
+      cluster_sync_all();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int c0 = (warp >> 2) * 32 + u * (kRsWarps / 4 * 32);
+        if (c0 < p.epad) store32(c0, v[u]);
+      }
+    } else {
+      tc_fence_before();
+      cluster_sync_all();
+      // own tokens: the sum over the cluster in rank order, in place (no peer reads these rows)
+      const int e4 = p.epad / 4;
+      if (C > 1 || p.bias != nullptr)
+        for (int i = tid; i < TC * e4; i += kRsThreads) {
+          const int e = (i % e4) * 4;
+          float* at = part + (own0 + i / e4) * pitch + e;
+          const uint32_t addr = smem_u32(at);
+          float4 v[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c)  // all on their way before the first is added
+            if (c < C) v[c] = ld_cluster_f4(mapa_shared(addr, static_cast<uint32_t>(c)));
+          float4 s = v[0];
+#pragma unroll
+          for (int c = 1; c < 8; ++c)
+            if (c < C) {
+              s.x += v[c].x;
+              s.y += v[c].y;
+              s.z += v[c].z;
+              s.w += v[c].w;
+            }
+          if (p.bias != nullptr) {
+            s.x += e < p.E ? p.bias[e] : 0.f;
+            s.y += e + 1 < p.E ? p.bias[e + 1] : 0.f;
+            s.z += e + 2 < p.E ? p.bias[e + 2] : 0.f;
+            s.w += e + 3 < p.E ? p.bias[e + 3] : 0.f;
+          }
+          *reinterpret_cast<float4*>(at) = s;
+        }
+    }
     __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, cols);
   }
 
   // ---- a warp per token
-  float sb[NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i)
-    sb[i] = p.score_bias != nullptr && lane + 32 * i < p.E ? p.score_bias[lane + 32 * i] : 0.f;
+  ChoiceSetup<NI> cs;
+  cs.make(p);
   for (int i = warp; i < TC; i += kRsWarps) {
     const int t = t0 + own0 + i;
     if (t >= p.M) break;
@@ -627,16 +779,13 @@ __global__ void __launch_bounds__(kRsThreads, 1)
       float* mine = part + warp * pitch;
 #pragma unroll
       for (int j = 0; j < NI; ++j)
-        if (lane + 32 * j < p.E) {
-          const float v = p.logits_in[static_cast<size_t>(t) * p.E + lane + 32 * j];
-          mine[lane + 32 * j] = v;
-          if (p.logits_out != nullptr) p.logits_out[static_cast<size_t>(t) * p.E + lane + 32 * j] = v;
-        }
+        if (lane + 32 * j < p.E) mine[lane + 32 * j] = p.logits_in[static_cast<size_t>(t) * p.E + lane + 32 * j];
       row = mine;
       __syncwarp();
     }
     float mx, sum;
-    bool bad = choose<NI>(row, p, sb, scratch, sm.ids[warp], mx, sum);
+    bool bad = choose<NI>(row, p, cs, p.logits_out != nullptr ? p.logits_out + static_cast<size_t>(t) * p.E : nullptr,
+                          scratch, sm.ids[warp], mx, sum);
     weigh(row, p, sm.ids[warp], t, mx, sum);
     const int a = p.adapter_ids[t];
     bad |= a < -1 || a >= p.L;
@@ -675,7 +824,7 @@ __global__ void __launch_bounds__(kRsThreads, 1)
       }
     }
     if (tid == 0) p.flags[chunk] = sm.flag;
-    if (C > 1) cluster_sync_all();  // the peers have read this CTA's partial sums
+    cluster_sync_all();  // the peers have read this CTA's partial sums
     return;
   }
 
@@ -683,22 +832,27 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   int* run = reinterpret_cast<int*>(scratch);            // next place by adapter, of this warp
   int* s_base = reinterpret_cast<int*>(sm.ids);          // pairs of lower experts (the ids are done)
   uint8_t* s_ad = reinterpret_cast<uint8_t*>(sm.ids) + 1024;  // adapters of the tokens
+  const int my_ad = tid < p.M ? p.adapter_ids[tid] : -1;      // (of the first 128 threads)
   cluster_sync_all();
   uint4 m = make_uint4(0u, 0u, 0u, 0u);
   int n = 0;
   if (tid < p.E) {
-    for (int c = 0; c < C; ++c) {
-      const uint4 v = ld_cluster_u32x4(mapa_shared(smem_u32(sm.map + tid), static_cast<uint32_t>(c)));
-      m = make_uint4(m.x | v.x, m.y | v.y, m.z | v.z, m.w | v.w);
-    }
+    uint4 v[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < C) v[c] = ld_cluster_u32x4(mapa_shared(smem_u32(sm.map + tid), static_cast<uint32_t>(c)));
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < C) m = make_uint4(m.x | v[c].x, m.y | v[c].y, m.z | v[c].z, m.w | v[c].w);
     n = __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
   }
-  if (rank == 0 && tid == 0) {  // the call's status word
-    int flag = kRsClean;
-    for (int c = 0; c < C; ++c)
-      flag = min(flag, ld_cluster_s32(mapa_shared(smem_u32(&sm.flag), static_cast<uint32_t>(c))));
-    p.status[0] = flag == kRsClean ? MOE_LORA_OK : flag < 0 ? MOE_LORA_ERR_TIMEOUT : MOE_LORA_ERR_DEVICE_CHECK;
-    p.status[1] = flag == kRsClean || flag < 0 ? 0 : flag;
+  if (rank == 0 && warp == kRsWarps - 1) {  // the call's status word
+    int flag = lane < C ? ld_cluster_s32(mapa_shared(smem_u32(&sm.flag), static_cast<uint32_t>(lane))) : kRsClean;
+    flag = __reduce_min_sync(0xffffffffu, flag);
+    if (lane == 0) {
+      p.status[0] = flag == kRsClean ? MOE_LORA_OK : flag < 0 ? MOE_LORA_ERR_TIMEOUT : MOE_LORA_ERR_DEVICE_CHECK;
+      p.status[1] = flag == kRsClean || flag < 0 ? 0 : flag;
+    }
   }
   cluster_sync_all();  // every peer has read the maps
   const int base = block_prefix(n, sm.scan);
@@ -706,10 +860,7 @@ __global__ void __launch_bounds__(kRsThreads, 1)
     s_base[tid] = base;
     sm.map[tid] = m;
   }
-  if (tid < 128) {
-    const int a = tid < p.M ? p.adapter_ids[tid] : -1;
-    s_ad[tid] = static_cast<uint8_t>(a >= 0 && a < p.L ? a : p.L);
-  }
+  if (tid < 128) s_ad[tid] = static_cast<uint8_t>(my_ad >= 0 && my_ad < p.L ? my_ad : p.L);
   __syncthreads();
   const int LA = p.L + 1;
   for (int e = rank * kRsWarps + warp; e < p.E; e += C * kRsWarps) {
@@ -736,6 +887,7 @@ __global__ void __launch_bounds__(kRsThreads) route_scored_sort_kernel(const RsP
   __shared__ int s_run[kRsWarps][65];
   __shared__ int s_off[65];
   __shared__ uint16_t s_list[kRsWarps][1024];
+  __shared__ uint8_t s_ad[kRsWarps][512];  // adapters of the list's first tokens
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int e = blockIdx.x, LA = p.L + 1;
   const int words = p.tiles * 4, chunks = p.tiles * p.C;
@@ -786,7 +938,11 @@ __global__ void __launch_bounds__(kRsThreads) route_scored_sort_kernel(const RsP
   for (int w = 0; w < kRsWarps; ++w) base += s_scan[w];
   for (int r = r0; r < r1; ++r) {
     compact(r);
-    for (int i = lane; i < n; i += 32) atomicAdd(&s_run[warp][adapter(r * 1024 + list[i])], 1);
+    for (int i = lane; i < n; i += 32) {
+      const int a = adapter(r * 1024 + list[i]);
+      if (i < 512) s_ad[warp][i] = static_cast<uint8_t>(a);
+      atomicAdd(&s_run[warp][a], 1);
+    }
   }
   __syncthreads();
   if (tid < LA) {  // counts of the expert by adapter; s_run: the warps' exclusive prefix
@@ -812,13 +968,14 @@ __global__ void __launch_bounds__(kRsThreads) route_scored_sort_kernel(const RsP
     for (int i0 = 0; i0 < n; i0 += 32) {
       const bool in = i0 + lane < n;
       const int t = in ? r * 1024 + list[i0 + lane] : 0;
-      place32(p, in, t, in ? adapter(t) : 0, e, s_run[warp]);
+      place32(p, in, t, !in ? 0 : r1 - r0 > 1 || i0 >= 512 ? adapter(t) : s_ad[warp][i0 + lane], e, s_run[warp]);
     }
   }
 }
 
 // ------------------------------------------------------------------ host
-// CTAs per tile of 128 tokens: as many as keep one CTA per SM, 8 at most.
+// CTAs per tile of 128 tokens: as many as keep one CTA per SM, 8 at most.  One: then pairs of
+// CTAs make the logits of two tiles (see above), and the count of tiles is even.
 constexpr int kRsSms = 148;
 
 static int scored_split(int M) {
@@ -829,7 +986,7 @@ static int scored_split(int M) {
 }
 
 void route_scored_scratch(int M, int E, size_t* bitmap, size_t* before, size_t* flags) {
-  const size_t tiles = (static_cast<size_t>(M) + 127) / 128;
+  const size_t tiles = M <= 128 ? 1 : (static_cast<size_t>(M) + 255) / 256 * 2;
   const size_t chunks = std::max<size_t>(tiles, std::min<size_t>(8 * tiles, kRsSms));  // or more: grows with M
   *bitmap = tiles > 1 ? E * tiles * 16 : 0;
   *before = tiles > 1 ? E * chunks * 4 : 0;
@@ -841,7 +998,7 @@ static cudaError_t launch_choice(const RsParams& p, const CUtensorMap& tmx, cons
   const int pitch = p.epad + 4;
   const size_t rows = p.logits_in ? kRsWarps : 128;
   size_t body = rows * pitch * 4 + static_cast<size_t>(kRsWarps) * p.epad * 8;
-  if (!p.logits_in) body = std::max(body, static_cast<size_t>(p.stages) * (128 + p.epad) * 128);
+  if (!p.logits_in) body = std::max(body, static_cast<size_t>(p.stages) * ((p.wide ? 256 : 128) + p.epad) * 128);
   static std::atomic<bool> attr_set[kMaxDevices];
   const int dev = current_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
@@ -859,7 +1016,7 @@ static cudaError_t launch_choice(const RsParams& p, const CUtensorMap& tmx, cons
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.C;
+  attr[0].val.clusterDim.x = p.wide ? 2 : p.C;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -896,7 +1053,9 @@ cudaError_t launch_route_scored(const RouteScoredArgs& a, cudaStream_t st) {
   p.C = scored_split(a.M);
   p.tiles = (a.M + 127) / 128;
   p.epad = std::max(48, (a.E + 15) / 16 * 16);  // (the sort's 65 counters fit a warp's doubles)
-  p.stages = std::min(kRsMaxStages, kRsRing / ((128 + p.epad) * 128));
+  p.wide = p.C == 1;
+  if (p.wide) p.tiles = (p.tiles + 1) & ~1;
+  p.stages = std::min(kRsMaxStages, kRsRing / (((p.wide ? 256 : 128) + p.epad) * 128));
   p.f = a.f;
   CUtensorMap tmx{}, tmw{};
   if (a.logits_in == nullptr &&

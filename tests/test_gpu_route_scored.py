@@ -277,3 +277,21 @@ def test_huge_biases_of_both_signs(M):
     for rule in ("max", "top2"):
         _check(M, 32, 5, 3, 2, lg=lg, score="sigmoid", score_bias=b, n_group=4, topk_group=3, group_rule=rule)
         _check(M, 32, 5, 3, 2, lg=lg, score="softmax", score_bias=b, n_group=8, topk_group=3, group_rule=rule)
+
+
+@pytest.mark.parametrize("M,H", [(9473, 8), (9600, 72), (10001, 264), (12345, 128)])
+@pytest.mark.parametrize("E", [20, 96, 256])
+def test_pairs_of_tiles(M, H, E):
+    """Batches whose tiles fill the SMs: two CTAs share 256 tokens."""
+    x, wr, lg = grid_router(M, E, H, M + E)
+    ad = adapters(M, 5, M)
+    b = np.random.default_rng(E).standard_normal(E).astype(np.float32) * 0.05
+    bias = (np.random.default_rng(6).integers(-16, 17, size=E) * 0.125).astype(np.float32)
+    fmt = dict(score="sigmoid", n_group=4, topk_group=2, group_rule="max", scale=2.5)
+    res = ml.route_scored(torch.from_numpy(ad).cuda(), 4, 5, x=x.cuda(), w_router=wr.cuda(),
+                          bias=torch.from_numpy(bias).cuda(), score_bias=torch.from_numpy(b).cuda(),
+                          want_logits=True, **fmt)
+    torch.cuda.synchronize()
+    assert np.array_equal(res["logits"].cpu().numpy().astype(np.float64), lg + bias[None, :])
+    check_route(res, lg + bias[None, :], ad, E, 4, 5, score_bias=b.astype(np.float64), **fmt)
+    ml.check_status(res["workspace"])
