@@ -10,7 +10,7 @@
 // partial logits of 128 / C tokens from its peers' shared memory in rank order; its warps
 // then choose those tokens' experts, a warp per token, the logits never leaving the SM.
 // Batches that fill the SMs with 128 tokens each are bound by what the SMs read (x once, W_r
-// once per tile): there two CTAs share 256 tokens, each over half of H.
+// once per tile): there CTA pairs (tcgen05 cta_group::2) share W_r, each reading half of it.
 //
 // The sort needs no atomics on global memory: a CTA leaves one bit per (expert, token) and
 // the running count of its pairs by expert.  Up to 128 tokens the cluster itself sorts (a
@@ -29,6 +29,8 @@ constexpr int kRsThreads = 512;
 constexpr int kRsWarps = kRsThreads / 32;
 constexpr int kRsMaxStages = 8;
 constexpr int kRsRing = 196608;  // bytes of the ring at most
+constexpr int kRsBody = 128 * 260 * 4 + kRsWarps * 256 * 16;  // of its later use: logits, two doubles per warp and expert
+static_assert(kRsBody >= kRsRing, "the dynamic shared memory of the largest case");
 
 struct RsParams {
   const float* logits_in;
@@ -47,7 +49,7 @@ struct RsParams {
   int M, H, E, k, L;
   int tiles;  // of 128 tokens
   int C;      // CTAs that share a tile's tokens
-  int wide;   // two CTAs make the logits of two tiles, then take one each (C = 1)
+  int wide;   // CTA pairs make the logits of two tiles (C = 1)
   int epad, stages;
   ScoreFormat f;
 };
@@ -60,6 +62,7 @@ struct RsCore {
   int abort_flag;
   int flag;
   int scan[kRsWarps];
+  float score_bias[256];
   alignas(16) uint4 map[256];  // tokens of the tile (this CTA's: 128 / C of them) by expert
   uint8_t ids[kRsWarps][256];  // a token's choice
 };
@@ -98,11 +101,11 @@ struct ChoiceSetup {
   float sb[NI];        // selection bias
   int group_lane[NI];  // first lane of the expert's group (groups take `per` lanes each)
   int per;
-  float lo, scale;     // of fixed-point scores
-  uint32_t slack;      // difference of q that proves an order of scores
+  float lo, range;     // selection biases: the smallest, and from there to the largest
+  float most;          // ... the largest magnitude, plus one
   bool exact;          // every token in 64 bits
 
-  __device__ __forceinline__ void make(const RsParams& p) {
+  __device__ __forceinline__ void make(const RsParams& p, const float* score_bias) {
     const int lane = threadIdx.x & 31;
     per = 32;
     while (per > 1 && per * p.f.n_group > 32) per >>= 1;
@@ -112,14 +115,14 @@ struct ChoiceSetup {
     for (int i = 0; i < NI; ++i) {
       const int e = lane + 32 * i;
       const bool in = e < p.E;
-      sb[i] = in && p.score_bias != nullptr ? p.score_bias[e] : 0.f;
+      sb[i] = score_bias[e];
       group_lane[i] = in && !exact ? e / p.f.group_size * per : 0;
       const float b = fabsf(sb[i]);
       if (in && b <= kBiasMost) {
         bmin = fminf(bmin, sb[i]);
         bmax = fmaxf(bmax, sb[i]);
       }
-      // (a score is at most 1: a bias between the range and 2 beyond it might cross over)
+      // (a score is at most 1: a bias up to 2 beyond the range might cross over)
       exact |= in && b > kBiasMost && b < kBiasMost + 2.f;
     }
     exact = __any_sync(0xffffffffu, exact);
@@ -127,15 +130,8 @@ struct ChoiceSetup {
     bmax = warp_max(bmax);
     if (bmin > bmax) bmin = bmax = 0.f;
     lo = bmin;
-    const float range = 1.f + (bmax - bmin);
-    scale = kQSpan / range;
-    // Error of a selection score in 2^-24: a sigmoid's exponential (2 ulp), sum and quotient 3;
-    // a softmax's exponential and its argument 5, the sum of up to 256 of them (4 each, 13
-    // roundings) 17, quotient and product 3; the add of the bias |c|; then (c - lo) scale and
-    // its floor, the range each.  Two scores, in units of range 2^-24.
-    const float most = fmaxf(fabsf(bmin), fabsf(bmax + 1.f));
-    slack = static_cast<uint32_t>(2.f * ((p.f.sigmoid ? 3.f : 25.f) + most + 3.f * range) / range) + 2u;
-    if (p.f.by_logit) slack = 0u;
+    range = bmax - bmin;
+    most = fmaxf(fabsf(bmin), fabsf(bmax)) + 1.f;
   }
 };
 
@@ -159,8 +155,9 @@ __device__ __forceinline__ float row_max(const float* row, int E) {
   return warp_max(mx);
 }
 
-__device__ __forceinline__ double exact_sum(const float* row, int E, float mx) {
+__device__ __noinline__ double exact_sum(const float* row, int E, float mx) {
   double sum = 0.0;
+#pragma unroll 1
   for (int e = threadIdx.x & 31; e < E; e += 32)
     if (row[e] == row[e]) sum += exp(static_cast<double>(clamp_finite(row[e])) - mx);
 #pragma unroll
@@ -168,7 +165,7 @@ __device__ __forceinline__ double exact_sum(const float* row, int E, float mx) {
   return sum;
 }
 
-__device__ __forceinline__ double exact_score(float logit, int sigmoid, float mx, double sum) {
+__device__ __noinline__ double exact_score(float logit, int sigmoid, float mx, double sum) {
   const double l = clamp_finite(logit);
   const double x = exp(sigmoid ? -l : l - mx);
   return sigmoid ? 1.0 / (1.0 + x) : x / sum;
@@ -197,44 +194,41 @@ __device__ __noinline__ void order_candidates(const float* row, const RsParams& 
   __syncwarp();
 }
 
-// The definition in 64 bits: for tokens whose 32-bit scores lie too close to prove an order.
-// Lane l holds experts l, l + 32, ...; c: 256 doubles of the warp.
-template <int NI>
-__device__ __noinline__ void choose_exact(const float* row, const RsParams& p, double* c_of, uint8_t* ids) {
+// The definition in 64 bits, for tokens whose 32-bit scores lie too close to prove an order.
+// Few instructions rather than few steps: rarely run, its code is read from far.  c: a double
+// of the warp per expert; g: a double per group (n_group > 1 only).
+__device__ __noinline__ void choose_exact(const float* row, const RsParams& p, double* c, double* g, uint8_t* ids) {
   const int lane = threadIdx.x & 31;
-  const int E = p.E;
   const ScoreFormat& f = p.f;
-  unsigned alive = 0u;
-  float mx = -FLT_MAX;
-  if (!f.sigmoid) mx = row_max(row, E);
-  const double sum = f.sigmoid ? 1.0 : exact_sum(row, E, mx);
-  auto score = [&](int e) -> double { return exact_score(row[e], f.sigmoid, mx, sum); };
-  auto bias = [&](int e) -> double { return p.score_bias ? static_cast<double>(clamp_finite(p.score_bias[e])) : 0.0; };
-  double c[NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int e = lane + 32 * i;
-    c[i] = -INFINITY;
-    if (e >= E) continue;
-    alive |= 1u << i;
-    c[i] = exact_selection(row, p, e, mx, sum);
-    c_of[e] = c[i];
-  }
+  const bool by_score = !f.sigmoid && !f.by_logit;
+  const float mx = by_score ? row_max(row, p.E) : 0.f;
+  const double sum = by_score ? exact_sum(row, p.E, mx) : 1.0;
+#pragma unroll 1
+  for (int e = lane; e < p.E; e += 32) c[e] = exact_selection(row, p, e, mx, sum);
   __syncwarp();
+  // takes the largest of v[0, n), the first of equals; taken: bit i of lane l for 32 i + l
+  auto take = [&](const double* v, int n, unsigned& taken) -> int {
+    double bv = -INFINITY;
+    int bi = 0x7fffffff;
+#pragma unroll 1
+    for (int i = 0; 32 * i + lane < n; ++i)
+      if (!(taken >> i & 1u) && (bi == 0x7fffffff || v[32 * i + lane] > bv)) {
+        bv = v[32 * i + lane];
+        bi = 32 * i + lane;
+      }
+    warp_argmax(bv, bi);
+    if ((bi & 31) == lane) taken |= 1u << (bi >> 5);
+    return bi;
+  };
+  unsigned out = 0u;  // this lane's experts that are no candidates (any more)
   if (f.n_group > 1) {
-    double gs[NI];  // lane g holds groups g, g + 32, ...
-    unsigned galive = 0u;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int g = lane + 32 * i;
-      gs[i] = -INFINITY;
-      if (g >= f.n_group) continue;
-      galive |= 1u << i;
+#pragma unroll 1
+    for (int q = lane; q < f.n_group; q += 32) {
       double m1 = -INFINITY, m2 = -INFINITY;
-      int e1 = g * f.group_size, e2 = e1;
-      for (int j = 0; j < f.group_size; ++j) {
-        const int e = g * f.group_size + j;
-        const double v = c_of[e];
+      int e1 = q * f.group_size, e2 = e1;
+#pragma unroll 1
+      for (int e = q * f.group_size; e < (q + 1) * f.group_size; ++e) {
+        const double v = c[e];
         if (v > m1) {
           m2 = m1;
           e2 = e1;
@@ -245,49 +239,40 @@ __device__ __noinline__ void choose_exact(const float* row, const RsParams& p, d
           e2 = e;
         }
       }
-      gs[i] = m1;
       // scores and biases summed apart, so that groups whose two best have the same scores
       // and the same sum of biases tie, whatever the roundings
-      if (f.top2 && f.group_size > 1)
-        gs[i] = m2 == -INFINITY ? m2 : (score(e1) + score(e2)) + (bias(e1) + bias(e2));
-    }
-    unsigned keep = 0u;  // this lane's experts in a kept group
-    for (int j = 0; j < f.topk_group; ++j) {
-      double bv = -INFINITY;
-      int bg = 0x7fffffff;
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-        if ((galive >> i & 1u) && (bg == 0x7fffffff || gs[i] > bv)) {
-          bv = gs[i];
-          bg = lane + 32 * i;
-        }
-      warp_argmax(bv, bg);
-      if ((bg & 31) == lane) galive &= ~(1u << (bg >> 5));
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-        if ((lane + 32 * i) / f.group_size == bg) keep |= 1u << i;
-    }
-    alive &= keep;
-  }
-  for (int j = 0; j < p.k; ++j) {
-    double bv = -INFINITY;
-    int be = 0x7fffffff;
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-      if ((alive >> i & 1u) && (be == 0x7fffffff || c[i] > bv)) {
-        bv = c[i];
-        be = lane + 32 * i;
+      if (f.top2 && f.group_size > 1 && m2 != -INFINITY) {
+        const double s1 = exact_score(row[e1], f.sigmoid, mx, sum), s2 = exact_score(row[e2], f.sigmoid, mx, sum);
+        const double b1 = p.score_bias ? static_cast<double>(clamp_finite(p.score_bias[e1])) : 0.0;
+        const double b2 = p.score_bias ? static_cast<double>(clamp_finite(p.score_bias[e2])) : 0.0;
+        m1 = (s1 + s2) + (b1 + b2);
+      } else if (f.top2 && f.group_size > 1) {
+        m1 = m2;
       }
-    warp_argmax(bv, be);
-    if ((be & 31) == lane) alive &= ~(1u << (be >> 5));
-    if (lane == 0) ids[j] = static_cast<uint8_t>(be);
+      g[q] = m1;
+    }
+    __syncwarp();
+    out = 0xffffffffu;
+    unsigned taken = 0u;
+#pragma unroll 1
+    for (int j = 0; j < f.topk_group; ++j) {
+      const int q = take(g, f.n_group, taken);
+#pragma unroll 1
+      for (int i = 0; 32 * i + lane < p.E; ++i)
+        if ((32 * i + lane) / f.group_size == q) out &= ~(1u << i);
+    }
+  }
+#pragma unroll 1
+  for (int j = 0; j < p.k; ++j) {
+    const int e = take(c, p.E, out);
+    if (lane == 0) ids[j] = static_cast<uint8_t>(e);
   }
   __syncwarp();
 }
 
 // The k experts of the token whose logits are row[0, E), in order, into ids; returns whether
 // a NaN was met.  Also the row's largest logit and the sum of its exponentials (softmax).
-// scratch: a double of the warp per expert.
+// scratch: two doubles of the warp per expert.
 template <int NI>
 __device__ __forceinline__ bool choose(const float* row, const RsParams& p, const ChoiceSetup<NI>& cs, float* copy_to,
                                        double* scratch, uint8_t* ids, float& mx, float& sum) {
@@ -309,6 +294,7 @@ __device__ __forceinline__ bool choose(const float* row, const RsParams& p, cons
   }
   mx = -FLT_MAX;
   sum = 1.f;
+  float top = 1.f;
   if (!f.sigmoid || f.by_logit) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) mx = fmaxf(mx, l[i]);
@@ -325,15 +311,23 @@ __device__ __forceinline__ bool choose(const float* row, const RsParams& p, cons
     }
     sum = warp_sum(sum);
     if (!f.by_logit) {
-      const float inv = 1.f / sum;
+      top = 1.f / sum;  // the largest score
 #pragma unroll
-      for (int i = 0; i < NI; ++i) l[i] = s[i] * inv;
+      for (int i = 0; i < NI; ++i) l[i] = s[i] * top;
     }
   } else if (!f.by_logit) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) l[i] = 1.f / (1.f + expf(-l[i]));
+    for (int i = 0; i < NI; ++i) l[i] = __fdividef(1.f, 1.f + __expf(-l[i]));
   }
   // (l: the logits, or the scores)
+  // Error of a selection score in 2^-24: a sigmoid's exponential (s (1 - s) times 2 + 1.17 |l|
+  // steps) 2, its sum 1, its quotient 4; a softmax's exponential and its argument 5, the sum of
+  // up to 256 of them (4 each, 13 roundings) 17, quotient and product 3, of the largest score;
+  // the add of the bias |c|; then (c - lo) scale and its floor, the range each.  Two scores, in
+  // units of range 2^-24.
+  const float range = top + cs.range, scale = kQSpan / range;
+  const uint32_t base_slack =
+      f.by_logit ? 0u : static_cast<uint32_t>(2.f * ((f.sigmoid ? 7.f : 25.f * top) + cs.most + 3.f * range) / range) + 2u;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int e = lane + 32 * i;
@@ -342,7 +336,7 @@ __device__ __forceinline__ bool choose(const float* row, const RsParams& p, cons
       const float d = l[i] - (mx - kLogitSpan);
       q = d < 0.f ? kQLow : kQMin + static_cast<uint32_t>(d * (kQSpan / kLogitSpan));
     } else {
-      q = kQMin + static_cast<uint32_t>(fmaxf(l[i] + cs.sb[i] - cs.lo, 0.f) * cs.scale);
+      q = kQMin + static_cast<uint32_t>(fmaxf(l[i] + cs.sb[i] - cs.lo, 0.f) * scale);
       if (fabsf(cs.sb[i]) > kBiasMost) q = cs.sb[i] < 0.f ? kQLow : kQHigh;
     }
     if (nan[i]) q = kQNan;
@@ -376,7 +370,7 @@ __device__ __forceinline__ bool choose(const float* row, const RsParams& p, cons
       m2 = max(max(m2, a2), min(m1, a1));
       m1 = max(m1, a1);
     }
-    uint32_t gk = m1, slack = cs.slack;
+    uint32_t gk = m1, slack = base_slack;
     if (f.top2 && f.group_size > 1) {
       // (sums with a member beyond the range say nothing)
       exact = __any_sync(0xffffffffu, g < f.n_group && (m1 >= kQHigh || m2 == kQLow));
@@ -411,22 +405,22 @@ __device__ __forceinline__ bool choose(const float* row, const RsParams& p, cons
       return m;
     };
     for (int j = 0; j < p.k; ++j) {
-      const uint32_t top = next();
-      open |= j > 0 && !proved(prev >> 8, top >> 8, cs.slack);
-      prev = top;
-      const int e = 255 - static_cast<int>(top & 255u);
+      const uint32_t best = next();
+      open |= j > 0 && !proved(prev >> 8, best >> 8, base_slack);
+      prev = best;
+      const int e = 255 - static_cast<int>(best & 255u);
       mine = lane == j ? e : mine;
       if (lane == 0) ids[j] = static_cast<uint8_t>(e);
     }
-    uint32_t top = next();  // the first one left out
-    open |= !proved(prev >> 8, top >> 8, cs.slack);
+    uint32_t best = next();  // the first one left out
+    open |= !proved(prev >> 8, best >> 8, base_slack);
     if (open) {  // with every expert that may belong to the first k
       int n = p.k;
-      for (; n < 32 && !proved(prev >> 8, top >> 8, cs.slack); ++n) {
-        mine = lane == n ? 255 - static_cast<int>(top & 255u) : mine;
-        top = next();
+      for (; n < 32 && !proved(prev >> 8, best >> 8, base_slack); ++n) {
+        mine = lane == n ? 255 - static_cast<int>(best & 255u) : mine;
+        best = next();
       }
-      exact = n > 32 || !proved(prev >> 8, top >> 8, cs.slack);
+      exact = n > 32 || !proved(prev >> 8, best >> 8, base_slack);
       __syncwarp();
       if (!exact) order_candidates(row, p, mine, n, ids);
     }
@@ -434,7 +428,7 @@ __device__ __forceinline__ bool choose(const float* row, const RsParams& p, cons
   }
   if (exact) {
     __syncwarp();
-    choose_exact<NI>(row, p, scratch, ids);
+    choose_exact(row, p, scratch, scratch + p.epad, ids);
   }
   return __any_sync(0xffffffffu, bad);
 }
@@ -585,13 +579,12 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   const int C = p.C, TC = 128 / C;
   const int rank = static_cast<int>(blockIdx.x) % C, tile = static_cast<int>(blockIdx.x) / C;
   const int t0 = tile * 128, own0 = rank * TC;
-  const int splits = p.wide ? 2 : C, split = p.wide ? static_cast<int>(blockIdx.x) & 1 : rank;  // of H
   const int pitch = p.epad + 4;  // floats: rows 16-byte aligned, neighbours 4 banks apart
   const bool given = p.logits_in != nullptr;
   // logits: the tile's partial sums [128][pitch], or a row per warp of given ones
   float* part = reinterpret_cast<float*>(ring);
   double* scratch = reinterpret_cast<double*>(ring + static_cast<size_t>(given ? kRsWarps : 128) * pitch * 4) +
-                    warp * p.epad;
+                    warp * 2 * p.epad;
   volatile int* abort_flag = &sm.abort_flag;
   pdl_trigger();  // the sort of a large batch may be launched
 
@@ -609,22 +602,30 @@ __global__ void __launch_bounds__(kRsThreads, 1)
       tma_prefetch_desc(&tmw);
     }
   }
-  for (int i = tid; i < 256; i += kRsThreads) sm.map[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (tid < 256) {
+    sm.map[tid] = make_uint4(0u, 0u, 0u, 0u);
+    sm.score_bias[tid] = p.score_bias != nullptr && tid < p.E ? p.score_bias[tid] : 0.f;
+  }
   uint32_t cols = 32;
   while (cols < static_cast<uint32_t>(p.epad)) cols <<= 1;
-  const uint32_t second = cols;  // the other tile's accumulator
-  if (p.wide) cols <<= 1;
-  if (!given && warp == 1) tmem_alloc(&sm.tmem_base, cols);
+  if (!given && warp == 1) {
+    if (p.wide) tmem_alloc_pair(&sm.tmem_base, cols);
+    else tmem_alloc(&sm.tmem_base, cols);
+  }
   tc_fence_before();
-  __syncthreads();
+  if (p.wide) cluster_sync_all();  // the pair's barriers are ready
+  else __syncthreads();
   tc_fence_after();
 
   if (!given) {
     const uint32_t tmem = sm.tmem_base;
     const int nkb = (p.H + 63) / 64;
-    const int kb0 = static_cast<int>(static_cast<long long>(nkb) * split / splits);
-    const int kb1 = static_cast<int>(static_cast<long long>(nkb) * (split + 1) / splits);
-    const int x_bytes = (p.wide ? 256 : 128) * 128, stage_bytes = x_bytes + p.epad * 128;
+    const int kb0 = static_cast<int>(static_cast<long long>(nkb) * rank / C);
+    const int kb1 = static_cast<int>(static_cast<long long>(nkb) * (rank + 1) / C);
+    // pairs: M = 256 over both CTAs, each holding its own tokens and half of the experts' rows;
+    // copies are counted and MMAs issued by the even CTA
+    const int half = static_cast<int>(blockIdx.x) & 1, w_rows = p.wide ? p.epad / 2 : p.epad;
+    const int stage_bytes = (128 + w_rows) * 128;
     if (warp == 0) {
       if (lane == 0) {
         int stage = 0;
@@ -632,10 +633,16 @@ __global__ void __launch_bounds__(kRsThreads, 1)
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, nullptr, kFtWaitNs, 70)) break;
           uint8_t* s = ring + stage * stage_bytes;
-          mbar_arrive_expect_tx(&sm.full[stage], static_cast<uint32_t>(stage_bytes));
-          tma_load_2d(s, &tmx, &sm.full[stage], kb * 64, p.wide ? (tile & ~1) * 128 : t0);
-          if (p.wide) tma_load_2d(s + 128 * 128, &tmx, &sm.full[stage], kb * 64, (tile | 1) * 128);
-          tma_load_2d(s + x_bytes, &tmw, &sm.full[stage], kb * 64, 0);
+          if (p.wide) {
+            const uint32_t fb = mapa_shared(smem_u32(&sm.full[stage]), 0);
+            if (half == 0) mbar_arrive_expect_tx(&sm.full[stage], 2u * static_cast<uint32_t>(stage_bytes));
+            tma_load_2d_pair(s, &tmx, fb, kb * 64, t0);
+            tma_load_2d_pair(s + 128 * 128, &tmw, fb, kb * 64, half * w_rows);
+          } else {
+            mbar_arrive_expect_tx(&sm.full[stage], static_cast<uint32_t>(stage_bytes));
+            tma_load_2d(s, &tmx, &sm.full[stage], kb * 64, t0);
+            tma_load_2d(s + 128 * 128, &tmw, &sm.full[stage], kb * 64, 0);
+          }
           filled |= 1u << stage;
           parity_of = (parity_of & ~(1u << stage)) | (phase << stage);
           if (++stage == p.stages) {
@@ -643,109 +650,95 @@ __global__ void __launch_bounds__(kRsThreads, 1)
             phase ^= 1u;
           }
         }
-        if (*abort_flag)  // let our own copies land before the ring is reused
-          for (int s = 0; s < p.stages; ++s)
-            if (filled & (1u << s)) {
-              volatile int dummy = 0;
-              mbar_wait(&sm.full[s], (parity_of >> s) & 1u, &dummy, nullptr, kFtWaitNs / 4, 0);
+        if (*abort_flag) {  // let our own copies land before the ring is reused
+          if (p.wide && half != 0) {  // (counted on the leader's barriers: a fixed 50 us)
+            const uint64_t c0 = globaltimer_ns();
+            while (globaltimer_ns() - c0 < 50000ull) {
             }
+          } else {
+            for (int s = 0; s < p.stages; ++s)
+              if (filled & (1u << s)) {
+                volatile int dummy = 0;
+                mbar_wait(&sm.full[s], (parity_of >> s) & 1u, &dummy, nullptr, kFtWaitNs / 4, 0);
+              }
+          }
+        }
       }
       __syncwarp();
     } else if (warp == 1) {
       if (lane == 0) {
-        int stage = 0;
-        uint32_t phase = 0;
-        const uint32_t idesc = umma_idesc_bf16(128, p.epad);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&sm.full[stage], phase, abort_flag, nullptr, kFtWaitNs, 71)) break;
-          tc_fence_after();
-          const uint32_t s = smem_u32(ring + stage * stage_bytes);
-          const uint64_t ad = umma_desc_sw128(s), bd = umma_desc_sw128(s + x_bytes);
+        if (!p.wide || half == 0) {
+          int stage = 0;
+          uint32_t phase = 0;
+          const uint32_t idesc = umma_idesc_bf16(p.wide ? 256 : 128, p.epad);
+          for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait(&sm.full[stage], phase, abort_flag, nullptr, kFtWaitNs, 71)) break;
+            tc_fence_after();
+            const uint32_t s = smem_u32(ring + stage * stage_bytes);
+            const uint64_t ad = umma_desc_sw128(s), bd = umma_desc_sw128(s + 128 * 128);
+            if (p.wide) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) umma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
-          if (p.wide) {
-            const uint64_t od = umma_desc_sw128(s + 128 * 128);
+              for (int k = 0; k < 4; ++k)
+                umma_bf16_pair(tmem, ad + 2 * k, bd + 2 * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
+              umma_commit_pair(&sm.empty[stage], 3);
+            } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_bf16(tmem + second, od + 2 * k, bd + 2 * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
+              for (int k = 0; k < 4; ++k)
+                umma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
+              umma_commit(&sm.empty[stage]);
+            }
+            if (++stage == p.stages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          umma_commit(&sm.empty[stage]);
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (p.wide) umma_commit_pair(&sm.tfull, 3);
+          else umma_commit(&sm.tfull);
         }
-        umma_commit(&sm.tfull);
-        volatile int dummy = 0;
-        mbar_wait(&sm.tfull, 0, &dummy, nullptr, kFtWaitNs, 0);
+        if (!mbar_wait(&sm.tfull, 0, abort_flag, nullptr, kFtWaitNs, 72)) {  // (aborted: the MMAs issued end still)
+          volatile int dummy = 0;
+          mbar_wait(&sm.tfull, 0, &dummy, nullptr, kFtWaitNs, 0);
+        }
       }
       __syncwarp();
     }
     __syncthreads();  // the ring is idle
     tc_fence_after();
-    // accumulator (the peer's tile of the two) -> partial sums: warps of a lane quarter take
-    // every fourth run of 32 experts
+    // accumulator -> partial sums: warps of a lane quarter take every fourth run of 32 experts
     const int q4 = warp & 3, m = q4 * 32 + lane;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
-    auto store32 = [&](int c0, const float* v) {
-#pragma unroll
-      for (int j = 0; j < 32; j += 4)
-        if (c0 + j < p.epad)
-          *reinterpret_cast<float4*>(part + m * pitch + c0 + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-    };
     for (int c0 = (warp >> 2) * 32; c0 < p.epad; c0 += kRsWarps / 4 * 32) {
       float v[32];
-      tmem_ld_32x32b_x32(lanes + (p.wide && split == 0 ? second : 0u) + c0, v);
+      tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q4 * 32) << 16) + c0, v);
       if (kb1 == kb0) {  // no K block of its own: nothing was accumulated
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0.f;
       }
-      store32(c0, v);
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        if (c0 + j < p.epad)
+          *reinterpret_cast<float4*>(part + m * pitch + c0 + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
     }
-    if (p.wide) {  // the other half of the sum comes from the peer; its rows then take the logits
-      float v[2][32];
-      cluster_sync_all();
-      const uint32_t other = mapa_shared(smem_u32(part + m * pitch), static_cast<uint32_t>(split ^ 1));
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int c0 = (warp >> 2) * 32 + u * (kRsWarps / 4 * 32);
-        if (c0 < p.epad) {
-          float4 o[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            o[j] = c0 + 4 * j < p.epad ? ld_cluster_f4(other + (c0 + 4 * j) * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-          tmem_ld_32x32b_x32(lanes + (split == 0 ? 0u : second) + c0, v[u]);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float4 w = o[j / 4];
-            if (kb1 == kb0) v[u][j] = 0.f;
-            v[u][j] += j % 4 == 0 ? w.x : j % 4 == 1 ? w.y : j % 4 == 2 ? w.z : w.w;
-            if (p.bias != nullptr && c0 + j < p.E) v[u][j] += p.bias[c0 + j];
-          }
-        }
-      }
-      tc_fence_before();
-      cluster_sync_all();
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int c0 = (warp >> 2) * 32 + u * (kRsWarps / 4 * 32);
-        if (c0 < p.epad) store32(c0, v[u]);
-      }
-    } else {
-      tc_fence_before();
-      cluster_sync_all();
-      // own tokens: the sum over the cluster in rank order, in place (no peer reads these rows)
-      const int e4 = p.epad / 4;
-      if (C > 1 || p.bias != nullptr)
-        for (int i = tid; i < TC * e4; i += kRsThreads) {
-          const int e = (i % e4) * 4;
-          float* at = part + (own0 + i / e4) * pitch + e;
+    tc_fence_before();
+    if (C > 1) cluster_sync_all();
+    else __syncthreads();
+    tc_fence_after();
+    if (!p.wide && warp == 1) tmem_dealloc(tmem, cols);
+    // own tokens: the sum over the cluster in rank order, in place (no peer reads these rows)
+    const int e4 = p.epad / 4;
+    if (C > 1 || p.bias != nullptr)
+      for (int i = tid; i < TC * e4; i += kRsThreads) {
+        const int e = (i % e4) * 4;
+        float* at = part + (own0 + i / e4) * pitch + e;
+        float4 s;
+        if (C == 1) {
+          s = *reinterpret_cast<const float4*>(at);
+        } else {
           const uint32_t addr = smem_u32(at);
           float4 v[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c)  // all on their way before the first is added
             if (c < C) v[c] = ld_cluster_f4(mapa_shared(addr, static_cast<uint32_t>(c)));
-          float4 s = v[0];
+          s = v[0];
 #pragma unroll
           for (int c = 1; c < 8; ++c)
             if (c < C) {
@@ -754,27 +747,26 @@ __global__ void __launch_bounds__(kRsThreads, 1)
               s.z += v[c].z;
               s.w += v[c].w;
             }
-          if (p.bias != nullptr) {
-            s.x += e < p.E ? p.bias[e] : 0.f;
-            s.y += e + 1 < p.E ? p.bias[e + 1] : 0.f;
-            s.z += e + 2 < p.E ? p.bias[e + 2] : 0.f;
-            s.w += e + 3 < p.E ? p.bias[e + 3] : 0.f;
-          }
-          *reinterpret_cast<float4*>(at) = s;
         }
-    }
+        if (p.bias != nullptr) {
+          s.x += e < p.E ? p.bias[e] : 0.f;
+          s.y += e + 1 < p.E ? p.bias[e + 1] : 0.f;
+          s.z += e + 2 < p.E ? p.bias[e + 2] : 0.f;
+          s.w += e + 3 < p.E ? p.bias[e + 3] : 0.f;
+        }
+        *reinterpret_cast<float4*>(at) = s;
+      }
     __syncthreads();
-    tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, cols);
   }
 
   // ---- a warp per token
   ChoiceSetup<NI> cs;
-  cs.make(p);
+  cs.make(p, sm.score_bias);
   for (int i = warp; i < TC; i += kRsWarps) {
     const int t = t0 + own0 + i;
     if (t >= p.M) break;
     const float* row = part + (own0 + i) * pitch;
+    const int a = p.adapter_ids[t];
     if (given) {
       float* mine = part + warp * pitch;
 #pragma unroll
@@ -787,7 +779,6 @@ __global__ void __launch_bounds__(kRsThreads, 1)
     bool bad = choose<NI>(row, p, cs, p.logits_out != nullptr ? p.logits_out + static_cast<size_t>(t) * p.E : nullptr,
                           scratch, sm.ids[warp], mx, sum);
     weigh(row, p, sm.ids[warp], t, mx, sum);
-    const int a = p.adapter_ids[t];
     bad |= a < -1 || a >= p.L;
     if (bad && lane == 0) atomicMin(&sm.flag, t);
     const int b = own0 + i;  // the token's bit
@@ -824,7 +815,10 @@ __global__ void __launch_bounds__(kRsThreads, 1)
       }
     }
     if (tid == 0) p.flags[chunk] = sm.flag;
+    tc_fence_before();
     cluster_sync_all();  // the peers have read this CTA's partial sums
+    tc_fence_after();
+    if (p.wide && !given && warp == 1) tmem_dealloc_pair(sm.tmem_base, cols);
     return;
   }
 
@@ -974,8 +968,8 @@ __global__ void __launch_bounds__(kRsThreads) route_scored_sort_kernel(const RsP
 }
 
 // ------------------------------------------------------------------ host
-// CTAs per tile of 128 tokens: as many as keep one CTA per SM, 8 at most.  One: then pairs of
-// CTAs make the logits of two tiles (see above), and the count of tiles is even.
+// CTAs per tile of 128 tokens: as many as keep one CTA per SM, 8 at most.  One: CTA pairs, an
+// even count of tiles.
 constexpr int kRsSms = 148;
 
 static int scored_split(int M) {
@@ -997,14 +991,14 @@ template <int NI>
 static cudaError_t launch_choice(const RsParams& p, const CUtensorMap& tmx, const CUtensorMap& tmw, cudaStream_t st) {
   const int pitch = p.epad + 4;
   const size_t rows = p.logits_in ? kRsWarps : 128;
-  size_t body = rows * pitch * 4 + static_cast<size_t>(kRsWarps) * p.epad * 8;
-  if (!p.logits_in) body = std::max(body, static_cast<size_t>(p.stages) * ((p.wide ? 256 : 128) + p.epad) * 128);
+  size_t body = rows * pitch * 4 + static_cast<size_t>(kRsWarps) * p.epad * 16;
+  if (!p.logits_in) body = std::max(body, static_cast<size_t>(p.stages) * (128 + p.epad / (p.wide ? 2 : 1)) * 128);
   static std::atomic<bool> attr_set[kMaxDevices];
   const int dev = current_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     const cudaError_t e = cudaFuncSetAttribute(route_scored_kernel<NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               1024 + kRsRing);
+                                               1024 + kRsBody);
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
@@ -1055,14 +1049,14 @@ cudaError_t launch_route_scored(const RouteScoredArgs& a, cudaStream_t st) {
   p.epad = std::max(48, (a.E + 15) / 16 * 16);  // (the sort's 65 counters fit a warp's doubles)
   p.wide = p.C == 1;
   if (p.wide) p.tiles = (p.tiles + 1) & ~1;
-  p.stages = std::min(kRsMaxStages, kRsRing / (((p.wide ? 256 : 128) + p.epad) * 128));
+  p.stages = std::min(kRsMaxStages, kRsRing / ((128 + p.epad / (p.wide ? 2 : 1)) * 128));
   p.f = a.f;
   CUtensorMap tmx{}, tmw{};
   if (a.logits_in == nullptr &&
       (encode_tmap_2d(&tmx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.H, a.M, static_cast<uint64_t>(a.H) * 2, 64, 128,
                       CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
        encode_tmap_2d(&tmw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.w_router, a.H, a.E, static_cast<uint64_t>(a.H) * 2, 64,
-                      p.epad, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS))
+                      p.wide ? p.epad / 2 : p.epad, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS))
     return cudaErrorInvalidValue;
   cudaError_t e = a.E <= 64    ? launch_choice<2>(p, tmx, tmw, st)
                   : a.E <= 128 ? launch_choice<4>(p, tmx, tmw, st)
