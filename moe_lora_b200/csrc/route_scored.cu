@@ -80,56 +80,86 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 }
 __device__ __forceinline__ float warp_max(float v) { return key_value(__reduce_max_sync(0xffffffffu, order_key(v))); }
 
-// Selection scores as 24-bit fixed point q, so that q and the expert fit one word whose
-// warp-wide maximum is one instruction, equal q going to the lower expert.
+// Selection scores as 23-bit fixed point q, so that q and the expert fit one word whose
+// warp-wide maximum is one instruction, equal q going to the lower expert:
 //   0 not a candidate, kQNan NaN, kQLow / kQHigh beyond the range, else kQMin + (v - lo) scale
-// An order is proved where q differs by more than `slack` (or the lower one is NaN); what is
-// not proved is decided in 64 bits.  Logits compared as such: every step is monotone, so any
-// difference of q is a proof.
-constexpr uint32_t kQNan = 1u, kQLow = 2u, kQHigh = (1u << 24) - 2u, kQMin = 8u;
-constexpr float kQSpan = 16777200.f;  // 2^24 - 16
-constexpr float kBiasMost = 1024.f;   // larger biases leave the fixed-point range
-constexpr float kLogitSpan = 32.f;    // logits further below the largest are kQLow
+// A fused multiply-add onto 2^23 leaves q in the mantissa.  An order is proved where q differs
+// by more than `slack` (or the lower one is NaN); what is not proved is decided in 64 bits.
+// Logits compared as such: every step is monotone, so any difference of q is a proof.
+constexpr uint32_t kQNan = 1u, kQLow = 2u, kQHigh = (1u << 23) - 2u, kQMin = 16u;
+constexpr float kQSpan = 8388576.f;  // 2^23 - 32
+constexpr float kQOne = 8388608.f;   // 2^23: steps of one
+constexpr float kBiasMost = 1024.f;  // larger biases leave the fixed-point range
+constexpr float kLogitSpan = 32.f;   // logits further below the largest are kQLow
 
 __device__ __forceinline__ bool proved(uint32_t above, uint32_t below, uint32_t slack) {
   return below <= kQNan || above > below + slack;
 }
 
+__device__ __forceinline__ float exp2_approx(float x) {  // within 2^-22 of the value
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {  // within a unit of the last place
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // What the choice needs of the call, by lane (experts lane, lane + 32, ...).
 template <int NI>
 struct ChoiceSetup {
-  float sb[NI];        // selection bias
-  int group_lane[NI];  // first lane of the expert's group (groups take `per` lanes each)
-  int per;
-  float lo, range;     // selection biases: the smallest, and from there to the largest
-  float most;          // ... the largest magnitude, plus one
-  bool exact;          // every token in 64 bits
+  float above[NI];      // selection bias above the smallest one
+  unsigned group[NI];   // bit of the first lane of the expert's group (a group takes `per` lanes)
+  int at[NI];           // the expert's place among the groups' keys
+  int per, stride;      // ... a group's experts lie `stride` apart from the next one's
+  float range, most;    // of the biases: from the smallest to the largest; the magnitude, plus one
+  unsigned valid, nan, low, high;  // bit i: an expert, its bias NaN, or out of the range
+  bool odd;             // some expert of the call is not just valid
+  bool exact;           // every token in 64 bits
 
   __device__ __forceinline__ void make(const RsParams& p, const float* score_bias) {
     const int lane = threadIdx.x & 31;
     per = 32;
     while (per > 1 && per * p.f.n_group > 32) per >>= 1;
     exact = p.f.n_group > 32;
+    stride = p.f.group_size | 1;  // (lanes of neighbouring groups meet other banks)
+    valid = nan = low = high = 0u;
     float bmin = FLT_MAX, bmax = -FLT_MAX;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int e = lane + 32 * i;
-      const bool in = e < p.E;
-      sb[i] = score_bias[e];
-      group_lane[i] = in && !exact ? e / p.f.group_size * per : 0;
-      const float b = fabsf(sb[i]);
-      if (in && b <= kBiasMost) {
-        bmin = fminf(bmin, sb[i]);
-        bmax = fmaxf(bmax, sb[i]);
+      const float b = score_bias[e];
+      above[i] = 0.f;
+      group[i] = 0u;
+      at[i] = 0;
+      if (e >= p.E) continue;
+      valid |= 1u << i;
+      if (p.f.n_group > 1 && !exact) {
+        const int g = e / p.f.group_size;
+        group[i] = 1u << (g * per);
+        at[i] = e + g * (stride - p.f.group_size);
       }
-      // (a score is at most 1: a bias up to 2 beyond the range might cross over)
-      exact |= in && b > kBiasMost && b < kBiasMost + 2.f;
+      if (b != b) {
+        nan |= 1u << i;
+      } else if (fabsf(b) > kBiasMost) {
+        (b < 0.f ? low : high) |= 1u << i;
+        exact |= fabsf(b) < kBiasMost + 2.f;  // (a score is at most 1: it might cross over)
+      } else {
+        above[i] = b;
+        bmin = fminf(bmin, b);
+        bmax = fmaxf(bmax, b);
+      }
     }
     exact = __any_sync(0xffffffffu, exact);
+    odd = __any_sync(0xffffffffu, valid != (1u << NI) - 1u || (nan | low | high) != 0u);
     bmin = -warp_max(-bmin);
     bmax = warp_max(bmax);
     if (bmin > bmax) bmin = bmax = 0.f;
-    lo = bmin;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if ((valid & ~(nan | low | high)) >> i & 1u) above[i] -= bmin;
     range = bmax - bmin;
     most = fmaxf(fabsf(bmin), fabsf(bmax)) + 1.f;
   }
@@ -279,90 +309,101 @@ __device__ __forceinline__ bool choose(const float* row, const RsParams& p, cons
   const int lane = threadIdx.x & 31;
   const int E = p.E;
   const ScoreFormat& f = p.f;
-  float l[NI];
+  float v[NI];       // logits, then scores (exponentials, for a softmax)
   uint32_t key[NI];  // q and 255 - expert
-  bool nan[NI], bad = false;
+  unsigned nan = cs.nan;
+  float probe = 0.f;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int e = lane + 32 * i;
-    const float v = e < E ? row[e] : -FLT_MAX;
-    if (copy_to != nullptr && e < E) copy_to[e] = v;
-    nan[i] = v != v;
-    l[i] = nan[i] ? -FLT_MAX : clamp_finite(v);
-    nan[i] |= cs.sb[i] != cs.sb[i];
-    bad |= nan[i];
+    v[i] = cs.valid >> i & 1u ? row[lane + 32 * i] : 0.f;
+    if (copy_to != nullptr && (cs.valid >> i & 1u)) copy_to[lane + 32 * i] = v[i];
+    probe = fmaf(v[i], 0.f, probe);
+  }
+  const bool odd = __any_sync(0xffffffffu, probe != probe) || cs.odd;
+  if (odd) {  // infinities, NaN; no experts
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if (v[i] != v[i]) nan |= 1u << i;
+      v[i] = v[i] != v[i] || !(cs.valid >> i & 1u) ? -FLT_MAX : clamp_finite(v[i]);
+    }
   }
   mx = -FLT_MAX;
   sum = 1.f;
-  float top = 1.f;
   if (!f.sigmoid || f.by_logit) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) mx = fmaxf(mx, l[i]);
+    for (int i = 0; i < NI; ++i) mx = fmaxf(mx, v[i]);
     mx = warp_max(mx);
   }
+  // q = v unit + above bias + base
+  float unit = kQSpan / kLogitSpan, bias = 0.f, base = kQOne + kQMin + kQSpan, top = 1.f;
   if (!f.sigmoid && !(f.by_logit && f.renorm)) {
     float s[NI];
     sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int e = lane + 32 * i;
-      s[i] = e < E && row[e] == row[e] ? expf(l[i] - mx) : 0.f;
+      s[i] = cs.valid >> i & 1u ? expf(v[i] - mx) : 0.f;
+      if (odd && (nan & ~cs.nan) >> i & 1u) s[i] = 0.f;
       sum += s[i];
     }
     sum = warp_sum(sum);
     if (!f.by_logit) {
       top = 1.f / sum;  // the largest score
 #pragma unroll
-      for (int i = 0; i < NI; ++i) l[i] = s[i] * top;
+      for (int i = 0; i < NI; ++i) v[i] = s[i];
     }
   } else if (!f.by_logit) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) l[i] = __fdividef(1.f, 1.f + __expf(-l[i]));
+    for (int i = 0; i < NI; ++i) v[i] = rcp_approx(1.f + exp2_approx(v[i] * -1.4426950408889634f));
   }
-  // (l: the logits, or the scores)
-  // Error of a selection score in 2^-24: a sigmoid's exponential (s (1 - s) times 2 + 1.17 |l|
-  // steps) 2, its sum 1, its quotient 4; a softmax's exponential and its argument 5, the sum of
-  // up to 256 of them (4 each, 13 roundings) 17, quotient and product 3, of the largest score;
-  // the add of the bias |c|; then (c - lo) scale and its floor, the range each.  Two scores, in
-  // units of range 2^-24.
-  const float range = top + cs.range, scale = kQSpan / range;
-  const uint32_t base_slack =
-      f.by_logit ? 0u : static_cast<uint32_t>(2.f * ((f.sigmoid ? 7.f : 25.f * top) + cs.most + 3.f * range) / range) + 2u;
+  // Error of a selection score in 2^-24: a sigmoid's exponential (s (1 - s) times 4 for the
+  // value and 2 |l| for the argument) 2, its sum 1, its quotient 2; a softmax's exponential and
+  // its argument 5, the sum of up to 256 of them (4 each, 13 roundings) 17, quotient and unit 3,
+  // of the largest score; the bias above the smallest, the range.  In steps of range 2^-23, with
+  // a step for the two roundings of q and one for `unit`; for two scores.
+  uint32_t slack = 0u;
+  if (f.by_logit) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) v[i] -= mx;
+  } else {
+    const float range = top + cs.range;
+    bias = kQSpan / range;
+    unit = bias * top;
+    base = kQOne + kQMin;
+    slack = static_cast<uint32_t>(2.f * (0.5f * ((f.sigmoid ? 5.f : 25.f * top) + range) / range + 2.f)) + 1u;
+  }
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int e = lane + 32 * i;
-    uint32_t q;
-    if (f.by_logit) {
-      const float d = l[i] - (mx - kLogitSpan);
-      q = d < 0.f ? kQLow : kQMin + static_cast<uint32_t>(d * (kQSpan / kLogitSpan));
-    } else {
-      q = kQMin + static_cast<uint32_t>(fmaxf(l[i] + cs.sb[i] - cs.lo, 0.f) * scale);
-      if (fabsf(cs.sb[i]) > kBiasMost) q = cs.sb[i] < 0.f ? kQLow : kQHigh;
+    const float q = fmaxf(fmaf(v[i], unit, fmaf(cs.above[i], bias, base)), kQOne + kQLow);
+    key[i] = __float_as_uint(q) * 256u + static_cast<uint32_t>(255 - 32 * i - lane);  // (drops the exponent)
+  }
+  if (odd) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const uint32_t tag = static_cast<uint32_t>(255 - 32 * i - lane);
+      if (cs.low >> i & 1u) key[i] = kQLow << 8 | tag;
+      if (cs.high >> i & 1u) key[i] = kQHigh << 8 | tag;
+      if (nan >> i & 1u) key[i] = kQNan << 8 | tag;
+      if (!(cs.valid >> i & 1u)) key[i] = 0u;
     }
-    if (nan[i]) q = kQNan;
-    key[i] = e < E ? min(q, kQHigh) << 8 | static_cast<uint32_t>(255 - e) : 0u;
   }
   bool exact = cs.exact;
   if (f.n_group > 1 && !exact) {
     uint32_t* keys = reinterpret_cast<uint32_t*>(scratch);
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-      if (lane + 32 * i < E) keys[lane + 32 * i] = key[i] >> 8;
+      if (cs.valid >> i & 1u) keys[cs.at[i]] = key[i];
     __syncwarp();
-    // `per` lanes per group walk its experts, starting at different places so that the lanes
-    // stay on different banks, and join their two largest
+    // `per` lanes per group walk its experts and join their two largest
     const int per = cs.per, g = lane / per, sub = lane & (per - 1);
+    const bool in = g < f.n_group;
     uint32_t m1 = 0u, m2 = 0u;
-    if (g < f.n_group) {
-      const int cnt = (f.group_size - sub + per - 1) / per;
-      const uint32_t* mine = keys + g * f.group_size + sub;
-      int j = cnt > 0 ? g % cnt : 0;
-#pragma unroll 4
-      for (int n = 0; n < cnt; ++n) {
-        const uint32_t v = mine[j * per];
-        m2 = max(m2, min(m1, v));
-        m1 = max(m1, v);
-        j = j + 1 == cnt ? 0 : j + 1;
+    if (in) {
+      const uint32_t* from = keys + g * cs.stride;
+#pragma unroll 8
+      for (int j = sub; j < f.group_size; j += per) {
+        const uint32_t o = from[j];
+        m2 = max(m2, min(m1, o));
+        m1 = max(m1, o);
       }
     }
     for (int o = 1; o < per; o <<= 1) {
@@ -370,67 +411,87 @@ __device__ __forceinline__ bool choose(const float* row, const RsParams& p, cons
       m2 = max(max(m2, a2), min(m1, a1));
       m1 = max(m1, a1);
     }
-    uint32_t gk = m1, slack = base_slack;
+    m1 >>= 8;
+    m2 >>= 8;
+    uint32_t gk = m1, group_slack = slack;
     if (f.top2 && f.group_size > 1) {
       // (sums with a member beyond the range say nothing)
-      exact = __any_sync(0xffffffffu, g < f.n_group && (m1 >= kQHigh || m2 == kQLow));
+      exact = __any_sync(0xffffffffu, in && (m1 >= kQHigh || m2 == kQLow));
       gk = m2 <= kQNan ? kQNan : m1 + m2;
-      slack *= 2u;
+      group_slack *= 2u;
     }
     gk = gk << 5 | static_cast<uint32_t>(31 - g);
-    const bool in = g < f.n_group;
-    int rank = 0;
+    int rank = 0;  // larger groups, and as large ones before
 #pragma unroll 4
     for (int h = 0; h < f.n_group; ++h) rank += __shfl_sync(0xffffffffu, gk, h * per) > gk ? 1 : 0;
     const bool kept = in && rank < f.topk_group;
     const uint32_t last = __reduce_min_sync(0xffffffffu, kept ? gk : 0xffffffffu);
     const uint32_t first = __reduce_max_sync(0xffffffffu, in && !kept ? gk : 0u);
-    exact |= !proved(last >> 5, first >> 5, slack);
+    exact |= !proved(last >> 5, first >> 5, group_slack);
     const unsigned keep = __ballot_sync(0xffffffffu, kept);
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-      if (!(keep >> cs.group_lane[i] & 1u)) key[i] = 0u;
+      if ((keep & cs.group[i]) == 0u) key[i] = 0u;
   }
   if (!exact) {
-    uint32_t prev = 0u;
-    int mine = 0;
-    bool open = false;  // an order that is not proved
+    // each lane's three largest in order; the warp takes the largest of all, k times
+    uint32_t a = 0u, b = 0u, c = 0u;
+    auto refill = [&](uint32_t below) {
+      a = b = c = 0u;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const uint32_t o = key[i] < below ? key[i] : 0u, u = min(a, o), w = min(b, u);
+        a = max(a, o);
+        b = max(b, u);
+        c = max(c, w);
+      }
+    };
+    refill(0xffffffffu);
+    int used = 0;
     auto next = [&]() -> uint32_t {
-      uint32_t m = key[0];
-#pragma unroll
-      for (int i = 1; i < NI; ++i) m = max(m, key[i]);
-      m = __reduce_max_sync(0xffffffffu, m);
-#pragma unroll
-      for (int i = 0; i < NI; ++i) key[i] = key[i] == m ? 0u : key[i];
+      const uint32_t m = __reduce_max_sync(0xffffffffu, a);
+      if (a == m) {
+        a = b;
+        b = c;
+        c = 0u;
+        ++used;
+      }
+      if (used == 3) {
+        refill(m);
+        used = 0;
+      }
       return m;
     };
-    for (int j = 0; j < p.k; ++j) {
-      const uint32_t best = next();
-      open |= j > 0 && !proved(prev >> 8, best >> 8, base_slack);
-      prev = best;
-      const int e = 255 - static_cast<int>(best & 255u);
-      mine = lane == j ? e : mine;
-      if (lane == 0) ids[j] = static_cast<uint8_t>(e);
+    uint32_t prev = next(), gap = 0xffffffffu;
+    uint32_t mine = prev;
+    if (p.k > 32 && lane == 0) ids[0] = static_cast<uint8_t>(255u - (prev & 255u));
+    for (int j = 1; j < p.k; ++j) {
+      const uint32_t m = next();
+      gap = min(gap, prev - m);
+      prev = m;
+      mine = lane == j ? m : mine;
+      if (p.k > 32 && lane == 0) ids[j] = static_cast<uint8_t>(255u - (m & 255u));
     }
-    uint32_t best = next();  // the first one left out
-    open |= !proved(prev >> 8, best >> 8, base_slack);
-    if (open) {  // with every expert that may belong to the first k
-      int n = p.k;
-      for (; n < 32 && !proved(prev >> 8, best >> 8, base_slack); ++n) {
-        mine = lane == n ? 255 - static_cast<int>(best & 255u) : mine;
-        best = next();
-      }
-      exact = n > 32 || !proved(prev >> 8, best >> 8, base_slack);
-      __syncwarp();
-      if (!exact) order_candidates(row, p, mine, n, ids);
-    }
+    uint32_t left = next();  // the first one left out
+    gap = min(gap, prev - left);
+    if (p.k <= 32 && lane < p.k) ids[lane] = static_cast<uint8_t>(255u - (mine & 255u));
     __syncwarp();
+    if (gap <= slack * 256u + 256u) {  // (a difference of q above the slack is a larger gap)
+      // with every expert that may belong to the first k
+      int n = p.k;
+      for (; n < 32 && !proved(prev >> 8, left >> 8, slack); ++n) {
+        mine = lane == n ? left : mine;
+        left = next();
+      }
+      exact = n > 32 || !proved(prev >> 8, left >> 8, slack);
+      if (!exact) order_candidates(row, p, static_cast<int>(255u - (mine & 255u)), n, ids);
+    }
   }
   if (exact) {
     __syncwarp();
     choose_exact(row, p, scratch, scratch + p.epad, ids);
   }
-  return __any_sync(0xffffffffu, bad);
+  return __any_sync(0xffffffffu, nan != 0u);
 }
 
 // Weights of the chosen, in 32 bits.  Renormalised: relative to the largest chosen logit (at
@@ -455,18 +516,19 @@ __device__ __forceinline__ void weigh(const float* row, const RsParams& p, const
     if (!f.sigmoid) return expf(v - top);
     return v > 0.f ? 1.f / (1.f + expf(-v)) : expf(v - top) / (1.f + expf(v));
   };
-  float mul = f.scale;
+  float w = lane < p.k ? weight(ids[lane]) : 0.f, mul = f.scale;
   if (f.renorm) {
-    float wsum = 0.f;
-    for (int j = lane; j < p.k; j += 32) wsum += weight(ids[j]);
+    float wsum = w;
+    for (int j = lane + 32; j < p.k; j += 32) wsum += weight(ids[j]);
     wsum = warp_sum(wsum);
     mul = wsum > 0.f ? f.scale / wsum : 0.f;
   } else if (!f.sigmoid) {
     mul = sum > 0.f ? f.scale / sum : 0.f;
   }
   for (int j = lane; j < p.k; j += 32) {
+    if (j >= 32) w = weight(ids[j]);
     p.topk_ids[static_cast<size_t>(t) * p.k + j] = ids[j];
-    p.topk_w[static_cast<size_t>(t) * p.k + j] = weight(ids[j]) * mul;
+    p.topk_w[static_cast<size_t>(t) * p.k + j] = w * mul;
   }
 }
 
