@@ -8,6 +8,7 @@ there is no fallback: a missing library or a non-OK status raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -106,7 +107,12 @@ def _ptr(t: torch.Tensor | None):
     return t.data_ptr()
 
 
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no stream object is made
+
+
 def _stream(stream=None):
+    if stream is None and _current_raw_stream is not None:
+        return _current_raw_stream(torch.cuda.current_device())
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
 
@@ -182,22 +188,31 @@ def route(adapter_ids: torch.Tensor, k: int, L: int, *, x=None, w_router=None, b
 
 
 def _expect(name: str, t: torch.Tensor | None, shape: tuple, dtype: torch.dtype) -> None:
-    if t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
+    if t is not None and (t.dtype != dtype or t.shape != shape):
         raise ValueError(f"{name} must be {dtype} of shape {shape}, got {t.dtype} of shape {tuple(t.shape)}")
 
 
 def _one_device(*tensors) -> torch.device:
     """The device of all tensors given (None left out): it has to be the current one, since the
     library launches on the current device."""
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"tensors on several devices: {sorted(map(str, devs))}")
-    dev = devs.pop()
-    if dev.type != "cuda":
+    first = None
+    for t in tensors:
+        if t is None:
+            continue
+        if first is None:
+            first = t
+        elif t.get_device() != first.get_device():
+            raise ValueError(f"tensors on several devices: {first.device} and {t.device}")
+    if not first.is_cuda:
         raise ValueError("tensors passed to the library must be CUDA tensors")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-    return dev
+    if first.get_device() != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {first.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return first.device
+
+
+@functools.lru_cache(maxsize=4096)
+def _sized(op: int, M: int, H: int, I: int, E: int, k: int, L: int, r: int) -> int:
+    return workspace_size(op, M, H, I, E, k, L, r)
 
 
 def _used_on(stream, *tensors) -> None:
@@ -234,34 +249,45 @@ def route_scored(adapter_ids: torch.Tensor, k: int, L: int, *, x=None, w_router=
         _expect("bias", bias, (E,), torch.float32)
     _expect("score_bias", score_bias, (E,), torch.float32)
     fmt = RouteFormat(_choice("score", score, SCORES), int(n_group), int(topk_group),
-                      _choice("group_rule", group_rule, GROUP_RULES), 1 if renormalize else 0, float(scale))
+                      _choice("group_rule", group_rule, GROUP_RULES), 1 if renormalize else 0, scale)
     o = out if out is not None else {}
     dev = _one_device(adapter_ids, x, w_router, bias, logits_in, score_bias, workspace, *o.values())
-    made = []
-
-    def buf(name, shape, dtype):
+    # what the caller did not pass is cut from one buffer, in pieces of whole 256 bytes
+    shapes = {"topk_ids": (M, k), "topk_w": (M, k), "sorted_pairs": (M * k,), "seg_offsets": (E * (L + 1) + 1,)}
+    if want_logits:
+        shapes["logits"] = (M, E)
+    need = 0 if workspace is not None else max(_sized(OP_ROUTE_SCORED, M, H, 0, E, k, L, 0), 256) // 4
+    place, total = {}, need
+    for name, shape in shapes.items():
         t = o.get(name)
+        n = shape[0] * shape[1] if len(shape) == 2 else shape[0]
+        dtype = torch.float32 if name in ("topk_w", "logits") else torch.int32
         if t is None:
-            made.append(torch.empty(shape, dtype=dtype, device=dev))
-            return made[-1]
-        if t.numel() < torch.Size(shape).numel() or t.dtype != dtype:
-            raise ValueError(f"out[{name!r}] must be {dtype} with at least {torch.Size(shape).numel()} elements")
-        return t
-
-    ids = buf("topk_ids", (M, k), torch.int32)
-    w = buf("topk_w", (M, k), torch.float32)
-    sp = buf("sorted_pairs", (M * k,), torch.int32)
-    so = buf("seg_offsets", (E * (L + 1) + 1,), torch.int32)
-    lg = buf("logits", (M, E), torch.float32) if want_logits else None
+            place[name] = total
+            total += (n + 63) // 64 * 64
+        elif t.numel() < n or t.dtype != dtype:
+            raise ValueError(f"out[{name!r}] must be {dtype} with at least {n} elements")
+    made = []
+    if total:
+        made.append(torch.empty(total, dtype=torch.int32, device=dev))
+    got = {}
+    for name, shape in shapes.items():
+        if name not in place:
+            got[name] = o[name]
+            continue
+        t = made[0].as_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), place[name])
+        got[name] = t.view(torch.float32) if name in ("topk_w", "logits") else t
     if workspace is None:
-        workspace = new_workspace(workspace_size(OP_ROUTE_SCORED, M, H, 0, E, k, L, 0), dev)
-        made.append(workspace)
+        workspace = made[0].as_strided((need,), (1,), 0).view(torch.uint8)
+    lg = got.get("logits")
+    ids, w, sp, so = got["topk_ids"], got["topk_w"], got["sorted_pairs"], got["seg_offsets"]
     _check(lib().moe_lora_route_scored(
         _ptr(x), _ptr(w_router), _ptr(bias), _ptr(logits_in), _ptr(score_bias), _ptr(adapter_ids), M, H, E, k, L,
         ctypes.byref(fmt), _ptr(lg), _ptr(ids), _ptr(w), _ptr(sp), _ptr(so), _ptr(workspace), workspace.numel(),
         _stream(stream)))
     _used_on(stream, *made)
-    res = {"topk_ids": ids, "topk_w": w, "sorted_pairs": sp[: M * k], "seg_offsets": so, "workspace": workspace}
+    res = {"topk_ids": ids, "topk_w": w, "sorted_pairs": sp if sp.numel() == M * k else sp[: M * k],
+           "seg_offsets": so, "workspace": workspace}
     if want_logits:
         res["logits"] = lg
     return res
@@ -376,7 +402,7 @@ def dense_lora_fused(x, w, lora_a=None, lora_b=None, seg_offsets=None, seg_adapt
         y = torch.empty((T, h_out), dtype=dt, device=dev)
         made.append(y)
     if workspace is None:
-        workspace = new_workspace(workspace_size(OP_DENSE_FUSED, T, h_in, h_out, 1, 1, L, r), dev)
+        workspace = new_workspace(_sized(OP_DENSE_FUSED, T, h_in, h_out, 1, 1, L, r), dev)
         made.append(workspace)
     _check(lib().dense_lora_fused(_ptr(x), _ptr(w), _ptr(bias), _ptr(lora_a) if L else None,
                                   _ptr(lora_b) if L else None, _ptr(seg_offsets), _ptr(seg_adapter), S, T, h_in,

@@ -29,7 +29,7 @@ constexpr int kRsThreads = 512;
 constexpr int kRsWarps = kRsThreads / 32;
 constexpr int kRsMaxStages = 8;
 constexpr int kRsRing = 196608;  // bytes of the ring at most
-constexpr int kRsBody = 128 * 260 * 4 + kRsWarps * 256 * 16;  // of its later use: logits, two doubles per warp and expert
+constexpr int kRsBody = 128 * 260 * 4 + kRsWarps * 256 * 16;  // of its later use: logits, two words per warp and expert
 static_assert(kRsBody >= kRsRing, "the dynamic shared memory of the largest case");
 
 struct RsParams {
@@ -61,6 +61,7 @@ struct RsCore {
   uint32_t tmem_base;
   int abort_flag;
   int flag;
+  int next;  // token that no warp has taken yet
   int scan[kRsWarps];
   float score_bias[256];
   alignas(16) uint4 map[256];  // tokens of the tile (this CTA's: 128 / C of them) by expert
@@ -165,16 +166,19 @@ struct ChoiceSetup {
   }
 };
 
-__device__ __forceinline__ void warp_argmax(double& v, int& e) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const double ov = __shfl_xor_sync(0xffffffffu, v, o);
-    const int oe = __shfl_xor_sync(0xffffffffu, e, o);
-    if (ov > v || (ov == v && oe < e)) {
-      v = ov;
-      e = oe;
-    }
-  }
+// The same for 64-bit scores: larger than 0, the key of "not a candidate".
+__device__ __forceinline__ uint64_t order_key64(double v) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+  return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+}
+
+// the warp's largest key, the smallest index of those that hold it
+__device__ __forceinline__ int warp_argmax(uint64_t key, int at) {
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(key >> 32));
+  const bool same = static_cast<uint32_t>(key >> 32) == hi;
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, same ? static_cast<uint32_t>(key) : 0u);
+  return static_cast<int>(
+      __reduce_min_sync(0xffffffffu, same && static_cast<uint32_t>(key) == lo ? static_cast<uint32_t>(at) : 0xffffffffu));
 }
 
 // Scores in 64 bits.
@@ -225,40 +229,39 @@ __device__ __noinline__ void order_candidates(const float* row, const RsParams& 
 }
 
 // The definition in 64 bits, for tokens whose 32-bit scores lie too close to prove an order.
-// Few instructions rather than few steps: rarely run, its code is read from far.  c: a double
-// of the warp per expert; g: a double per group (n_group > 1 only).
-__device__ __noinline__ void choose_exact(const float* row, const RsParams& p, double* c, double* g, uint8_t* ids) {
+// Few instructions rather than few steps: rarely run, its code is read from far.  c: a key of
+// the warp per expert; g: a key per group (n_group > 1 only).
+__device__ __noinline__ void choose_exact(const float* row, const RsParams& p, uint64_t* c, uint64_t* g, uint8_t* ids) {
   const int lane = threadIdx.x & 31;
   const ScoreFormat& f = p.f;
   const bool by_score = !f.sigmoid && !f.by_logit;
   const float mx = by_score ? row_max(row, p.E) : 0.f;
   const double sum = by_score ? exact_sum(row, p.E, mx) : 1.0;
 #pragma unroll 1
-  for (int e = lane; e < p.E; e += 32) c[e] = exact_selection(row, p, e, mx, sum);
+  for (int e = lane; e < p.E; e += 32) c[e] = order_key64(exact_selection(row, p, e, mx, sum));
   __syncwarp();
-  // takes the largest of v[0, n), the first of equals; taken: bit i of lane l for 32 i + l
-  auto take = [&](const double* v, int n, unsigned& taken) -> int {
-    double bv = -INFINITY;
-    int bi = 0x7fffffff;
+  // takes the largest of v[0, n), the first of equals
+  auto take = [&](uint64_t* v, int n) -> int {
+    uint64_t best = 0ull;
+    int at = lane;
 #pragma unroll 1
-    for (int i = 0; 32 * i + lane < n; ++i)
-      if (!(taken >> i & 1u) && (bi == 0x7fffffff || v[32 * i + lane] > bv)) {
-        bv = v[32 * i + lane];
-        bi = 32 * i + lane;
+    for (int i = lane; i < n; i += 32)
+      if (v[i] > best) {
+        best = v[i];
+        at = i;
       }
-    warp_argmax(bv, bi);
-    if ((bi & 31) == lane) taken |= 1u << (bi >> 5);
-    return bi;
+    at = warp_argmax(best, at);
+    if ((at & 31) == lane) v[at] = 0ull;
+    return at;
   };
-  unsigned out = 0u;  // this lane's experts that are no candidates (any more)
   if (f.n_group > 1) {
 #pragma unroll 1
     for (int q = lane; q < f.n_group; q += 32) {
-      double m1 = -INFINITY, m2 = -INFINITY;
-      int e1 = q * f.group_size, e2 = e1;
+      uint64_t m1 = 0ull, m2 = 0ull;
+      int e1 = 0, e2 = 0;
 #pragma unroll 1
       for (int e = q * f.group_size; e < (q + 1) * f.group_size; ++e) {
-        const double v = c[e];
+        const uint64_t v = c[e];
         if (v > m1) {
           m2 = m1;
           e2 = e1;
@@ -271,30 +274,34 @@ __device__ __noinline__ void choose_exact(const float* row, const RsParams& p, d
       }
       // scores and biases summed apart, so that groups whose two best have the same scores
       // and the same sum of biases tie, whatever the roundings
-      if (f.top2 && f.group_size > 1 && m2 != -INFINITY) {
-        const double s1 = exact_score(row[e1], f.sigmoid, mx, sum), s2 = exact_score(row[e2], f.sigmoid, mx, sum);
-        const double b1 = p.score_bias ? static_cast<double>(clamp_finite(p.score_bias[e1])) : 0.0;
-        const double b2 = p.score_bias ? static_cast<double>(clamp_finite(p.score_bias[e2])) : 0.0;
-        m1 = (s1 + s2) + (b1 + b2);
-      } else if (f.top2 && f.group_size > 1) {
-        m1 = m2;
+      if (f.top2 && f.group_size > 1) {
+        if (m2 == order_key64(-INFINITY)) {  // a NaN
+          m1 = m2;
+        } else {
+          const double s1 = exact_score(row[e1], f.sigmoid, mx, sum), s2 = exact_score(row[e2], f.sigmoid, mx, sum);
+          const double b1 = p.score_bias ? static_cast<double>(clamp_finite(p.score_bias[e1])) : 0.0;
+          const double b2 = p.score_bias ? static_cast<double>(clamp_finite(p.score_bias[e2])) : 0.0;
+          m1 = order_key64((s1 + s2) + (b1 + b2));
+        }
       }
       g[q] = m1;
     }
     __syncwarp();
-    out = 0xffffffffu;
-    unsigned taken = 0u;
+    unsigned out = 0xffffffffu;  // this lane's experts of groups that are not kept
 #pragma unroll 1
     for (int j = 0; j < f.topk_group; ++j) {
-      const int q = take(g, f.n_group, taken);
+      const int q = take(g, f.n_group);
 #pragma unroll 1
       for (int i = 0; 32 * i + lane < p.E; ++i)
         if ((32 * i + lane) / f.group_size == q) out &= ~(1u << i);
     }
+#pragma unroll 1
+    for (int i = 0; 32 * i + lane < p.E; ++i)
+      if (out >> i & 1u) c[32 * i + lane] = 0ull;
   }
 #pragma unroll 1
   for (int j = 0; j < p.k; ++j) {
-    const int e = take(c, p.E, out);
+    const int e = take(c, p.E);
     if (lane == 0) ids[j] = static_cast<uint8_t>(e);
   }
   __syncwarp();
@@ -302,12 +309,11 @@ __device__ __noinline__ void choose_exact(const float* row, const RsParams& p, d
 
 // The k experts of the token whose logits are row[0, E), in order, into ids; returns whether
 // a NaN was met.  Also the row's largest logit and the sum of its exponentials (softmax).
-// scratch: two doubles of the warp per expert.
+// scratch: two 64-bit words of the warp per expert.
 template <int NI>
 __device__ __forceinline__ bool choose(const float* row, const RsParams& p, const ChoiceSetup<NI>& cs, float* copy_to,
-                                       double* scratch, uint8_t* ids, float& mx, float& sum) {
+                                       uint64_t* scratch, uint8_t* ids, float& mx, float& sum) {
   const int lane = threadIdx.x & 31;
-  const int E = p.E;
   const ScoreFormat& f = p.f;
   float v[NI];       // logits, then scores (exponentials, for a softmax)
   uint32_t key[NI];  // q and 255 - expert
@@ -490,6 +496,7 @@ __device__ __forceinline__ bool choose(const float* row, const RsParams& p, cons
   if (exact) {
     __syncwarp();
     choose_exact(row, p, scratch, scratch + p.epad, ids);
+    __syncwarp();
   }
   return __any_sync(0xffffffffu, nan != 0u);
 }
@@ -645,7 +652,7 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   const bool given = p.logits_in != nullptr;
   // logits: the tile's partial sums [128][pitch], or a row per warp of given ones
   float* part = reinterpret_cast<float*>(ring);
-  double* scratch = reinterpret_cast<double*>(ring + static_cast<size_t>(given ? kRsWarps : 128) * pitch * 4) +
+  uint64_t* scratch = reinterpret_cast<uint64_t*>(ring + static_cast<size_t>(given ? kRsWarps : 128) * pitch * 4) +
                     warp * 2 * p.epad;
   volatile int* abort_flag = &sm.abort_flag;
   pdl_trigger();  // the sort of a large batch may be launched
@@ -653,6 +660,7 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   if (tid == 0) {
     sm.abort_flag = 0;
     sm.flag = kRsClean;
+    sm.next = kRsWarps;
     if (!given) {
       for (int s = 0; s < p.stages; ++s) {
         mbar_init(&sm.full[s], 1);
@@ -824,9 +832,11 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   // ---- a warp per token
   ChoiceSetup<NI> cs;
   cs.make(p, sm.score_bias);
-  for (int i = warp; i < TC; i += kRsWarps) {
+  // (the next token goes to the first warp that is free: some take longer)
+  for (int i = warp, after = 0; i < TC; i = __shfl_sync(0xffffffffu, after, 0)) {
     const int t = t0 + own0 + i;
     if (t >= p.M) break;
+    if (lane == 0) after = TC > kRsWarps ? atomicAdd(&sm.next, 1) : TC;
     const float* row = part + (own0 + i) * pitch;
     const int a = p.adapter_ids[t];
     if (given) {
