@@ -520,8 +520,8 @@ __device__ __forceinline__ void weigh(const float* row, const RsParams& p, const
   auto weight = [&](int e) -> float {
     const float raw = row[e], v = clamp_finite(raw);
     if (raw != raw) return 0.f;
-    if (!f.sigmoid) return expf(v - top);
-    return v > 0.f ? 1.f / (1.f + expf(-v)) : expf(v - top) / (1.f + expf(v));
+    const float num = f.sigmoid && v > 0.f ? 1.f : expf(v - top);
+    return f.sigmoid ? num / (1.f + expf(-fabsf(v))) : num;
   };
   float w = lane < p.k ? weight(ids[lane]) : 0.f, mul = f.scale;
   if (f.renorm) {
@@ -541,33 +541,23 @@ __device__ __forceinline__ void weigh(const float* row, const RsParams& p, const
 
 // ------------------------------------------------------------------ the stable sort
 // Slot of expert e among token t's k choices (the token chose it); written by this kernel's
-// peers or the kernel ahead.
+// peers or the kernel ahead.  No early exit: the loads of several calls overlap.
 __device__ __forceinline__ int slot_of_expert(const int32_t* topk_ids, int t, int k, int e) {
   const int32_t* row = topk_ids + static_cast<size_t>(t) * k;
-  if ((k & 3) == 0) {
-    for (int q0 = 0; q0 < k; q0 += 16) {
-      int4 v[4];
+  int at = 0;
+  if ((k & 3) == 0 && k <= 16) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q0 + 4 * q < k) v[q] = __ldcg(reinterpret_cast<const int4*>(row + q0) + q);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q0 + 4 * q < k) {
-          const int at = v[q].x == e ? 0 : v[q].y == e ? 1 : v[q].z == e ? 2 : v[q].w == e ? 3 : -1;
-          if (at >= 0) return q0 + 4 * q + at;
-        }
+    for (int q = 0; q < 4; ++q) {
+      if (4 * q >= k) break;
+      const int4 v = __ldcg(reinterpret_cast<const int4*>(row) + q);
+      at = v.x == e ? 4 * q : v.y == e ? 4 * q + 1 : v.z == e ? 4 * q + 2 : v.w == e ? 4 * q + 3 : at;
     }
-    return 0;
+    return at;
   }
-  for (int j0 = 0; j0 < k; j0 += 8) {
-    int v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __ldcg(row + min(j0 + j, k - 1));
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (v[j] == e) return min(j0 + j, k - 1);
-  }
-  return 0;
+#pragma unroll 8
+  for (int j = 0; j < k; ++j)
+    if (__ldcg(row + j) == e) at = j;
+  return at;
 }
 
 __device__ __forceinline__ uint4 ld_cluster_u32x4(uint32_t cluster_addr) {
@@ -625,12 +615,12 @@ __device__ __forceinline__ void warp_offsets(int* run, int n, int base, int32_t*
 }
 
 // Places one warp's pairs of up to 32 tokens in token order (lane = token; chosen: it chose
-// the expert): run[a] is the next free place of adapter a.
-__device__ __forceinline__ void place32(const RsParams& p, bool chosen, int t, int a, int e, int* run) {
+// the expert, as `pair`): run[a] is the next free place of adapter a.
+__device__ __forceinline__ void place32(const RsParams& p, bool chosen, int pair, int a, int* run) {
   const int lane = threadIdx.x & 31;
   const unsigned peers = __match_any_sync(0xffffffffu, chosen ? a : 128 + lane);
   const unsigned before = peers & ((1u << lane) - 1u);
-  if (chosen) p.sorted_pairs[run[a] + __popc(before)] = t * p.k + slot_of_expert(p.topk_ids, t, p.k, e);
+  if (chosen) p.sorted_pairs[run[a] + __popc(before)] = pair;
   __syncwarp();
   if (chosen && before == 0u) run[a] += __popc(peers);
   __syncwarp();
@@ -933,27 +923,36 @@ __global__ void __launch_bounds__(kRsThreads, 1)
     const unsigned* w = reinterpret_cast<const unsigned*>(sm.map + e);
     for (int a = lane; a < LA; a += 32) run[a] = 0;
     __syncwarp();
+    int pair[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int t = q * 32 + lane;
+      pair[q] = w[q] >> lane & 1u ? t * p.k + slot_of_expert(p.topk_ids, t, p.k, e) : -1;
+    }
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       if (w[q] >> lane & 1u) atomicAdd(run + s_ad[q * 32 + lane], 1);
     __syncwarp();
     warp_offsets(run, LA, s_base[e], p.seg_offsets + e * LA);
+#pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (w[q] != 0u) place32(p, w[q] >> lane & 1u, q * 32 + lane, s_ad[q * 32 + lane], e, run);
+      if (w[q] != 0u) place32(p, pair[q] >= 0, pair[q], s_ad[q * 32 + lane], run);
   }
   if (rank == 0 && tid == 0) p.seg_offsets[p.E * LA] = p.M * p.k;
 }
 
 // ------------------------------------------------------------------ sort of large batches
 // A CTA per expert; its warps split the expert's words of 32 tokens and compact the set bits
-// of 32 words at a time into a list, so that sparse experts cost loads for their own pairs
-// only.  Two walks: count by adapter, then place in token order.
+// of up to 32 words at a time into a list, so that sparse experts cost loads for their own
+// pairs only and an expert that every token chose is spread over the CTA.  Two walks: count
+// by adapter, then place in token order.
+constexpr int kRsList = 1024;  // tokens of 32 words
+
 __global__ void __launch_bounds__(kRsThreads) route_scored_sort_kernel(const RsParams p) {
+  extern __shared__ uint32_t s_lists[];  // [kRsWarps][kRsList]: token | slot << 10 | adapter << 18
   __shared__ int s_scan[kRsWarps];
   __shared__ int s_run[kRsWarps][65];
   __shared__ int s_off[65];
-  __shared__ uint16_t s_list[kRsWarps][1024];
-  __shared__ uint8_t s_ad[kRsWarps][512];  // adapters of the list's first tokens
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int e = blockIdx.x, LA = p.L + 1;
   const int words = p.tiles * 4, chunks = p.tiles * p.C;
@@ -974,14 +973,13 @@ __global__ void __launch_bounds__(kRsThreads) route_scored_sort_kernel(const RsP
     }
   }
   const uint32_t* map = reinterpret_cast<const uint32_t*>(p.bitmap) + static_cast<size_t>(e) * words;
-  // each warp's words, whole runs of 32
-  const int runs = (words + 31) / 32;
-  const int r0 = static_cast<int>(static_cast<long long>(runs) * warp / kRsWarps);
-  const int r1 = static_cast<int>(static_cast<long long>(runs) * (warp + 1) / kRsWarps);
-  uint16_t* list = s_list[warp];
+  const int w0 = static_cast<int>(static_cast<long long>(words) * warp / kRsWarps);
+  const int w1 = static_cast<int>(static_cast<long long>(words) * (warp + 1) / kRsWarps);
+  uint32_t* list = s_lists + warp * kRsList;
   int n = 0;
-  auto compact = [&](int r) {  // the run's tokens, relative to its first, in order
-    uint32_t w = r * 32 + lane < words ? map[r * 32 + lane] : 0u;
+  // the tokens of words [r, min(r + 32, w1)) in order, with their slots and adapters
+  auto compact = [&](int r) {
+    uint32_t w = r + lane < w1 ? map[r + lane] : 0u;
     const int c = __popc(w);
     int incl = c;
 #pragma unroll
@@ -991,24 +989,24 @@ __global__ void __launch_bounds__(kRsThreads) route_scored_sort_kernel(const RsP
     }
     n = __shfl_sync(0xffffffffu, incl, 31);
     __syncwarp();
-    for (int at = incl - c; w != 0u; ++at, w &= w - 1u) list[at] = static_cast<uint16_t>(lane * 32 + __ffs(w) - 1);
+    for (int at = incl - c; w != 0u; ++at, w &= w - 1u) list[at] = static_cast<uint32_t>(lane * 32 + __ffs(w) - 1);
     __syncwarp();
-  };
-  auto adapter = [&](int t) -> int {
-    const int a = p.adapter_ids[t];
-    return a >= 0 && a < p.L ? a : p.L;
+#pragma unroll 4
+    for (int i = lane; i < n; i += 32) {
+      const int t = r * 32 + static_cast<int>(list[i]);
+      const int a = p.adapter_ids[t];
+      list[i] |= static_cast<uint32_t>(slot_of_expert(p.topk_ids, t, p.k, e)) << 10 |
+                 static_cast<uint32_t>(a >= 0 && a < p.L ? a : p.L) << 18;
+    }
+    __syncwarp();
   };
   __syncthreads();
   int base = 0;
 #pragma unroll
   for (int w = 0; w < kRsWarps; ++w) base += s_scan[w];
-  for (int r = r0; r < r1; ++r) {
+  for (int r = w0; r < w1; r += 32) {
     compact(r);
-    for (int i = lane; i < n; i += 32) {
-      const int a = adapter(r * 1024 + list[i]);
-      if (i < 512) s_ad[warp][i] = static_cast<uint8_t>(a);
-      atomicAdd(&s_run[warp][a], 1);
-    }
+    for (int i = lane; i < n; i += 32) atomicAdd(&s_run[warp][list[i] >> 18], 1);
   }
   __syncthreads();
   if (tid < LA) {  // counts of the expert by adapter; s_run: the warps' exclusive prefix
@@ -1029,12 +1027,13 @@ __global__ void __launch_bounds__(kRsThreads) route_scored_sort_kernel(const RsP
   __syncthreads();
   for (int a = lane; a < LA; a += 32) s_run[warp][a] += s_off[a];
   __syncwarp();
-  for (int r = r0; r < r1; ++r) {
-    if (r1 - r0 > 1) compact(r);
+  for (int r = w0; r < w1; r += 32) {
+    if (w1 - w0 > 32) compact(r);
     for (int i0 = 0; i0 < n; i0 += 32) {
       const bool in = i0 + lane < n;
-      const int t = in ? r * 1024 + list[i0 + lane] : 0;
-      place32(p, in, t, !in ? 0 : r1 - r0 > 1 || i0 >= 512 ? adapter(t) : s_ad[warp][i0 + lane], e, s_run[warp]);
+      const uint32_t o = in ? list[i0 + lane] : 0u;
+      const int t = r * 32 + static_cast<int>(o & 1023u);
+      place32(p, in, t * p.k + static_cast<int>(o >> 10 & 255u), static_cast<int>(o >> 18), s_run[warp]);
     }
   }
 }
@@ -1134,10 +1133,21 @@ cudaError_t launch_route_scored(const RouteScoredArgs& a, cudaStream_t st) {
                   : a.E <= 128 ? launch_choice<4>(p, tmx, tmw, st)
                                : launch_choice<8>(p, tmx, tmw, st);
   if (e != cudaSuccess || p.tiles == 1) return e != cudaSuccess ? e : cudaGetLastError();
+  constexpr size_t sort_smem = sizeof(uint32_t) * kRsWarps * kRsList;
+  static std::atomic<bool> attr_set[kMaxDevices];
+  const int dev = current_device_index();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(route_scored_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(sort_smem));
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
   ProfScope ps(K_SORT, st);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(a.E);
   cfg.blockDim = dim3(kRsThreads);
+  cfg.dynamicSmemBytes = sort_smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
