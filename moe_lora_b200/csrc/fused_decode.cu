@@ -34,8 +34,7 @@ struct FdParams {
   const int32_t* seg_offsets;
   const int32_t* seg_adapter;
   int* status;
-  int S, T, K, h_out, n, r, L, act, gated, C;
-  int clear_status;  // no shrink kernel ahead: this kernel's first thread clears the status
+  int S, T, K, h_out, n, r, L, act, gated, C, stages;
 };
 
 struct FdCore {
@@ -52,11 +51,7 @@ template <int BN>
 struct FdCfg {
   static constexpr int kStageBytes = 128 * 128 + BN * 128;
   static constexpr int kTmemCols = BN < 32 ? 32 : BN;
-  // two CTAs per SM up to 128 tokens (108 KB of ring each), one above
-  static constexpr int kBudget = BN <= 128 ? 108 * 1024 : 200 * 1024;
-  static constexpr int kStages = kBudget / kStageBytes < kFdMaxStages ? kBudget / kStageBytes : kFdMaxStages;
   static constexpr int kPart = BN * kFdPitch * 4;
-  static constexpr int kRing = kStages * kStageBytes > kPart ? kStages * kStageBytes : kPart;
 };
 
 template <int BN>
@@ -69,7 +64,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
   float* part = reinterpret_cast<float*>(ring);  // [BN][kFdPitch], once the ring is idle
   __shared__ FdCore sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int S = Cfg::kStages;
+  const int S = p.stages;
   volatile int* abort_flag = &sm.abort_flag;
   const int rank = static_cast<int>(blockIdx.x) % p.C;
   const int tile = static_cast<int>(blockIdx.x) / p.C;
@@ -94,22 +89,34 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
     fence_mbarrier_init();
     tma_prefetch_desc(&tmw);
     tma_prefetch_desc(&tmx);
-    if (p.clear_status && blockIdx.x == 0) p.status[0] = 0;
   }
   if (warp == 1) tmem_alloc(&sm.tmem_base, Cfg::kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  if (p.r == 0) {  // the call's only kernel: what ran ahead is done
+    pdl_wait();
+    if (blockIdx.x == 0 && tid == 0) p.status[0] = 0;
+  }
 
   // the tokens' adapters, looked up by the epilogue warps while the stream starts
   auto adapter_mask = [&]() -> uint64_t {
     if (p.r == 0 || !mbar_wait(&sm.rows, 0, abort_flag, p.status, kFtWaitNs, 57)) return 0ull;
     return sm.mask[0] | (static_cast<uint64_t>(sm.mask[1]) << 32);
   };
-  // the adapters' K columns come after three quarters of the CTA's K blocks: late enough for
-  // the shrink kernel to be done, early enough to hide behind the rest of the stream
-  const int kbz = kb0 + (kb1 - kb0) * 3 / 4;
+  // The adapters' K columns come one group at a time between the K blocks of the second half:
+  // late enough for the shrink kernel to be done, far enough apart that the weight stream never
+  // waits for a group's z.  group_at(j): K block that this CTA's j-th group follows.
+  const int kbz = kb0 + (kb1 - kb0) / 2;
+  auto group_step = [&](const AdapterGroups& g) -> int {  // K blocks between two groups
+    if (p.r == 0) return 1;
+    const int cap = p.r > 64 ? 1 : 64 / p.r, cnt = __popcll(g.rem);
+    const int total = p.r > 64 ? 2 * cnt : (cnt + cap - 1) / cap;
+    const int mine = (total + p.C - 1 - rank) / p.C;
+    return mine > 0 ? (kb1 - kbz) / mine : 1;
+  };
+  auto group_at = [&](int j, int step) -> int { return min(kbz + j * step, kb1 - 1); };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -124,6 +131,9 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
           phase ^= 1u;
         }
       };
+      AdapterGroups g(0ull, p.r);
+      int j = 0, step = 1;
+      bool more = false;
       for (int kb = kb0; ok && kb < kb1; ++kb) {
         ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 50);
         if (!ok) break;
@@ -133,10 +143,13 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
         tma_load_2d(s + 64 * 128, &tmw, &sm.full[stage], kb * 64, row1);
         tma_load_2d(s + 128 * 128, &tmx, &sm.full[stage], kb * 64, 0);
         advance();
-        if (kb != kbz) continue;
-        AdapterGroups g(adapter_mask(), p.r);
-        for (int gi = 0; ok && g.next(); ++gi) {
-          if (gi % p.C != rank) continue;
+        if (kb < kbz) continue;
+        if (kb == kbz) {
+          g.start(adapter_mask());
+          step = group_step(g);
+          more = g.next_of(rank, p.C);
+        }
+        for (; ok && more && group_at(j, step) == kb; ++j, more = g.next_of(0, p.C)) {
           ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 51);
           if (!ok) break;
           mbar_arrive(&sm.zgo[stage]);  // the z tile may be written
@@ -176,6 +189,9 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
         }
       };
       const uint32_t zdesc = umma_idesc_bf16_amn(128, n_mma);
+      AdapterGroups g(0ull, p.r);
+      int j = 0, step = 1;
+      bool more = false;
       for (int kb = kb0; ok && kb < kb1; ++kb) {
         ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 52);
         if (!ok) break;
@@ -185,11 +201,14 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) umma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
         advance();
-        if (kb != kbz) continue;
+        if (kb < kbz) continue;
+        if (kb == kbz) {
+          g.start(adapter_mask());
+          step = group_step(g);
+          more = g.next_of(rank, p.C);
+        }
         // adapters: A = B_a^T, MN-major (64-feature blocks 8 KB apart), 16 rank rows per step
-        AdapterGroups g(adapter_mask(), p.r);
-        for (int gi = 0; ok && g.next(); ++gi) {
-          if (gi % p.C != rank) continue;
+        for (; ok && more && group_at(j, step) == kb; ++j, more = g.next_of(0, p.C)) {
           ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 53) &&
                mbar_wait(&sm.zfull[stage], static_cast<uint32_t>(zi >> stage) & 1u, abort_flag, p.status, kFtWaitNs, 54);
           if (!ok) break;
@@ -222,15 +241,17 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
         sm.row_ad[t] = a;
       }
       mbar_arrive(&sm.rows);
-      // the stage and lap that follow the K blocks up to kbz
-      int stage = (kbz + 1 - kb0) % S;
-      uint32_t lap = static_cast<uint32_t>((kbz + 1 - kb0) / S) & 1u, zi = 0;
       AdapterGroups g(adapter_mask(), p.r);
+      const int step = group_step(g);
+      uint32_t zi = 0;
       ZTile<128, BN / 16> zt;
       zt.rows(sm.row_ad, 0, BN, e);
       bool ok = true, waited = false;
-      for (int gi = 0; ok && g.next(); ++gi) {
-        if (gi % p.C != rank) continue;
+      int j = 0;
+      for (bool more = g.next_of(rank, p.C); ok && more; ++j, more = g.next_of(0, p.C)) {
+        const int at = group_at(j, step) + 1 - kb0 + j;  // ring stages ahead of this one
+        const int stage = at % S;
+        const uint32_t lap = static_cast<uint32_t>(at / S) & 1u;
         if (!waited) pdl_wait();  // z comes from the shrink kernel
         waited = true;
         zt.load(g, p.z, 0, p.r, e);
@@ -275,10 +296,6 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
         }
         fence_proxy_async_smem();
         mbar_arrive(&sm.zfull[stage]);
-        if (++stage == S) {
-          stage = 0;
-          lap ^= 1u;
-        }
       }
     }
     bool got = mbar_wait(&sm.tfull, 0, abort_flag, p.status, kFtWaitNs, 56);
@@ -301,6 +318,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
 
   // tokens rank, rank + C, ...: a warp per token, 4 features per lane (gated: lanes 0-15 the
   // gate's 64 features, lanes 16-31 the up projection's)
+  pdl_trigger();  // a call behind this one may set itself up
   if (p.r) pdl_wait();  // the call ends behind the shrink kernel, whatever the tokens need of it
   if (!*abort_flag) {
     const int col = p.gated ? ((lane < 16 ? 0 : p.h_out) + f0 + 4 * (lane & 15)) : f0 + 4 * lane;  // row of W
@@ -321,20 +339,33 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
         bad |= ld_cluster_u64(mapa_shared(smem_u32(sm.broken), static_cast<uint32_t>(c)));
         bad_up |= ld_cluster_u64(mapa_shared(smem_u32(sm.broken + 2), static_cast<uint32_t>(c)));
       }
-    for (int t = rank + p.C * warp; t < p.T; t += p.C * (kFdThreads / 32)) {
-      const bool writer = in && (!p.gated || lane < 16);
-      uint2 res = make_uint2(0u, 0u);
-      if (p.residual != nullptr && writer)
-        res = *reinterpret_cast<const uint2*>(p.residual + static_cast<size_t>(t) * p.h_out + feat);
+    // the next token's partial sums are on their way while one is finished
+    const int t_step = p.C * (kFdThreads / 32);
+    const bool writer = in && (!p.gated || lane < 16);
+    float4 v[8];
+    uint2 res_next = make_uint2(0u, 0u);
+    auto fetch = [&](int t) {
+      if (t >= p.T) return;
       const uint32_t at = smem_u32(part + t * kFdPitch + 4 * lane);
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < p.C) v[c] = ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(c)));
+      if (p.residual != nullptr && writer)
+        res_next = *reinterpret_cast<const uint2*>(p.residual + static_cast<size_t>(t) * p.h_out + feat);
+    };
+    fetch(rank + p.C * warp);
+    for (int t = rank + p.C * warp; t < p.T; t += t_step) {
       float h[4] = {b[0], b[1], b[2], b[3]};
-      for (int c = 0; c < p.C; ++c) {
-        const float4 v = ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(c)));
-        h[0] += v.x;
-        h[1] += v.y;
-        h[2] += v.z;
-        h[3] += v.w;
-      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < p.C) {
+          h[0] += v[c].x;
+          h[1] += v[c].y;
+          h[2] += v[c].z;
+          h[3] += v[c].w;
+        }
+      const uint2 res = res_next;
+      fetch(t + t_step);
       if ((bad | bad_up) != 0) {  // an adapter with values that are not finite: its own tokens only
         const int ad = sm.row_ad[t];
         const bool lo = ad >= 0 && (bad >> ad & 1ull), up = ad >= 0 && (bad_up >> ad & 1ull);
@@ -399,20 +430,33 @@ static cudaError_t launch_bn(const FusedTcArgs& f, cudaStream_t st) {
   p.r = a.r;
   p.act = a.act;
   p.gated = a.act == ML_ACT_SILU_AND_MUL;
-  p.clear_status = a.r == 0;
   const int tiles = p.gated ? (a.h_out + 63) / 64 : (a.h_out + 127) / 128;
-  // K splits: as many as keep one wave (a second wave starts its stream anew: 64 x 4096 ->
-  // 2 x 11008 in 41 us with C = 1, 172 CTAs for 296 slots, 47 us with C = 2; 4096 -> 11008 for
-  // one token 26, 21, 21 and 26 us with C = 1 to 4) and two K blocks per split
-  const int slots = a.num_sms * (BN <= 128 ? 2 : 1), nkb = (a.h_in + 63) / 64;
-  p.C = std::max(1, std::min(std::min(8, slots / tiles), nkb / 2));
-  const size_t smem = 1024 + Cfg::kRing;
+  // CTAs per SM and K splits.  As many splits as keep one wave (a second wave starts its stream
+  // anew: 64 x 4096 -> 2 x 11008 in 41 us with 172 CTAs for 296 slots, 47 us with 344; 4096 ->
+  // 11008 for one token 26, 21, 21 and 26 us with 1 to 4 splits) and two K blocks per split;
+  // of two or three CTAs per SM (one above 128 tokens) what has more of the ring in use.
+  const int nkb = (a.h_in + 63) / 64, most = BN <= 64 ? 3 : BN <= 128 ? 2 : 1;
+  long long in_use = -1;
+  size_t smem = 0;
+  for (int per_sm = BN <= 128 ? 2 : 1; per_sm <= most; ++per_sm) {
+    const int budget = per_sm == 3 ? 72 * 1024 : per_sm == 2 ? 108 * 1024 : 200 * 1024;
+    const int C = std::max(1, std::min(std::min(8, per_sm * a.num_sms / tiles), nkb / 2));
+    const int stages = std::min(kFdMaxStages, budget / Cfg::kStageBytes);
+    const long long bytes = std::min(tiles * C, per_sm * a.num_sms) * static_cast<long long>(stages);
+    if (tiles * C > per_sm * a.num_sms && in_use >= 0) continue;
+    if (bytes > in_use + in_use / 8) {
+      in_use = bytes;
+      p.C = C;
+      p.stages = stages;
+      smem = 1024 + std::max(stages * Cfg::kStageBytes, Cfg::kPart);
+    }
+  }
   static std::atomic<bool> attr_set[kMaxDevices];
   const int dev = current_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     const cudaError_t e = cudaFuncSetAttribute(fused_decode_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+                                               1024 + (BN <= 128 ? 108 : 200) * 1024);
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
@@ -430,7 +474,7 @@ static cudaError_t launch_bn(const FusedTcArgs& f, cudaStream_t st) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = a.r ? 2 : 1;
+  cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, fused_decode_kernel<BN>, tmw, tmx, tmb, p);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();

@@ -40,7 +40,6 @@ struct FpParams {
   int* status;
   int T, K, h_out, n, r, act, gated;
   int tok_tiles, feat_tiles;
-  int clear_status;
 };
 
 struct FpCore {
@@ -89,15 +88,19 @@ __global__ void __launch_bounds__(kFpThreads, 1)
     fence_mbarrier_init();
     tma_prefetch_desc(&tmw);
     tma_prefetch_desc(&tmx);
-    if (p.clear_status && blockIdx.x == 0) p.status[0] = 0;
   }
   if (warp == 1) tmem_alloc_pair(&sm.tmem_base, 512);
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  if (p.r == 0) {  // the call's only kernel: what ran ahead is done
+    pdl_wait();
+    if (blockIdx.x == 0 && tid == 0) p.status[0] = 0;
+  }
 
-  // adapters of a 256-token tile; every role that asks has waited for the shrink kernel
+  // Adapters of a 256-token tile; every role that asks has waited for the shrink kernel.  From a
+  // role's second tile on it asks ahead of the K loop, behind which the mask is needed.
   auto adapter_mask = [&](int tt) -> uint64_t {
     if (p.r == 0) return 0ull;
     uint64_t m = *reinterpret_cast<const volatile uint64_t*>(p.tile_mask + 2 * tt);
@@ -123,6 +126,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
         fp_tile(p, t, tt, ft);
         const int t0 = tt * 256 + static_cast<int>(rank) * 128;
         const int wrow = p.gated ? static_cast<int>(rank) * p.h_out + ft * 128 : ft * 256 + static_cast<int>(rank) * 128;
+        uint64_t mask = t != pair ? adapter_mask(tt) : 0ull;
         for (int kb = 0; kb < nk; ++kb) {
           ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 60);
           if (!ok) break;
@@ -134,8 +138,11 @@ __global__ void __launch_bounds__(kFpThreads, 1)
           advance();
         }
         if (!ok || p.r == 0) continue;
-        pdl_wait();
-        AdapterGroups g(adapter_mask(tt), p.r);
+        if (t == pair) {
+          pdl_wait();
+          mask = adapter_mask(tt);
+        }
+        AdapterGroups g(mask, p.r);
         while (ok && g.next()) {
           ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 61);
           if (!ok) break;
@@ -190,6 +197,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
         fp_tile(p, t, tt, ft);
         const int buf = it & 1;
         const uint32_t d = tmem + buf * 256;
+        uint64_t mask = it != 0 ? adapter_mask(tt) : 0ull;
         ok = mbar_wait(&sm.tempty[buf], (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u, abort_flag, p.status, kFtWaitNs, 62);
         if (!ok) break;
         tc_fence_after();
@@ -205,8 +213,11 @@ __global__ void __launch_bounds__(kFpThreads, 1)
           advance();
         }
         if (ok && p.r) {
-          pdl_wait();
-          AdapterGroups g(adapter_mask(tt), p.r);
+          if (it == 0) {
+            pdl_wait();
+            mask = adapter_mask(tt);
+          }
+          AdapterGroups g(mask, p.r);
           while (ok && g.next()) {
             ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 64) &&
                  mbar_wait_cluster(&sm.zfull[stage], zphase >> stage & 1u, abort_flag, p.status, kFtWaitNs, 65);
@@ -350,6 +361,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
     }
   }
 
+  pdl_trigger();  // a call behind this one may set itself up
   if (p.r) pdl_wait();
   tc_fence_before();
   __syncwarp();
@@ -390,7 +402,6 @@ cudaError_t launch_fused_prefill_tc(const FusedTcArgs& f, cudaStream_t st) {
   p.gated = a.act == ML_ACT_SILU_AND_MUL;
   p.tok_tiles = (a.T + 255) / 256;
   p.feat_tiles = p.gated ? (a.h_out + 127) / 128 : (a.h_out + 255) / 256;
-  p.clear_status = a.r == 0;
   const long long total = static_cast<long long>(p.tok_tiles) * p.feat_tiles;
   const int grid = 2 * static_cast<int>(std::min<long long>(a.num_sms / 2, total));
   const size_t smem = 1024 + kFpStages * kFpStageBytes;
@@ -417,7 +428,7 @@ cudaError_t launch_fused_prefill_tc(const FusedTcArgs& f, cudaStream_t st) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = a.r ? 2 : 1;
+  cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, fused_prefill_kernel, tmw, tmx, tmb, p);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();

@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(kScanThreads) fused_scan_kernel(const ShParams
   __shared__ unsigned s_mask[2], s_bad[2];
   __shared__ int s_wrong, s_ids[64];
   const int tid = threadIdx.x;
+  pdl_wait();  // what ran ahead of the call is done, for the kernels behind this one too
   pdl_trigger();
   if (tid < 2) s_mask[tid] = s_bad[tid] = 0u;
   if (tid == 0) s_wrong = 0x7fffffff;
@@ -106,7 +107,8 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
   float* part = reinterpret_cast<float*>(ring + kShStages * kShStageBytes);  // [128][r + 4]
   __shared__ ShCore sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_trigger();  // the projection streams its weights meanwhile
+  if (p.validate) pdl_wait();  // the call's first kernel: what ran ahead is done
+  pdl_trigger();               // the projection streams its weights meanwhile
 
   const int rank = static_cast<int>(blockIdx.x) % p.C;
   const int group = static_cast<int>(blockIdx.x) / p.C;  // cluster index
@@ -293,6 +295,23 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
   if (warp == 1) tmem_dealloc(tmem, kShN);
 }
 
+// A launch that may start while what runs ahead ends (it waits for that itself).
+template <typename... P, typename... A>
+static cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool scan, cudaStream_t st) {
   const DenseFusedArgs& a = f.a;
   CUtensorMap tmx, tma;
@@ -339,8 +358,8 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool scan, cudaStream_t
   }
   ProfScope ps(K_FUSED_SHRINK, st);
   if (scan) {
-    fused_scan_kernel<<<p.scan_ctas, kScanThreads, 0, st>>>(p);
-    count_launch();
+    const cudaError_t e = launch_behind(fused_scan_kernel, dim3(p.scan_ctas), kScanThreads, st, p);
+    if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(tiles * p.P * p.C);
@@ -355,7 +374,7 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool scan, cudaStream_t
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = scan ? 2 : 1;
+  cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, fused_shrink_kernel, tmx, tma, p);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -372,6 +391,7 @@ __global__ void __launch_bounds__(kSsThreads) fused_shrink_small_kernel(const Sh
   __shared__ float s_red[8][kSsTok * kSsRank];
   __shared__ int s_item[4];  // segment, first token, tokens (0: no such item), any segment wrong
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();  // what ran ahead of the call is done, for the projection too
   pdl_trigger();
   const int i0 = blockIdx.y * kSsRank;
   for (int item = blockIdx.x;; item += gridDim.x) {
@@ -476,10 +496,20 @@ cudaError_t launch_fused_shrink_simt(const FusedTcArgs& f, cudaStream_t st) {
   p.status = a.status;
   ProfScope ps(K_FUSED_SHRINK, st);
   const int items = std::min(a.S, a.T) + a.T / kSsTok;  // one per segment and one per 4 more tokens
-  fused_shrink_small_kernel<<<dim3(items, a.r / kSsRank), kSsThreads, 0, st>>>(
-      p, static_cast<const __nv_bfloat16*>(a.x), static_cast<const __nv_bfloat16*>(a.lora_a));
-  count_launch();
-  return cudaGetLastError();
+  // The projection's CTAs fill an SM's shared memory: an SM that runs this kernel has to be
+  // split that way already, or it is drained first (64 x 11008 -> 4096: the last of them began
+  // 7.6 us late).
+  static std::atomic<bool> attr_set[kMaxDevices];
+  const int dev = current_device_index();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(fused_shrink_small_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                               cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  return launch_behind(fused_shrink_small_kernel, dim3(items, a.r / kSsRank), kSsThreads, st, p,
+                       static_cast<const __nv_bfloat16*>(a.x), static_cast<const __nv_bfloat16*>(a.lora_a));
 }
 
 }  // namespace mlb

@@ -101,6 +101,16 @@ struct AdapterGroups {
   int ids[8];  // adapters of the current group (-2: none)
   int na;      // how many
   __device__ __forceinline__ AdapterGroups(uint64_t mask, int rank) : rem(mask), r(rank), half(0), na(0) {}
+  __device__ __forceinline__ void start(uint64_t mask) { rem = mask; }
+  // groups dealt out over n CTAs: the next of this CTA's (first: skip = its rank, then 0)
+  __device__ __forceinline__ bool next_of(int skip, int n) {
+    if (taken) skip += n - 1;
+    taken = true;
+    for (int i = 0; i < skip; ++i)
+      if (!next()) return false;
+    return next();
+  }
+  bool taken = false;
   // B boxes per 64 features: an odd adapter of rank 8 fills half an MMA step, so its rows come
   // once more and meet zeros of z
   __device__ __forceinline__ int boxes() const { return (r == 8 && (na & 1)) ? na + 1 : na; }

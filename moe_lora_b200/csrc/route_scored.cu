@@ -645,7 +645,6 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   uint64_t* scratch = reinterpret_cast<uint64_t*>(ring + static_cast<size_t>(given ? kRsWarps : 128) * pitch * 4) +
                     warp * 2 * p.epad;
   volatile int* abort_flag = &sm.abort_flag;
-  pdl_trigger();  // the sort of a large batch may be launched
 
   if (tid == 0) {
     sm.abort_flag = 0;
@@ -662,6 +661,8 @@ __global__ void __launch_bounds__(kRsThreads, 1)
       tma_prefetch_desc(&tmw);
     }
   }
+  pdl_wait();  // what ran ahead of the call is done
+  if (p.tiles > 1) pdl_trigger();  // the sort may be launched
   if (tid < 256) {
     sm.map[tid] = make_uint4(0u, 0u, 0u, 0u);
     sm.score_bias[tid] = p.score_bias != nullptr && tid < p.E ? p.score_bias[tid] : 0.f;
@@ -885,6 +886,7 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   }
 
   // ---- up to 128 tokens: the cluster sorts, a warp per expert
+  pdl_trigger();  // a call behind this one may set itself up
   int* run = reinterpret_cast<int*>(scratch);            // next place by adapter, of this warp
   int* s_base = reinterpret_cast<int*>(sm.ids);          // pairs of lower experts (the ids are done)
   uint8_t* s_ad = reinterpret_cast<uint8_t*>(sm.ids) + 1024;  // adapters of the tokens
@@ -1027,6 +1029,7 @@ __global__ void __launch_bounds__(kRsThreads) route_scored_sort_kernel(const RsP
   __syncthreads();
   for (int a = lane; a < LA; a += 32) s_run[warp][a] += s_off[a];
   __syncwarp();
+  pdl_trigger();  // a call behind this one may set itself up
   for (int r = w0; r < w1; r += 32) {
     if (w1 - w0 > 32) compact(r);
     for (int i0 = 0; i0 < n; i0 += 32) {
@@ -1079,13 +1082,15 @@ static cudaError_t launch_choice(const RsParams& p, const CUtensorMap& tmx, cons
   cfg.blockDim = dim3(kRsThreads);
   cfg.dynamicSmemBytes = 1024 + body;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = p.wide ? 2 : p.C;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, route_scored_kernel<NI>, tmx, tmw, p);
   count_launch();
   return e;
