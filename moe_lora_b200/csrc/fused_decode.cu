@@ -55,7 +55,7 @@ struct FdCfg {
 };
 
 template <int BN>
-__global__ void __launch_bounds__(kFdThreads, BN <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
     fused_decode_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmx,
                         const __grid_constant__ CUtensorMap tmb, const FdParams p) {
   using Cfg = FdCfg<BN>;
@@ -458,6 +458,9 @@ static cudaError_t launch_bn(const FusedTcArgs& f, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(fused_decode_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                1024 + (BN <= 128 ? 108 : 200) * 1024);
     if (e != cudaSuccess) return e;
+    const cudaError_t c = cudaFuncSetAttribute(fused_decode_kernel<BN>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                               cudaSharedmemCarveoutMaxShared);
+    if (c != cudaSuccess) return c;
     attr_set[dev].store(true, std::memory_order_release);
   }
   ProfScope ps(K_DENSE_FUSED, st);

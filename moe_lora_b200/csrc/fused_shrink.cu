@@ -386,7 +386,7 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool scan, cudaStream_t
 // CTA takes 4 rank rows of an item, its 8 warps split h_in.
 constexpr int kSsTok = 4, kSsRank = 4, kSsThreads = 256;
 
-__global__ void __launch_bounds__(kSsThreads) fused_shrink_small_kernel(const ShParams p, const __nv_bfloat16* __restrict__ x,
+__global__ void __launch_bounds__(kSsThreads, 4) fused_shrink_small_kernel(const ShParams p, const __nv_bfloat16* __restrict__ x,
                                                                        const __nv_bfloat16* __restrict__ lora_a) {
   __shared__ float s_red[8][kSsTok * kSsRank];
   __shared__ int s_item[4];  // segment, first token, tokens (0: no such item), any segment wrong
