@@ -23,6 +23,8 @@ namespace mlb {
 
 constexpr int kFdThreads = 192;
 constexpr int kFdMaxStages = 8;
+constexpr int kGroupStep = 4;  // K blocks between two groups of adapters, at most
+constexpr int kGroupTail = 2;  // ... and behind the last
 constexpr int kFdPitch = 132;  // floats per token row of partial sums (128 features)
 
 struct FdParams {
@@ -105,18 +107,20 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
     if (p.r == 0 || !mbar_wait(&sm.rows, 0, abort_flag, p.status, kFtWaitNs, 57)) return 0ull;
     return sm.mask[0] | (static_cast<uint64_t>(sm.mask[1]) << 32);
   };
-  // The adapters' K columns come one group at a time between the K blocks of the second half:
-  // late enough for the shrink kernel to be done, far enough apart that the weight stream never
-  // waits for a group's z.  group_at(j): K block that this CTA's j-th group follows.
-  const int kbz = kb0 + (kb1 - kb0) / 2;
-  auto group_step = [&](const AdapterGroups& g) -> int {  // K blocks between two groups
-    if (p.r == 0) return 1;
-    const int cap = p.r > 64 ? 1 : 64 / p.r, cnt = __popcll(g.rem);
+  // The adapters' K columns come one group at a time between the last K blocks: late, for the
+  // shrink kernel to be done, and a few blocks apart, so that the weight stream goes on while a
+  // group's z is written.  group_at(j): K block that this CTA's j-th group follows; not before
+  // kbz, where the roles look the tokens' adapters up.
+  const int kbz = kb0 + (kb1 - kb0) / 4;
+  int groups = 0, step = 1;
+  auto deal = [&](uint64_t mask) {
+    if (p.r == 0) return;
+    const int cap = p.r > 64 ? 1 : 64 / p.r, cnt = __popcll(mask);
     const int total = p.r > 64 ? 2 * cnt : (cnt + cap - 1) / cap;
-    const int mine = (total + p.C - 1 - rank) / p.C;
-    return mine > 0 ? (kb1 - kbz) / mine : 1;
+    groups = (total + p.C - 1 - rank) / p.C;
+    if (groups > 0) step = min(kGroupStep, (kb1 - kbz) / groups);
   };
-  auto group_at = [&](int j, int step) -> int { return min(kbz + j * step, kb1 - 1); };
+  auto group_at = [&](int j) -> int { return max(kbz, kb1 - 1 - kGroupTail - step * (groups - 1 - j)); };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -132,7 +136,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         }
       };
       AdapterGroups g(0ull, p.r);
-      int j = 0, step = 1;
+      int j = 0;
       bool more = false;
       for (int kb = kb0; ok && kb < kb1; ++kb) {
         ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 50);
@@ -146,10 +150,10 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         if (kb < kbz) continue;
         if (kb == kbz) {
           g.start(adapter_mask());
-          step = group_step(g);
+          deal(g.rem);
           more = g.next_of(rank, p.C);
         }
-        for (; ok && more && group_at(j, step) == kb; ++j, more = g.next_of(0, p.C)) {
+        for (; ok && more && group_at(j) == kb; ++j, more = g.next_of(0, p.C)) {
           ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 51);
           if (!ok) break;
           mbar_arrive(&sm.zgo[stage]);  // the z tile may be written
@@ -190,7 +194,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
       };
       const uint32_t zdesc = umma_idesc_bf16_amn(128, n_mma);
       AdapterGroups g(0ull, p.r);
-      int j = 0, step = 1;
+      int j = 0;
       bool more = false;
       for (int kb = kb0; ok && kb < kb1; ++kb) {
         ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 52);
@@ -204,11 +208,11 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         if (kb < kbz) continue;
         if (kb == kbz) {
           g.start(adapter_mask());
-          step = group_step(g);
+          deal(g.rem);
           more = g.next_of(rank, p.C);
         }
         // adapters: A = B_a^T, MN-major (64-feature blocks 8 KB apart), 16 rank rows per step
-        for (; ok && more && group_at(j, step) == kb; ++j, more = g.next_of(0, p.C)) {
+        for (; ok && more && group_at(j) == kb; ++j, more = g.next_of(0, p.C)) {
           ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 53) &&
                mbar_wait(&sm.zfull[stage], static_cast<uint32_t>(zi >> stage) & 1u, abort_flag, p.status, kFtWaitNs, 54);
           if (!ok) break;
@@ -242,14 +246,14 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
       }
       mbar_arrive(&sm.rows);
       AdapterGroups g(adapter_mask(), p.r);
-      const int step = group_step(g);
+      deal(g.rem);
       uint32_t zi = 0;
       ZTile<128, BN / 16> zt;
       zt.rows(sm.row_ad, 0, BN, e);
       bool ok = true, waited = false;
       int j = 0;
       for (bool more = g.next_of(rank, p.C); ok && more; ++j, more = g.next_of(0, p.C)) {
-        const int at = group_at(j, step) + 1 - kb0 + j;  // ring stages ahead of this one
+        const int at = group_at(j) + 1 - kb0 + j;  // ring stages ahead of this one
         const int stage = at % S;
         const uint32_t lap = static_cast<uint32_t>(at / S) & 1u;
         if (!waited) pdl_wait();  // z comes from the shrink kernel

@@ -354,6 +354,10 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool scan, cudaStream_t
     const cudaError_t e = cudaFuncSetAttribute(fused_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                1024 + kShStages * kShStageBytes + 128 * (128 + 4) * 4);
     if (e != cudaSuccess) return e;
+    // (SMs that run the scan are split as the kernels behind it need them: see launch_small)
+    const cudaError_t c = cudaFuncSetAttribute(fused_scan_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                               cudaSharedmemCarveoutMaxShared);
+    if (c != cudaSuccess) return c;
     attr_set[dev].store(true, std::memory_order_release);
   }
   ProfScope ps(K_FUSED_SHRINK, st);
@@ -386,10 +390,11 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool scan, cudaStream_t
 // CTA takes 4 rank rows of an item, its 8 warps split h_in.
 constexpr int kSsTok = 4, kSsRank = 4, kSsThreads = 256;
 
-__global__ void __launch_bounds__(kSsThreads, 4) fused_shrink_small_kernel(const ShParams p, const __nv_bfloat16* __restrict__ x,
+template <int CTAS, int AHEAD>
+__global__ void __launch_bounds__(kSsThreads, CTAS) fused_shrink_small_kernel(const ShParams p, const __nv_bfloat16* __restrict__ x,
                                                                        const __nv_bfloat16* __restrict__ lora_a) {
   __shared__ float s_red[8][kSsTok * kSsRank];
-  __shared__ int s_item[4];  // segment, first token, tokens (0: no such item), any segment wrong
+  __shared__ int s_item[5];  // segment, first token, tokens (0: no such item), any segment wrong, adapter
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();  // what ran ahead of the call is done, for the projection too
   pdl_trigger();
@@ -422,6 +427,7 @@ __global__ void __launch_bounds__(kSsThreads, 4) fused_shrink_small_kernel(const
           s_item[0] = s;
           s_item[1] = lo + at * kSsTok;
           s_item[2] = min(kSsTok, hi - lo - at * kSsTok);
+          s_item[4] = a;
         }
         base += __shfl_sync(0xffffffffu, incl, 31);
       }
@@ -438,12 +444,12 @@ __global__ void __launch_bounds__(kSsThreads, 4) fused_shrink_small_kernel(const
     const int seg = s_item[0], t0 = s_item[1], nt = s_item[2];
     const bool wrong = s_item[3];
     if (nt == 0) return;
-    const int a = p.seg_adapter[seg];
+    const int a = s_item[4];
     float acc[kSsRank][kSsTok] = {};
     const int h8 = p.K / 8;
     const uint4* A = reinterpret_cast<const uint4*>(lora_a) + (static_cast<size_t>(a) * p.r + i0) * h8;
     const uint4* X = reinterpret_cast<const uint4*>(x) + static_cast<size_t>(t0) * h8;
-#pragma unroll 2
+#pragma unroll AHEAD
     for (int c = tid; c < h8; c += kSsThreads) {
       uint4 av[kSsRank], xv[kSsTok];
 #pragma unroll
@@ -481,6 +487,32 @@ __global__ void __launch_bounds__(kSsThreads, 4) fused_shrink_small_kernel(const
   }
 }
 
+// one item per segment and one per 4 more tokens
+static int fused_shrink_items(const DenseFusedArgs& a) { return std::min(a.S, a.T) + a.T / kSsTok; }
+
+bool fused_shrink_is_small(const DenseFusedArgs& a) {
+  return static_cast<long long>(fused_shrink_items(a)) * (a.r / kSsRank) <= 2 * a.num_sms;
+}
+
+template <int CTAS, int AHEAD>
+static cudaError_t launch_small(dim3 grid, cudaStream_t st, const ShParams& p, const __nv_bfloat16* x,
+                                const __nv_bfloat16* lora_a) {
+  // The projection's CTAs fill an SM's shared memory: an SM that runs this kernel has to be
+  // split that way already, or it is drained first (64 x 11008 -> 4096: the last of them began
+  // 7.6 us late).
+  static std::atomic<bool> attr_set[kMaxDevices];
+  const int dev = current_device_index();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(fused_shrink_small_kernel<CTAS, AHEAD>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  return launch_behind(fused_shrink_small_kernel<CTAS, AHEAD>, grid, kSsThreads, st, p, x, lora_a);
+}
+
 cudaError_t launch_fused_shrink_simt(const FusedTcArgs& f, cudaStream_t st) {
   const DenseFusedArgs& a = f.a;
   ShParams p{};
@@ -495,21 +527,10 @@ cudaError_t launch_fused_shrink_simt(const FusedTcArgs& f, cudaStream_t st) {
   p.z = f.z;
   p.status = a.status;
   ProfScope ps(K_FUSED_SHRINK, st);
-  const int items = std::min(a.S, a.T) + a.T / kSsTok;  // one per segment and one per 4 more tokens
-  // The projection's CTAs fill an SM's shared memory: an SM that runs this kernel has to be
-  // split that way already, or it is drained first (64 x 11008 -> 4096: the last of them began
-  // 7.6 us late).
-  static std::atomic<bool> attr_set[kMaxDevices];
-  const int dev = current_device_index();
-  if (dev < 0) return cudaErrorInvalidDevice;
-  if (!attr_set[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(fused_shrink_small_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                               cudaSharedmemCarveoutMaxShared);
-    if (e != cudaSuccess) return e;
-    attr_set[dev].store(true, std::memory_order_release);
-  }
-  return launch_behind(fused_shrink_small_kernel, dim3(items, a.r / kSsRank), kSsThreads, st, p,
-                       static_cast<const __nv_bfloat16*>(a.x), static_cast<const __nv_bfloat16*>(a.lora_a));
+  const dim3 grid(fused_shrink_items(a), a.r / kSsRank);
+  // Up to two CTAs per SM: more loads in flight each; above, registers for a third.
+  const __nv_bfloat16 *x = static_cast<const __nv_bfloat16*>(a.x), *la = static_cast<const __nv_bfloat16*>(a.lora_a);
+  return fused_shrink_is_small(a) ? launch_small<2, 3>(grid, st, p, x, la) : launch_small<3, 2>(grid, st, p, x, la);
 }
 
 }  // namespace mlb

@@ -223,6 +223,8 @@ struct FusedTcArgs {
 };
 constexpr int kScanCtasPerSm = 2;
 cudaError_t launch_fused_shrink_simt(const FusedTcArgs& p, cudaStream_t st);
+// the shrink on CUDA cores is two CTAs per SM at most
+bool fused_shrink_is_small(const DenseFusedArgs& a);
 // scan: also record the adapters that are not finite (launch_fused_prefill_tc asks for them)
 cudaError_t launch_fused_shrink_tc(const FusedTcArgs& p, bool scan, cudaStream_t st);
 cudaError_t launch_fused_decode_tc(const FusedTcArgs& p, cudaStream_t st);
