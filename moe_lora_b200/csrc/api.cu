@@ -297,10 +297,12 @@ struct FusedWs {
   int32_t* row_adapter;
   uint64_t* tile_mask;
   uint64_t* bad_part;
+  void* zc;
+  int zc_pitch;
   size_t bytes;
 };
 
-FusedWs fused_layout(void* base, int T, int r) {
+FusedWs fused_layout(void* base, int T, int r, int L) {
   size_t off = kStatusBytes;
   FusedWs w{};
   uint8_t* b = static_cast<uint8_t*>(base);
@@ -312,8 +314,10 @@ FusedWs fused_layout(void* base, int T, int r) {
   w.status = reinterpret_cast<int*>(b);
   w.z = reinterpret_cast<float*>(take(static_cast<size_t>(T) * r * 4));
   w.row_adapter = reinterpret_cast<int32_t*>(take(r ? static_cast<size_t>(T) * 4 : 0));
-  w.tile_mask = reinterpret_cast<uint64_t*>(take(r ? (static_cast<size_t>(T) + 127) / 128 * 8 : 0));
+  w.tile_mask = reinterpret_cast<uint64_t*>(take(r ? (static_cast<size_t>(T) + 255) / 256 * 8 : 0));
   w.bad_part = reinterpret_cast<uint64_t*>(take(r && T ? kFusedScanMax * 8 : 0));
+  w.zc_pitch = (L * r + 63) / 64 * 64;
+  w.zc = take(r && T > kFusedDecodeTokens ? static_cast<size_t>(T) * w.zc_pitch * 2 : 0);
   w.bytes = off;
   return w;
 }
@@ -442,7 +446,7 @@ size_t moe_lora_workspace_size(int op, int M, int H, int I, int E, int k, int L,
       return forward_layout(nullptr, M, H, I, k, L > 0 ? r : 0, false, lora_place(1LL * M * k, E), E * (L + 1))
           .bytes;
     case MOE_LORA_OP_ROUTE_SCORED: return scored_layout(nullptr, M, E).bytes;
-    case MOE_LORA_OP_DENSE_FUSED: return fused_layout(nullptr, M, L > 0 ? r : 0).bytes;
+    case MOE_LORA_OP_DENSE_FUSED: return fused_layout(nullptr, M, L > 0 ? r : 0, L).bytes;
     case MOE_LORA_OP_SGMV_SHRINK:
     case MOE_LORA_OP_SGMV_EXPAND: return kStatusBytes;
     case MOE_LORA_OP_DENSE: {
@@ -1152,7 +1156,7 @@ moe_lora_status dense_lora_fused(const void* x, const void* w, const void* bias,
   ML_REQUIRE(S >= 1 || T == 0 || L == 0, MOE_LORA_ERR_INVALID_ARG, "adapters need segments (S >= 1)");
   ML_REQUIRE(std::isfinite(lora_scale), MOE_LORA_ERR_INVALID_ARG, "lora_scale must be finite");
   const int rr = L > 0 ? r : 0;
-  const FusedWs need = fused_layout(nullptr, T, rr);
+  const FusedWs need = fused_layout(nullptr, T, rr, L);
   moe_lora_status st = check_ws(workspace, workspace_bytes, need.bytes);
   if (st != MOE_LORA_OK) return st;
   if (T == 0) return MOE_LORA_OK;
@@ -1170,7 +1174,7 @@ moe_lora_status dense_lora_fused(const void* x, const void* w, const void* bias,
   st = check_device();
   if (st != MOE_LORA_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  const FusedWs ws = fused_layout(workspace, T, rr);
+  const FusedWs ws = fused_layout(workspace, T, rr, L);
   if (dt == ML_BF16 && !tensor_map_encode_available())
     return fail(MOE_LORA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   // the status word (the first kernel of a bf16 projection clears it itself)
@@ -1197,6 +1201,8 @@ moe_lora_status dense_lora_fused(const void* x, const void* w, const void* bias,
   a.f32 = dt == ML_F32;
   a.z = ws.z;
   a.row_adapter = ws.row_adapter;
+  a.zc = ws.zc;
+  a.zc_pitch = ws.zc_pitch;
   a.tile_mask = ws.tile_mask;
   a.bad_part = ws.bad_part;
   a.status = ws.status;

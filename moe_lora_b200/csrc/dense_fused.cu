@@ -134,10 +134,7 @@ static cudaError_t launch_simt(const DenseFusedArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Token counts up to here take the weight-streaming kernel (all tokens in the MMA's N), more
-// the tiled one.
-constexpr int kDecodeTokens = 256;
-// ... and up to here the adapters' shrink runs on CUDA cores (up to kDecodeTokens where it is
+// Up to here the adapters' shrink runs on CUDA cores (up to kFusedDecodeTokens where it is
 // small: 203 x 2056 -> 1000 with 5 adapters of rank 8: 16.7 us in all, on the tensor cores 18.4)
 constexpr int kSmallTokens = 64;
 
@@ -147,16 +144,18 @@ cudaError_t launch_dense_fused(const DenseFusedArgs& a, cudaStream_t st) {
     FusedTcArgs f{};
     f.a = a;
     f.z = reinterpret_cast<__nv_bfloat16*>(a.z);
+    f.zc = static_cast<__nv_bfloat16*>(a.zc);
+    f.zc_pitch = a.zc_pitch;
     f.tile_mask = a.tile_mask;
     f.bad = reinterpret_cast<uint64_t*>(a.status + 32);  // in the status block
     f.bad_part = a.bad_part;
     if (a.r > 0) {
-      const bool simt = a.T <= kSmallTokens || (a.T <= kDecodeTokens && fused_shrink_is_small(a));
+      const bool simt = a.T <= kSmallTokens || (a.T <= kFusedDecodeTokens && fused_shrink_is_small(a));
       const cudaError_t e = simt ? launch_fused_shrink_simt(f, st)
-                                                : launch_fused_shrink_tc(f, a.T > kDecodeTokens, st);
+                                                : launch_fused_shrink_tc(f, a.T > kFusedDecodeTokens, st);
       if (e != cudaSuccess) return e;
     }
-    return a.T <= kDecodeTokens ? launch_fused_decode_tc(f, st) : launch_fused_prefill_tc(f, st);
+    return a.T <= kFusedDecodeTokens ? launch_fused_decode_tc(f, st) : launch_fused_prefill_tc(f, st);
   }
   if (a.r > 0) {
     ProfScope ps(K_FUSED_SHRINK, st);

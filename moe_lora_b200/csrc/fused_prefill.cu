@@ -10,9 +10,9 @@
 // in flight share the strip in L2.
 //
 // Adapters: h = [x, z] [W; B], the tokens' adapters as extra K columns (see AdapterGroups)
-// behind each tile's K loop: the A operand is the tokens' z, zero in other adapters' columns,
-// the B operand B_a as stored (MN-major).  The first tile waits for the shrink kernel there,
-// behind its K loop (programmatic dependent launch).
+// behind each tile's K loop: the A operand is the tile's z as the shrink kernel laid it out
+// (zero in other adapters' columns), the B operand B_a as stored (MN-major).  A role's first
+// tile waits for the shrink kernel there (programmatic dependent launch).
 #include "fused_tc.cuh"
 #include "prof.h"
 
@@ -21,11 +21,10 @@
 
 namespace mlb {
 
-constexpr int kFpThreads = 384;  // producer, MMA, 8 epilogue warps, 2 z warps
+constexpr int kFpThreads = 320;  // producer, MMA, 8 epilogue warps
 constexpr int kFpStages = 6;
 constexpr int kFpStageBytes = 2 * 128 * 128;
 constexpr int kFpEpiWarps = 8;
-constexpr int kFpZThreads = 64;
 constexpr int kFpBand = 16;  // token tiles per band
 
 struct FpParams {
@@ -43,7 +42,7 @@ struct FpParams {
 };
 
 struct FpCore {
-  uint64_t full[kFpStages], empty[kFpStages], zgo[kFpStages], zfull[kFpStages], tfull[2], tempty[2], tdone;
+  uint64_t full[kFpStages], empty[kFpStages], tfull[2], tempty[2], tdone;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -60,7 +59,8 @@ __device__ __forceinline__ void fp_tile(const FpParams& p, int t, int& tt, int& 
 
 __global__ void __launch_bounds__(kFpThreads, 1)
     fused_prefill_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmx,
-                         const __grid_constant__ CUtensorMap tmb, const FpParams p) {
+                         const __grid_constant__ CUtensorMap tmb, const __grid_constant__ CUtensorMap tmz,
+                         const FpParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ FpCore sm;
@@ -76,8 +76,6 @@ __global__ void __launch_bounds__(kFpThreads, 1)
     for (int s = 0; s < kFpStages; ++s) {
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
-      mbar_init(&sm.zgo[s], 1);
-      mbar_init(&sm.zfull[s], 2);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.tfull[b], 1);
@@ -103,9 +101,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
   // role's second tile on it asks ahead of the K loop, behind which the mask is needed.
   auto adapter_mask = [&](int tt) -> uint64_t {
     if (p.r == 0) return 0ull;
-    uint64_t m = *reinterpret_cast<const volatile uint64_t*>(p.tile_mask + 2 * tt);
-    if (tt * 256 + 128 < p.T) m |= *reinterpret_cast<const volatile uint64_t*>(p.tile_mask + 2 * tt + 1);
-    return m & ~*reinterpret_cast<const volatile uint64_t*>(p.bad);
+    return *reinterpret_cast<const volatile uint64_t*>(p.tile_mask + tt);
   };
 
   if (warp == 0) {
@@ -143,15 +139,16 @@ __global__ void __launch_bounds__(kFpThreads, 1)
           mask = adapter_mask(tt);
         }
         AdapterGroups g(mask, p.r);
-        while (ok && g.next()) {
+        for (int gi = 0; ok && g.next(); ++gi) {
           ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 61);
           if (!ok) break;
-          mbar_arrive(&sm.zgo[stage]);  // the z warps may write the stage's first half
-          uint8_t* s = ring + stage * kFpStageBytes + 128 * 128;
+          uint8_t* s = ring + stage * kFpStageBytes;
           const uint32_t fb = leader(&sm.full[stage]);
           const int rb = p.r < 64 ? p.r : 64;
           const int boxes = g.boxes();
-          if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], static_cast<uint32_t>(4 * boxes * rb) * 128u);
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], 2u * 128u * 128u + static_cast<uint32_t>(4 * boxes * rb) * 128u);
+          tma_load_2d_pair(s, &tmz, fb, gi * 64, t0);
+          s += 128 * 128;
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             if (q >= boxes) break;
@@ -181,7 +178,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       int stage = 0, it = 0;
-      uint32_t phase = 0, zphase = 0;
+      uint32_t phase = 0;
       bool ok = true;
       auto advance = [&]() {
         umma_commit_pair(&sm.empty[stage], 3);
@@ -219,10 +216,8 @@ __global__ void __launch_bounds__(kFpThreads, 1)
           }
           AdapterGroups g(mask, p.r);
           while (ok && g.next()) {
-            ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 64) &&
-                 mbar_wait_cluster(&sm.zfull[stage], zphase >> stage & 1u, abort_flag, p.status, kFtWaitNs, 65);
+            ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 64);
             if (!ok) break;
-            zphase ^= 1u << stage;
             tc_fence_after();
             const uint32_t s = smem_u32(ring + stage * kFpStageBytes);
             const uint64_t ad = umma_desc_sw128(s), bd = umma_desc_mn_sw128(s + 128 * 128, 64 * 128);
@@ -238,7 +233,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
       volatile int dummy = 0;
       mbar_wait(&sm.tdone, 0, &dummy, nullptr, kFtWaitNs, 0);
     }
-  } else if (warp < 2 + kFpEpiWarps) {
+  } else {
     // ------------------------------------------------------------ epilogue: thread = token
     const int g4 = warp & 3;           // TMEM lane quarter this warp may access
     const int half = (warp - 2) >> 2;  // half of the tile's output features
@@ -328,37 +323,6 @@ __global__ void __launch_bounds__(kFpThreads, 1)
         }
       }
     }
-  } else if (p.r) {
-    // ------------------------------------------------------------ z tiles of the adapters
-    const int i = tid - (2 + kFpEpiWarps) * 32;
-    long long sc = 0;  // ring stages so far
-    uint32_t used = 0;  // parity of each stage's uses by the z warps
-    bool ok = true;
-    pdl_wait();
-    ZTile<kFpZThreads, 128 * 8 / kFpZThreads> zt;
-    for (int t = pair; ok && t < total; t += pairs) {
-      int tt, ft;
-      fp_tile(p, t, tt, ft);
-      sc += nk;
-      AdapterGroups g(adapter_mask(tt), p.r);
-      const int t0 = tt * 256 + static_cast<int>(rank) * 128;
-      if (g.rem != 0) zt.rows(p.row_adapter, t0, p.T, i);
-      while (ok && g.next()) {
-        zt.load(g, p.z, t0, p.r, i);
-        const int stage = static_cast<int>(sc % kFpStages);
-        ok = mbar_wait(&sm.zgo[stage], used >> stage & 1u, abort_flag, p.status, kFtWaitNs, 67);
-        used ^= 1u << stage;
-        if (!named_bar_and(1, kFpZThreads, ok)) {
-          ok = false;
-          break;
-        }
-        zt.store(ring + stage * kFpStageBytes, i);
-        fence_proxy_async_smem();
-        named_bar_sync(1, kFpZThreads);
-        if (i == 0) mbar_arrive_cluster(leader(&sm.zfull[stage]));
-        ++sc;
-      }
-    }
   }
 
   pdl_trigger();  // a call behind this one may set itself up
@@ -372,16 +336,19 @@ __global__ void __launch_bounds__(kFpThreads, 1)
 
 cudaError_t launch_fused_prefill_tc(const FusedTcArgs& f, cudaStream_t st) {
   const DenseFusedArgs& a = f.a;
-  CUtensorMap tmw, tmx, tmb;
+  CUtensorMap tmw, tmx, tmb, tmz;
   if (encode_tmap_2d(&tmw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.w, a.h_in, a.n, static_cast<uint64_t>(a.h_in) * 2, 64,
                      128, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
       encode_tmap_2d(&tmx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.h_in, a.T, static_cast<uint64_t>(a.h_in) * 2, 64,
                      128, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  tmb = tmx;
+  tmb = tmz = tmx;
   if (a.r && encode_tmap_2d(&tmb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.lora_b, a.n, static_cast<uint64_t>(a.L) * a.r,
                             static_cast<uint64_t>(a.n) * 2, 64, a.r < 64 ? a.r : 64,
                             CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  if (a.r && encode_tmap_2d(&tmz, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f.zc, f.zc_pitch, a.T,
+                            static_cast<uint64_t>(f.zc_pitch) * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   FpParams p{};
   p.bias = static_cast<const __nv_bfloat16*>(a.bias);
@@ -429,7 +396,7 @@ cudaError_t launch_fused_prefill_tc(const FusedTcArgs& f, cudaStream_t st) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fused_prefill_kernel, tmw, tmx, tmb, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fused_prefill_kernel, tmw, tmx, tmb, tmz, p);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }

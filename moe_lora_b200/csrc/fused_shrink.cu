@@ -3,6 +3,8 @@
 //
 // A tile of 128 tokens fills the MMA's M; its N takes the rank rows of 128 / r of the tile's
 // adapters at a time, so every token meets each of them and keeps the columns of its own.
+// Ahead of the tiled projection z is also laid out as that kernel's operand: the columns of a
+// 256-token tile's adapters side by side, zeros where a token has another one.
 // A cluster of C CTAs splits h_in: each holds fp32 partial sums of all 128 tokens, then adds
 // up 128 / C tokens' partials in rank order from its peers' shared memory (no atomics: the
 // same bits every time).
@@ -31,6 +33,8 @@ struct ShParams {
   float scale;
   const __nv_bfloat16* lora_b;
   __nv_bfloat16* z;
+  __nv_bfloat16* zc;
+  int zc_pitch;
   int32_t* row_adapter;
   uint64_t* tile_mask;
   uint64_t* bad;
@@ -44,8 +48,10 @@ struct ShCore {
   uint64_t full[kShStages], empty[kShStages], tfull, tempty;
   uint32_t tmem_base;
   int abort_flag;
-  unsigned mask[2];
+  unsigned mask[2], own[2];  // adapters of the 256-token tile (no scan: of the 128), of these 128 tokens
+  uint64_t bad;
   int wrong;
+  int ids[16];  // adapters of the chunk
   int row_ad[128];
 };
 
@@ -123,7 +129,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
     mbar_init(&sm.tfull, 1);
     mbar_init(&sm.tempty, 128);
     sm.abort_flag = 0;
-    sm.mask[0] = sm.mask[1] = 0u;
+    sm.mask[0] = sm.mask[1] = sm.own[0] = sm.own[1] = 0u;
     sm.wrong = 0x7fffffff;
     fence_mbarrier_init();
   }
@@ -140,23 +146,38 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
       p.status[1] = sm.wrong != 0x7fffffff ? sm.wrong : 0;
     }
   }
-  if (tid < 128) {
-    const int t = t0 + tid;
+  const bool scan = p.scan_ctas > 0;
+  for (int i = tid; i < (scan ? 256 : 128); i += kShThreads) {  // own tokens, then the other half's
+    const int t = i < 128 ? t0 + i : (t0 ^ 128) + i - 128;
     int a = -1;
     if (t < p.T) {
       const int s = segment_of(p.seg_offsets, p.S, t);
       if (s >= 0) a = p.seg_adapter[s];
       if (a >= p.L || a < 0) a = -1;
-      if (chunk0 == 0 && rank == 0) p.row_adapter[t] = a;
+      if (scan && i < 128 && chunk0 == 0 && rank == 0) p.row_adapter[t] = a;
     }
-    sm.row_ad[tid] = a;
+    if (i < 128) sm.row_ad[i] = a;
     if (a >= 0) atomicOr(&sm.mask[a >> 5], 1u << (a & 31));
+    if (a >= 0 && i < 128) atomicOr(&sm.own[a >> 5], 1u << (a & 31));
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint64_t mask = sm.mask[0] | (static_cast<uint64_t>(sm.mask[1]) << 32);
-  if (tid == 0 && chunk0 == 0 && rank == 0) p.tile_mask[tile] = mask;
+  const uint64_t own = sm.own[0] | (static_cast<uint64_t>(sm.own[1]) << 32);
+  if (scan && warp == 2) {  // what the scan found; this launch ends behind it
+    pdl_wait();
+    uint64_t b = 0ull;
+    for (int i = lane; i < p.scan_ctas; i += 32) b |= *reinterpret_cast<const volatile uint64_t*>(p.bad_part + i);
+    const unsigned lo = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(b));
+    const unsigned hi = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(b >> 32));
+    b = lo | (static_cast<uint64_t>(hi) << 32);
+    if (lane == 0) {
+      sm.bad = b;
+      if (blockIdx.x == 0) *p.bad = b;
+      if (chunk0 == 0 && rank == 0 && (tile & 1) == 0) p.tile_mask[tile >> 1] = mask & ~b;
+    }
+  }
   const uint32_t tmem = sm.tmem_base;
   const int apc = kShN / p.r;  // adapters per chunk
   const int cnt = __popcll(mask);
@@ -170,12 +191,23 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
   bool ok = true;
   uint32_t filled = 0, parity_of = 0;
 
-  for (int ch = chunk0, it = 0; ch < chunks; ch += p.P, ++it) {
+  for (int ch = chunk0, it = 0; ch < chunks; ch += p.P) {
     // the chunk's adapters: bits [ch apc, ch apc + na) of the mask
     uint64_t rem = mask;
     for (int i = 0; i < ch * apc; ++i) rem &= rem - 1;
     const int na = min(apc, cnt - ch * apc);
-    if (warp == 0) {
+    uint64_t here = rem;  // the chunk's adapters, and whether a token of this CTA has one
+    for (int i = 0; i < na; ++i) here &= here - 1;
+    here ^= rem;
+    const bool work = (here & own) != 0ull;
+    if (tid < na) {
+      uint64_t m = rem;
+      for (int i = 0; i < tid; ++i) m &= m - 1;
+      sm.ids[tid] = __ffsll(static_cast<long long>(m)) - 1;
+    }
+    if (!work) {
+      // (the other half's adapters: zeros only)
+    } else if (warp == 0) {
       if (lane == 0) {
         for (int kb = kb0; ok && kb < kb1; ++kb) {
           ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 40);
@@ -252,9 +284,45 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
       }
       mbar_arrive(&sm.tempty);
     }
+    if (work) ++it;
     cluster_sync_all();
     // rows [rank 128 / C, ...): sum over the cluster in rank order
     const int rows = 128 / p.C, q4 = p.r / 4;
+    if (scan) {
+      const uint64_t good = mask & ~sm.bad;
+      const int r8 = p.r / 8, per_row = na * r8;
+      for (int e = tid; e < rows * per_row; e += kShThreads) {
+        const int row = rank * rows + e / per_row, q = e % per_row / r8, j = e % per_row % r8, a = sm.ids[q];
+        const int t = t0 + row;
+        if (t >= p.T) continue;
+        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+        if (sm.row_ad[row] == a) {
+          const uint32_t at = smem_u32(part + row * pitch + 8 * j);
+          float s[8] = {};
+          for (int c = 0; c < p.C; ++c) {
+            const float4 u = ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(c)));
+            const float4 w = ld_cluster_f4(mapa_shared(at + 16u, static_cast<uint32_t>(c)));
+            s[0] += u.x;
+            s[1] += u.y;
+            s[2] += u.z;
+            s[3] += u.w;
+            s[4] += w.x;
+            s[5] += w.y;
+            s[6] += w.z;
+            s[7] += w.w;
+          }
+          o = make_uint4(pack2_bf16(p.scale * s[0], p.scale * s[1]), pack2_bf16(p.scale * s[2], p.scale * s[3]),
+                         pack2_bf16(p.scale * s[4], p.scale * s[5]), pack2_bf16(p.scale * s[6], p.scale * s[7]));
+          *reinterpret_cast<uint4*>(p.z + static_cast<size_t>(t) * p.r + 8 * j) = o;
+        }
+        if (!(good >> a & 1ull)) continue;  // not finite: the projection adds it by itself
+        const int pos = __popcll(good & ((1ull << a) - 1ull));
+        __nv_bfloat16* zt = p.zc + static_cast<size_t>(t) * p.zc_pitch + pos * p.r + 8 * j;
+        *reinterpret_cast<uint4*>(zt) = o;
+        // an odd adapter of rank 8 ends inside an MMA step
+        if (p.r == 8 && !(pos & 1) && pos + 1 == __popcll(good)) reinterpret_cast<uint4*>(zt)[1] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    } else
     for (int e = tid; e < rows * q4; e += kShThreads) {
       const int row = rank * rows + e / q4, i = (e % q4) * 4;
       const int a = sm.row_ad[row];
@@ -281,14 +349,6 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
         volatile int dummy = 0;
         mbar_wait(&sm.full[s], (parity_of >> s) & 1u, &dummy, nullptr, kFtWaitNs / 4, 0);
       }
-  if (p.scan_ctas > 0 && blockIdx.x == 0 && warp == 2) {  // what the scan found; this launch ends behind it
-    pdl_wait();
-    uint64_t b = 0ull;
-    for (int i = lane; i < p.scan_ctas; i += 32) b |= *reinterpret_cast<const volatile uint64_t*>(p.bad_part + i);
-    const unsigned lo = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(b));
-    const unsigned hi = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(b >> 32));
-    if (lane == 0) *p.bad = lo | (static_cast<uint64_t>(hi) << 32);
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -333,6 +393,8 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool scan, cudaStream_t
   p.lora_b = static_cast<const __nv_bfloat16*>(a.lora_b);
   p.z = f.z;
   p.row_adapter = a.row_adapter;
+  p.zc = f.zc;
+  p.zc_pitch = f.zc_pitch;
   p.tile_mask = f.tile_mask;
   p.bad = f.bad;
   p.bad_part = f.bad_part;

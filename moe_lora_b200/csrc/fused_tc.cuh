@@ -57,40 +57,6 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t cluster_addr) {
   return v;
 }
 
-// arrive / wait whose release and acquire reach the whole cluster: for data that one CTA's
-// threads wrote to its shared memory and the leader's MMA reads there
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
-                                                  uint64_t limit_ns, int where) {
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait_cluster(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > limit_ns) {
-      *abort_flag = 1;
-      set_status(status, MOE_LORA_ERR_TIMEOUT, where);
-      return false;
-    }
-  }
-}
-
 // ------------------------------------------------------------------ adapters of a tile
 // The adapters of a token tile as extra K of the product: h = [x, z] [W; B].  A group of 64
 // K columns holds 64 / r adapters (half an adapter for r = 128); a token's z stands in its
@@ -217,7 +183,9 @@ struct ZTile {
 struct FusedTcArgs {
   DenseFusedArgs a;
   __nv_bfloat16* z;        // [T][r]
-  uint64_t* tile_mask;     // adapters of each 128-token tile
+  __nv_bfloat16* zc;       // z of each 256-token tile's adapters (no broken ones) side by side: [T][zc_pitch]
+  int zc_pitch;
+  uint64_t* tile_mask;     // ... those adapters
   uint64_t* bad;           // adapters whose B holds a value that is not finite
   uint64_t* bad_part;      // ... found by each CTA of the scan
 };

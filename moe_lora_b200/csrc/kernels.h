@@ -241,11 +241,16 @@ struct DenseFusedArgs {
   bool f32;
   float* z;                   // workspace [T][r]: scale (x A), fp32 (bf16 projections: bf16)
   int32_t* row_adapter;       // workspace [T]
-  uint64_t* tile_mask;        // workspace (bf16): adapters of each 128-token tile
+  void* zc;                   // workspace (bf16, T > kFusedDecodeTokens): z as a matrix operand
+  int zc_pitch;
+  uint64_t* tile_mask;        // workspace (bf16): adapters of each 256-token tile
   uint64_t* bad_part;         // workspace (bf16): kFusedScanMax words
   int* status;
   int num_sms;
 };
+// Token counts up to here take the weight-streaming kernel (all tokens in the MMA's N), more
+// the tiled one.
+constexpr int kFusedDecodeTokens = 256;
 constexpr int kFusedScanMax = 512;  // CTAs of the adapters' scan at most
 cudaError_t launch_dense_fused(const DenseFusedArgs& a, cudaStream_t st);
 
