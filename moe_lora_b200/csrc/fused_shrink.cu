@@ -1,7 +1,7 @@
 // Shrink of dense_lora_fused on the tensor cores: z_t = c x_t A_a(t), bf16
 // ([vLLM MoE-LoRA page], "O Papel da Multi-LoRA"; split-K, "Otimizações em Nível de Kernel").
 //
-// A tile of 128 tokens fills the MMA's M; its N takes the rank rows of 128 / r of the tile's
+// A tile of 128 tokens fills the MMA's M; its N takes the rank rows of 256 / r of the tile's
 // adapters at a time, so every token meets each of them and keeps the columns of its own.
 // Ahead of the tiled projection z is also laid out as that kernel's operand: the columns of a
 // 256-token tile's adapters side by side, zeros where a token has another one.
@@ -22,9 +22,9 @@
 namespace mlb {
 
 constexpr int kShThreads = 192;
-constexpr int kShStages = 4;
-constexpr int kShN = 128;
-constexpr int kShStageBytes = 2 * 128 * 128;
+constexpr int kShStages = 3;
+constexpr int kShN = 256;
+constexpr int kShStageBytes = (128 + kShN) * 128;
 
 struct ShParams {
   const int32_t* seg_offsets;
@@ -51,7 +51,7 @@ struct ShCore {
   unsigned mask[2], own[2];  // adapters of the 256-token tile (no scan: of the 128), of these 128 tokens
   uint64_t bad;
   int wrong;
-  int ids[16];  // adapters of the chunk
+  int ids[kShN / 8];  // adapters of the chunk
   int row_ad[128];
 };
 
@@ -399,7 +399,7 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool scan, cudaStream_t
   p.bad = f.bad;
   p.bad_part = f.bad_part;
   p.status = a.status;
-  // K splits: as many as keep one wave of CTAs (one per SM: 128 KB of ring each)
+  // K splits: as many as keep one wave of CTAs (one per SM: 144 KB of ring each)
   const int tiles = (a.T + 127) / 128;
   p.C = 8;
   while (p.C > 1 && tiles * p.C > a.num_sms) p.C /= 2;
