@@ -1177,8 +1177,7 @@ moe_lora_status dense_lora_fused(const void* x, const void* w, const void* bias,
   const FusedWs ws = fused_layout(workspace, T, rr, L);
   if (dt == ML_BF16 && !tensor_map_encode_available())
     return fail(MOE_LORA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  // the status word (the first kernel of a bf16 projection clears it itself)
-  if (dt == ML_F32) ML_CUDA(cudaMemsetAsync(workspace, 0, 8, cs), "status clear");
+  // (the call's first kernel writes the status word)
   DenseFusedArgs a{};
   a.x = x;
   a.w = w;

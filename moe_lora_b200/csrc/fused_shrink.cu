@@ -299,18 +299,23 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
         if (sm.row_ad[row] == a) {
           const uint32_t at = smem_u32(part + row * pitch + 8 * j);
           float s[8] = {};
-          for (int c = 0; c < p.C; ++c) {
-            const float4 u = ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(c)));
-            const float4 w = ld_cluster_f4(mapa_shared(at + 16u, static_cast<uint32_t>(c)));
-            s[0] += u.x;
-            s[1] += u.y;
-            s[2] += u.z;
-            s[3] += u.w;
-            s[4] += w.x;
-            s[5] += w.y;
-            s[6] += w.z;
-            s[7] += w.w;
-          }
+          float4 v[2][8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c < p.C) {
+              v[0][c] = ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(c)));
+              v[1][c] = ld_cluster_f4(mapa_shared(at + 16u, static_cast<uint32_t>(c)));
+            }
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c < p.C)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                s[4 * u] += v[u][c].x;
+                s[4 * u + 1] += v[u][c].y;
+                s[4 * u + 2] += v[u][c].z;
+                s[4 * u + 3] += v[u][c].w;
+              }
           o = make_uint4(pack2_bf16(p.scale * s[0], p.scale * s[1]), pack2_bf16(p.scale * s[2], p.scale * s[3]),
                          pack2_bf16(p.scale * s[4], p.scale * s[5]), pack2_bf16(p.scale * s[6], p.scale * s[7]));
           *reinterpret_cast<uint4*>(p.z + static_cast<size_t>(t) * p.r + 8 * j) = o;
