@@ -5,6 +5,8 @@
 #include "fused_tc.cuh"
 #include "prof.h"
 
+#include <algorithm>
+
 namespace mlb {
 
 // ---------------------------------------------------------------- fp32
@@ -262,8 +264,8 @@ cudaError_t launch_dense_fused(const DenseFusedArgs& a, cudaStream_t st) {
     f.zc = static_cast<__nv_bfloat16*>(a.zc);
     f.zc_pitch = a.zc_pitch;
     f.tile_mask = a.tile_mask;
-    f.bad = reinterpret_cast<uint64_t*>(a.status + 32);  // in the status block
     f.bad_part = a.bad_part;
+    f.scan_ctas = std::min(kFusedScanMax, 2 * a.num_sms);
     if (a.r > 0) {
       const bool simt = a.T <= kSmallTokens || (a.T <= kFusedDecodeTokens && fused_shrink_is_small(a));
       const cudaError_t e = simt ? launch_fused_shrink_simt(f, st)

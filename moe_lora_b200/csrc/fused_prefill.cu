@@ -35,14 +35,15 @@ struct FpParams {
   const __nv_bfloat16* lora_b;
   const int32_t* row_adapter;
   const uint64_t* tile_mask;
-  const uint64_t* bad;
+  const uint64_t* bad_part;
   int* status;
-  int T, K, h_out, n, r, act, gated;
+  int T, K, h_out, n, r, L, act, gated, scan_ctas;
   int tok_tiles, feat_tiles;
 };
 
 struct FpCore {
-  uint64_t full[kFpStages], empty[kFpStages], tfull[2], tempty[2], tdone;
+  uint64_t full[kFpStages], empty[kFpStages], tfull[2], tempty[2], tdone, scanned;
+  uint64_t bad;  // adapters whose B holds a value that is not finite
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -82,6 +83,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
       mbar_init(&sm.tempty[b], 2 * kFpEpiWarps);
     }
     mbar_init(&sm.tdone, 1);
+    mbar_init(&sm.scanned, 1);
     sm.abort_flag = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&tmw);
@@ -97,11 +99,10 @@ __global__ void __launch_bounds__(kFpThreads, 1)
     if (blockIdx.x == 0 && tid == 0) p.status[0] = 0;
   }
 
-  // Adapters of a 256-token tile; every role that asks has waited for the shrink kernel.  From a
+  // Adapters of a 256-token tile; every role that asks has waited for the kernels ahead.  From a
   // role's second tile on it asks ahead of the K loop, behind which the mask is needed.
   auto adapter_mask = [&](int tt) -> uint64_t {
-    if (p.r == 0) return 0ull;
-    return *reinterpret_cast<const volatile uint64_t*>(p.tile_mask + tt);
+    return p.r == 0 ? 0ull : *reinterpret_cast<const volatile uint64_t*>(p.tile_mask + tt);
   };
 
   if (warp == 0) {
@@ -137,7 +138,11 @@ __global__ void __launch_bounds__(kFpThreads, 1)
         if (t == pair) {
           pdl_wait();
           mask = adapter_mask(tt);
+          ok = mbar_wait(&sm.scanned, 0, abort_flag, p.status, kFtWaitNs, 65);
         }
+        // An adapter that is not finite stays out of the product: its rows come from behind the
+        // tensor, where they are zero, and the epilogue adds it for its own tokens.
+        const uint64_t bad = sm.bad;
         AdapterGroups g(mask, p.r);
         for (int gi = 0; ok && g.next(); ++gi) {
           ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 61);
@@ -153,8 +158,9 @@ __global__ void __launch_bounds__(kFpThreads, 1)
           for (int q = 0; q < 8; ++q) {
             if (q >= boxes) break;
             const int id = (q > 0 && q >= g.na) ? g.ids[q > 0 ? q - 1 : 0] : g.ids[q];
-            tma_load_2d_pair(s + q * rb * 128, &tmb, fb, wrow, id * p.r + g.k0);
-            tma_load_2d_pair(s + 64 * 128 + q * rb * 128, &tmb, fb, wrow + 64, id * p.r + g.k0);
+            const int row = bad >> id & 1ull ? p.L * p.r : id * p.r + g.k0;
+            tma_load_2d_pair(s + q * rb * 128, &tmb, fb, wrow, row);
+            tma_load_2d_pair(s + 64 * 128 + q * rb * 128, &tmb, fb, wrow + 64, row);
           }
           advance();
         }
@@ -238,6 +244,17 @@ __global__ void __launch_bounds__(kFpThreads, 1)
     const int g4 = warp & 3;           // TMEM lane quarter this warp may access
     const int half = (warp - 2) >> 2;  // half of the tile's output features
     const int width = p.gated ? 64 : 128;
+    if (p.r && warp == 2) {  // what the scan found
+      pdl_wait();
+      uint64_t b = 0ull;
+      for (int i = lane; i < p.scan_ctas; i += 32) b |= *reinterpret_cast<const volatile uint64_t*>(p.bad_part + i);
+      const unsigned lo = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(b));
+      const unsigned hi = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(b >> 32));
+      if (lane == 0) {
+        sm.bad = lo | (static_cast<uint64_t>(hi) << 32);
+        mbar_arrive(&sm.scanned);
+      }
+    }
     int it = 0;
     for (int t = pair; t < total; t += pairs, ++it) {
       int tt, ft;
@@ -251,7 +268,8 @@ __global__ void __launch_bounds__(kFpThreads, 1)
       int bad_ad = -1;
       if (p.r) {
         pdl_wait();
-        const uint64_t bad = *reinterpret_cast<const volatile uint64_t*>(p.bad);
+        mbar_wait(&sm.scanned, 0, abort_flag, p.status, kFtWaitNs, 67);
+        const uint64_t bad = sm.bad;
         if (bad != 0 && row_ok) {
           const int ad = p.row_adapter[tok];
           if (ad >= 0 && (bad >> ad & 1ull)) bad_ad = ad;
@@ -358,7 +376,9 @@ cudaError_t launch_fused_prefill_tc(const FusedTcArgs& f, cudaStream_t st) {
   p.lora_b = static_cast<const __nv_bfloat16*>(a.lora_b);
   p.row_adapter = a.row_adapter;
   p.tile_mask = f.tile_mask;
-  p.bad = f.bad;
+  p.bad_part = f.bad_part;
+  p.scan_ctas = f.scan_ctas;
+  p.L = a.L;
   p.status = a.status;
   p.T = a.T;
   p.K = a.h_in;

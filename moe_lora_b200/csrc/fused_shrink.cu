@@ -9,10 +9,10 @@
 // up 128 / C tokens' partials in rank order from its peers' shared memory (no atomics: the
 // same bits every time).
 //
-// A launch ahead reads the B rows of the adapters in use and records which hold a value that
-// is not finite: the projection keeps those out of its matrix product, where a zero times an
-// infinity would reach other tenants' tokens.  The rows read stay in L2, where the projection
-// finds them.
+// A launch beside it reads the B rows of the adapters in use and records which hold a value
+// that is not finite: the projection keeps those out of its matrix product, where a zero times
+// an infinity would reach other tenants' tokens.  The rows read stay in L2, where the
+// projection finds them.
 #include "fused_tc.cuh"
 #include "prof.h"
 
@@ -37,52 +37,42 @@ struct ShParams {
   int zc_pitch;
   int32_t* row_adapter;
   uint64_t* tile_mask;
-  uint64_t* bad;
   uint64_t* bad_part;
   int* status;
-  int C, P, scan_ctas;
-  int validate;  // no scan ahead: the first CTA checks the segments and clears the status
+  int C, P;
+  int operand;  // the tiled projection follows: zc, row_adapter and tile_mask as well
 };
 
 struct ShCore {
   uint64_t full[kShStages], empty[kShStages], tfull, tempty;
   uint32_t tmem_base;
   int abort_flag;
-  unsigned mask[2], own[2];  // adapters of the 256-token tile (no scan: of the 128), of these 128 tokens
-  uint64_t bad;
+  unsigned mask[2], own[2];  // adapters of the 256-token tile (of the 128 without zc), of these 128 tokens
   int wrong;
   int ids[kShN / 8];  // adapters of the chunk
   int row_ad[128];
 };
 
-// The adapters in use and whether their B rows are finite; the segments checked on the way.
-// First kernel of the call: it clears the status word (one thread writes it, whatever the
-// checks say) and lets the shrink kernel start at once.  Each CTA leaves the adapters that
-// it found broken in a word of its own, so that no counter has to be cleared.
+// Which adapters in use have B rows that are not finite.  Each CTA leaves those that it found
+// in a word of its own, so that no counter has to be cleared.  Launched behind the shrink
+// kernel, which it overlaps and ends behind; the projection launched behind it waits for both.
 constexpr int kScanThreads = 256;
 
 __global__ void __launch_bounds__(kScanThreads) fused_scan_kernel(const ShParams p) {
   __shared__ unsigned s_mask[2], s_bad[2];
-  __shared__ int s_wrong, s_ids[64];
+  __shared__ int s_ids[64];
   const int tid = threadIdx.x;
-  pdl_wait();  // what ran ahead of the call is done, for the kernels behind this one too
   pdl_trigger();
   if (tid < 2) s_mask[tid] = s_bad[tid] = 0u;
-  if (tid == 0) s_wrong = 0x7fffffff;
   __syncthreads();
   for (int s = tid; s < p.S; s += kScanThreads) {
     const int a = p.seg_adapter[s], lo = p.seg_offsets[s], hi = p.seg_offsets[s + 1];
     if (a >= 0 && a < p.L && hi > lo) atomicOr(&s_mask[a >> 5], 1u << (a & 31));
-    if (blockIdx.x == 0 && segment_wrong(lo, hi, a, p.T, p.L)) atomicMin(&s_wrong, s);
   }
   __syncthreads();
   const uint64_t mask = s_mask[0] | (static_cast<uint64_t>(s_mask[1]) << 32);
   const int cnt = __popcll(mask);
   if (tid < 64 && (mask >> tid & 1ull)) s_ids[__popcll(mask & ((1ull << tid) - 1ull))] = tid;
-  if (blockIdx.x == 0 && tid == 0) {
-    p.status[0] = s_wrong != 0x7fffffff ? MOE_LORA_ERR_DEVICE_CHECK : MOE_LORA_OK;
-    p.status[1] = s_wrong != 0x7fffffff ? s_wrong : 0;
-  }
   __syncthreads();
   const size_t chunks = static_cast<size_t>(p.r) * p.n / 8;  // 16 bytes each
   const size_t step = static_cast<size_t>(gridDim.x) * kScanThreads;
@@ -102,6 +92,7 @@ __global__ void __launch_bounds__(kScanThreads) fused_scan_kernel(const ShParams
     }
   }
   __syncthreads();
+  pdl_wait();
   if (tid == 0) p.bad_part[blockIdx.x] = s_bad[0] | (static_cast<uint64_t>(s_bad[1]) << 32);
 }
 
@@ -113,8 +104,8 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
   float* part = reinterpret_cast<float*>(ring + kShStages * kShStageBytes);  // [128][r + 4]
   __shared__ ShCore sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (p.validate) pdl_wait();  // the call's first kernel: what ran ahead is done
-  pdl_trigger();               // the projection streams its weights meanwhile
+  pdl_wait();     // what ran ahead of the call is done, for the kernels behind this one too
+  pdl_trigger();  // the projection streams its weights meanwhile
 
   const int rank = static_cast<int>(blockIdx.x) % p.C;
   const int group = static_cast<int>(blockIdx.x) / p.C;  // cluster index
@@ -135,7 +126,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
   }
   if (warp == 1) tmem_alloc(&sm.tmem_base, kShN);
   __syncthreads();
-  if (p.validate && blockIdx.x == 0) {  // the call's first kernel: its status word
+  if (blockIdx.x == 0) {  // the call's first kernel: its status word
     int wrong = 0x7fffffff;
     for (int s = tid; s < p.S; s += kShThreads)
       if (segment_wrong(p.seg_offsets[s], p.seg_offsets[s + 1], p.seg_adapter[s], p.T, p.L)) wrong = min(wrong, s);
@@ -146,15 +137,15 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
       p.status[1] = sm.wrong != 0x7fffffff ? sm.wrong : 0;
     }
   }
-  const bool scan = p.scan_ctas > 0;
-  for (int i = tid; i < (scan ? 256 : 128); i += kShThreads) {  // own tokens, then the other half's
+  const bool operand = p.operand != 0;
+  for (int i = tid; i < (operand ? 256 : 128); i += kShThreads) {  // own tokens, then the other half's
     const int t = i < 128 ? t0 + i : (t0 ^ 128) + i - 128;
     int a = -1;
     if (t < p.T) {
       const int s = segment_of(p.seg_offsets, p.S, t);
       if (s >= 0) a = p.seg_adapter[s];
       if (a >= p.L || a < 0) a = -1;
-      if (scan && i < 128 && chunk0 == 0 && rank == 0) p.row_adapter[t] = a;
+      if (operand && i < 128 && chunk0 == 0 && rank == 0) p.row_adapter[t] = a;
     }
     if (i < 128) sm.row_ad[i] = a;
     if (a >= 0) atomicOr(&sm.mask[a >> 5], 1u << (a & 31));
@@ -165,19 +156,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
   tc_fence_after();
   const uint64_t mask = sm.mask[0] | (static_cast<uint64_t>(sm.mask[1]) << 32);
   const uint64_t own = sm.own[0] | (static_cast<uint64_t>(sm.own[1]) << 32);
-  if (scan && warp == 2) {  // what the scan found; this launch ends behind it
-    pdl_wait();
-    uint64_t b = 0ull;
-    for (int i = lane; i < p.scan_ctas; i += 32) b |= *reinterpret_cast<const volatile uint64_t*>(p.bad_part + i);
-    const unsigned lo = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(b));
-    const unsigned hi = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(b >> 32));
-    b = lo | (static_cast<uint64_t>(hi) << 32);
-    if (lane == 0) {
-      sm.bad = b;
-      if (blockIdx.x == 0) *p.bad = b;
-      if (chunk0 == 0 && rank == 0 && (tile & 1) == 0) p.tile_mask[tile >> 1] = mask & ~b;
-    }
-  }
+  if (operand && tid == 0 && chunk0 == 0 && rank == 0 && (tile & 1) == 0) p.tile_mask[tile >> 1] = mask;
   const uint32_t tmem = sm.tmem_base;
   const int apc = kShN / p.r;  // adapters per chunk
   const int cnt = __popcll(mask);
@@ -288,8 +267,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
     cluster_sync_all();
     // rows [rank 128 / C, ...): sum over the cluster in rank order
     const int rows = 128 / p.C, q4 = p.r / 4;
-    if (scan) {
-      const uint64_t good = mask & ~sm.bad;
+    if (operand) {
       const int r8 = p.r / 8, per_row = na * r8;
       for (int e = tid; e < rows * per_row; e += kShThreads) {
         const int row = rank * rows + e / per_row, q = e % per_row / r8, j = e % per_row % r8, a = sm.ids[q];
@@ -320,12 +298,11 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
                          pack2_bf16(p.scale * s[4], p.scale * s[5]), pack2_bf16(p.scale * s[6], p.scale * s[7]));
           *reinterpret_cast<uint4*>(p.z + static_cast<size_t>(t) * p.r + 8 * j) = o;
         }
-        if (!(good >> a & 1ull)) continue;  // not finite: the projection adds it by itself
-        const int pos = __popcll(good & ((1ull << a) - 1ull));
+        const int pos = __popcll(mask & ((1ull << a) - 1ull));
         __nv_bfloat16* zt = p.zc + static_cast<size_t>(t) * p.zc_pitch + pos * p.r + 8 * j;
         *reinterpret_cast<uint4*>(zt) = o;
         // an odd adapter of rank 8 ends inside an MMA step
-        if (p.r == 8 && !(pos & 1) && pos + 1 == __popcll(good)) reinterpret_cast<uint4*>(zt)[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (p.r == 8 && !(pos & 1) && pos + 1 == cnt) reinterpret_cast<uint4*>(zt)[1] = make_uint4(0u, 0u, 0u, 0u);
       }
     } else
     for (int e = tid; e < rows * q4; e += kShThreads) {
@@ -377,7 +354,7 @@ static cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, c
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool scan, cudaStream_t st) {
+cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool operand, cudaStream_t st) {
   const DenseFusedArgs& a = f.a;
   CUtensorMap tmx, tma;
   if (encode_tmap_2d(&tmx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.h_in, a.T, static_cast<uint64_t>(a.h_in) * 2, 64,
@@ -401,7 +378,6 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool scan, cudaStream_t
   p.zc = f.zc;
   p.zc_pitch = f.zc_pitch;
   p.tile_mask = f.tile_mask;
-  p.bad = f.bad;
   p.bad_part = f.bad_part;
   p.status = a.status;
   // K splits: as many as keep one wave of CTAs (one per SM: 144 KB of ring each)
@@ -411,8 +387,7 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool scan, cudaStream_t
   // chunks of a tile side by side while SMs are left
   const int apc = kShN / a.r, most = (std::min(std::min(a.L, a.S), 128) + apc - 1) / apc;
   p.P = std::max(1, std::min(most, a.num_sms / (tiles * p.C)));
-  p.validate = !scan;
-  p.scan_ctas = !scan ? 0 : std::min(kFusedScanMax, kScanCtasPerSm * a.num_sms);
+  p.operand = operand;
   const size_t smem = 1024 + kShStages * kShStageBytes + 128u * (a.r + 4) * 4;
   static std::atomic<bool> attr_set[kMaxDevices];
   const int dev = current_device_index();
@@ -428,10 +403,6 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool scan, cudaStream_t
     attr_set[dev].store(true, std::memory_order_release);
   }
   ProfScope ps(K_FUSED_SHRINK, st);
-  if (scan) {
-    const cudaError_t e = launch_behind(fused_scan_kernel, dim3(p.scan_ctas), kScanThreads, st, p);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(tiles * p.P * p.C);
   cfg.blockDim = dim3(kShThreads);
@@ -446,8 +417,9 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool scan, cudaStream_t
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fused_shrink_kernel, tmx, tma, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, fused_shrink_kernel, tmx, tma, p);
   count_launch();
+  if (e == cudaSuccess && operand) return launch_behind(fused_scan_kernel, dim3(f.scan_ctas), kScanThreads, st, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

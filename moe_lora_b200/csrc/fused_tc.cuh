@@ -183,18 +183,17 @@ struct ZTile {
 struct FusedTcArgs {
   DenseFusedArgs a;
   __nv_bfloat16* z;        // [T][r]
-  __nv_bfloat16* zc;       // z of each 256-token tile's adapters (no broken ones) side by side: [T][zc_pitch]
+  __nv_bfloat16* zc;       // z of each 256-token tile's adapters side by side: [T][zc_pitch]
   int zc_pitch;
   uint64_t* tile_mask;     // ... those adapters
-  uint64_t* bad;           // adapters whose B holds a value that is not finite
-  uint64_t* bad_part;      // ... found by each CTA of the scan
+  uint64_t* bad_part;      // adapters whose B holds a value that is not finite, by CTA of the scan
+  int scan_ctas;
 };
-constexpr int kScanCtasPerSm = 2;
 cudaError_t launch_fused_shrink_simt(const FusedTcArgs& p, cudaStream_t st);
 // the shrink on CUDA cores is two CTAs per SM at most
 bool fused_shrink_is_small(const DenseFusedArgs& a);
-// scan: also record the adapters that are not finite (launch_fused_prefill_tc asks for them)
-cudaError_t launch_fused_shrink_tc(const FusedTcArgs& p, bool scan, cudaStream_t st);
+// operand: what launch_fused_prefill_tc asks for as well (zc, the masks, the scan)
+cudaError_t launch_fused_shrink_tc(const FusedTcArgs& p, bool operand, cudaStream_t st);
 cudaError_t launch_fused_decode_tc(const FusedTcArgs& p, cudaStream_t st);
 cudaError_t launch_fused_prefill_tc(const FusedTcArgs& p, cudaStream_t st);
 
