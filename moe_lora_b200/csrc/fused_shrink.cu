@@ -22,9 +22,12 @@
 namespace mlb {
 
 constexpr int kShThreads = 192;
-constexpr int kShStages = 3;
 constexpr int kShN = 256;
-constexpr int kShStageBytes = (128 + kShN) * 128;
+// The ring holds as many stages of a chunk's size as fit, at most kShStages: x is read from HBM
+// once, so what counts is the bytes on their way (4096 tokens with one adapter of rank 64:
+// 1036 cycles per 24 KB stage with three of them).
+constexpr int kShRing = 147456, kShStages = 8;
+constexpr int kShSegs = 512;  // segments kept in shared memory
 
 struct ShParams {
   const int32_t* seg_offsets;
@@ -51,6 +54,7 @@ struct ShCore {
   int wrong;
   int ids[kShN / 8];  // adapters of the chunk
   int row_ad[128];
+  int off[kShSegs + 1], ad[kShSegs];
 };
 
 // Which adapters in use have B rows that are not finite.  Each CTA leaves those that it found
@@ -101,7 +105,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
                                                                  const ShParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* part = reinterpret_cast<float*>(ring + kShStages * kShStageBytes);  // [128][r + 4]
+  float* part = reinterpret_cast<float*>(ring + kShRing);  // [128][r + 4]
   __shared__ ShCore sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();     // what ran ahead of the call is done, for the kernels behind this one too
@@ -125,11 +129,20 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
     fence_mbarrier_init();
   }
   if (warp == 1) tmem_alloc(&sm.tmem_base, kShN);
+  const bool near = p.S <= kShSegs;
+  if (near) {
+    for (int s = tid; s <= p.S; s += kShThreads) {
+      sm.off[s] = p.seg_offsets[s];
+      if (s < p.S) sm.ad[s] = p.seg_adapter[s];
+    }
+  }
+  const int32_t* seg_off = near ? sm.off : p.seg_offsets;
+  const int32_t* seg_ad = near ? sm.ad : p.seg_adapter;
   __syncthreads();
   if (blockIdx.x == 0) {  // the call's first kernel: its status word
     int wrong = 0x7fffffff;
     for (int s = tid; s < p.S; s += kShThreads)
-      if (segment_wrong(p.seg_offsets[s], p.seg_offsets[s + 1], p.seg_adapter[s], p.T, p.L)) wrong = min(wrong, s);
+      if (segment_wrong(seg_off[s], seg_off[s + 1], seg_ad[s], p.T, p.L)) wrong = min(wrong, s);
     atomicMin(&sm.wrong, wrong);
     __syncthreads();
     if (tid == 0) {
@@ -142,8 +155,8 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
     const int t = i < 128 ? t0 + i : (t0 ^ 128) + i - 128;
     int a = -1;
     if (t < p.T) {
-      const int s = segment_of(p.seg_offsets, p.S, t);
-      if (s >= 0) a = p.seg_adapter[s];
+      const int s = segment_of(seg_off, p.S, t);
+      if (s >= 0) a = seg_ad[s];
       if (a >= p.L || a < 0) a = -1;
       if (operand && i < 128 && chunk0 == 0 && rank == 0) p.row_adapter[t] = a;
     }
@@ -162,13 +175,11 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
   const int cnt = __popcll(mask);
   const int chunks = (cnt + apc - 1) / apc;
   const int nkb = (p.K + 63) / 64;
-  const int kb0 = static_cast<int>(static_cast<long long>(nkb) * rank / p.C);
-  const int kb1 = static_cast<int>(static_cast<long long>(nkb) * (rank + 1) / p.C);
+  const int kb0 = nkb * rank / p.C, kb1 = nkb * (rank + 1) / p.C;
   const int pitch = p.r + 4;  // floats per partial row: 16-byte aligned, rows on other banks
-  int stage = 0;
-  uint32_t phase = 0;
+  uint32_t phase = 0;  // by stage: parity of its next use
   bool ok = true;
-  uint32_t filled = 0, parity_of = 0;
+  uint32_t filled = 0;
 
   for (int ch = chunk0, it = 0; ch < chunks; ch += p.P) {
     // the chunk's adapters: bits [ch apc, ch apc + na) of the mask
@@ -179,6 +190,13 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
     for (int i = 0; i < na; ++i) here &= here - 1;
     here ^= rem;
     const bool work = (here & own) != 0ull;
+    // (every chunk begins with an idle ring: the one before ended in a cluster barrier)
+    const int stage_bytes = (128 + na * p.r) * 128, stages = min(kShStages, kShRing / stage_bytes);
+    int stage = 0;
+    auto advance = [&]() {
+      phase ^= 1u << stage;
+      if (++stage == stages) stage = 0;
+    };
     if (tid < na) {
       uint64_t m = rem;
       for (int i = 0; i < tid; ++i) m &= m - 1;
@@ -189,10 +207,10 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
     } else if (warp == 0) {
       if (lane == 0) {
         for (int kb = kb0; ok && kb < kb1; ++kb) {
-          ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 40);
+          ok = mbar_wait(&sm.empty[stage], (phase >> stage & 1u) ^ 1u, abort_flag, p.status, kFtWaitNs, 40);
           if (!ok) break;
-          uint8_t* s = ring + stage * kShStageBytes;
-          mbar_arrive_expect_tx(&sm.full[stage], 128u * 128u + static_cast<uint32_t>(na * p.r) * 128u);
+          uint8_t* s = ring + stage * stage_bytes;
+          mbar_arrive_expect_tx(&sm.full[stage], static_cast<uint32_t>(stage_bytes));
           tma_load_2d(s, &tmx, &sm.full[stage], kb * 64, t0);
           uint64_t m = rem;
           for (int q = 0; q < na; ++q, m &= m - 1) {
@@ -200,11 +218,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
             tma_load_2d(s + 128 * 128 + q * p.r * 128, &tma, &sm.full[stage], kb * 64, a * p.r);
           }
           filled |= 1u << stage;
-          parity_of = (parity_of & ~(1u << stage)) | (phase << stage);
-          if (++stage == kShStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          advance();
         }
       }
       __syncwarp();
@@ -214,18 +228,15 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
         ok = ok && mbar_wait(&sm.tempty, (static_cast<uint32_t>(it) & 1u) ^ 1u, abort_flag, p.status, kFtWaitNs, 41);
         tc_fence_after();
         for (int kb = kb0; ok && kb < kb1; ++kb) {
-          ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 42);
+          ok = mbar_wait(&sm.full[stage], phase >> stage & 1u, abort_flag, p.status, kFtWaitNs, 42);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t s = smem_u32(ring + stage * kShStageBytes);
+          const uint32_t s = smem_u32(ring + stage * stage_bytes);
           const uint64_t ad = umma_desc_sw128(s), bd = umma_desc_sw128(s + 128 * 128);
 #pragma unroll
           for (int k = 0; k < 4; ++k) umma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, (kb != kb0 || k != 0) ? 1u : 0u);
           umma_commit(&sm.empty[stage]);
-          if (++stage == kShStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          advance();
         }
         umma_commit(&sm.tfull);
       }
@@ -329,7 +340,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
     for (int s = 0; s < kShStages; ++s)
       if (filled & (1u << s)) {
         volatile int dummy = 0;
-        mbar_wait(&sm.full[s], (parity_of >> s) & 1u, &dummy, nullptr, kFtWaitNs / 4, 0);
+        mbar_wait(&sm.full[s], (phase >> s & 1u) ^ 1u, &dummy, nullptr, kFtWaitNs / 4, 0);  // (its last use)
       }
   tc_fence_before();
   __syncthreads();
@@ -388,13 +399,13 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool operand, cudaStrea
   const int apc = kShN / a.r, most = (std::min(std::min(a.L, a.S), 128) + apc - 1) / apc;
   p.P = std::max(1, std::min(most, a.num_sms / (tiles * p.C)));
   p.operand = operand;
-  const size_t smem = 1024 + kShStages * kShStageBytes + 128u * (a.r + 4) * 4;
+  const size_t smem = 1024 + kShRing + 128u * (a.r + 4) * 4;
   static std::atomic<bool> attr_set[kMaxDevices];
   const int dev = current_device_index();
   if (dev < 0) return cudaErrorInvalidDevice;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     const cudaError_t e = cudaFuncSetAttribute(fused_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               1024 + kShStages * kShStageBytes + 128 * (128 + 4) * 4);
+                                               1024 + kShRing + 128 * (128 + 4) * 4);
     if (e != cudaSuccess) return e;
     // (SMs that run the scan are split as the kernels behind it need them: see launch_small)
     const cudaError_t c = cudaFuncSetAttribute(fused_scan_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
