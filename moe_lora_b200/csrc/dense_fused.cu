@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(256) fused_shrink_f32_kernel(const DenseFusedA
 // fp32 projection on CUDA cores: 64 tokens x 64 features per tile (both halves of a gated
 // feature), 4 x 4 per thread from shared memory.  Few tiles leave SMs idle, so a cluster of C
 // CTAs splits h_in for a tile and each finishes 64 / C tokens, their partial sums added up in
-// rank order from the peers' shared memory (64 x 512 -> 512: 8 tiles, 64 CTAs).
+// rank order from the peers' shared memory (64 x 512 -> 512: 8 tiles, 64 CTAs, 9.9 us with
+// adapters; two dependent launches and the K loop's latency bound it).
 constexpr int kF32K = 32, kF32Pitch = 68;  // K step; floats per row, 16-byte aligned
 
 template <bool GATED>

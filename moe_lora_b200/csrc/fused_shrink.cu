@@ -578,7 +578,9 @@ cudaError_t launch_fused_shrink_simt(const FusedTcArgs& f, cudaStream_t st) {
   p.status = a.status;
   ProfScope ps(K_FUSED_SHRINK, st);
   const dim3 grid(fused_shrink_items(a), a.r / kSsRank);
-  // Up to two CTAs per SM: more loads in flight each; above, registers for a third.
+  // Up to two CTAs per SM: more loads in flight each (64 x 11008 -> 4096, one adapter: 26.0 us
+  // against 28.0 with the other form); above, registers for a third (19 adapters of rank 64: 49
+  // against 63 us).
   const __nv_bfloat16 *x = static_cast<const __nv_bfloat16*>(a.x), *la = static_cast<const __nv_bfloat16*>(a.lora_a);
   return fused_shrink_is_small(a) ? launch_small<2, 3>(grid, st, p, x, la) : launch_small<3, 2>(grid, st, p, x, la);
 }

@@ -12,6 +12,11 @@
 // Batches that fill the SMs with 128 tokens each are bound by what the SMs read (x once, W_r
 // once per tile): there CTA pairs (tcgen05 cta_group::2) share W_r, each reading half of it.
 //
+// 16384 tokens x 256 experts (H 7168) take 108 us: 47 us in which x streams (240 MB; 36 us at the
+// copy rate), about 30 us of choice and weights (some 1000 instructions per token and warp),
+// 10 us of sort.  One token in 13 us and 64 x 128 (H 7168) in 22 us are bound by latency: launch,
+// copies, three cluster barriers and the choice follow each other at 1 to 2 us each.
+//
 // The sort needs no atomics on global memory: a CTA leaves one bit per (expert, token) and
 // the running count of its pairs by expert.  Up to 128 tokens the cluster itself sorts (a
 // warp per expert); above, a second kernel does, a CTA per expert.
