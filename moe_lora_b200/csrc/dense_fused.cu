@@ -60,23 +60,40 @@ __global__ void __launch_bounds__(256) fused_shrink_f32_kernel(const DenseFusedA
   }
 }
 
-// fp32 projection on CUDA cores: 64 tokens x 64 features per tile (both halves of a gated
-// feature), 4 x 4 per thread from shared memory.  Few tiles leave SMs idle, so a cluster of C
-// CTAs splits h_in for a tile and each finishes 64 / C tokens, their partial sums added up in
-// rank order from the peers' shared memory (64 x 512 -> 512: 8 tiles, 64 CTAs, 9.9 us with
-// adapters; two dependent launches and the K loop's latency bound it).
-constexpr int kF32K = 32, kF32Pitch = 68;  // K step; floats per row, 16-byte aligned
+// fp32 projection on CUDA cores: 64 tokens x 128 weight rows per tile (gated: 64 gate rows and
+// the matching 64 up rows), 8 x 8 per thread from shared memory (4 x 8 waited for its loads:
+// 512 x 2048 -> 2048 in 135 us), two rows per packed multiply-add.  Few tiles leave SMs idle, so a cluster of C CTAs splits h_in for a tile and
+// each finishes 64 / C tokens, their partial sums added up in rank order from the peers' shared
+// memory (64 x 512 -> 512: 4 tiles, 10.7 us with adapters; two dependent launches and the K
+// loop's latency bound it.  468 x 1576 -> 864: 45 us; 512 x 2048 -> 2048: 106 us, 41 TFLOP/s).
+constexpr int kF32Threads = 128, kF32K = 16, kF32Pitch = 68;  // K step; floats per token of the partial sums
+
+// Shared tiles hold 64 rows per K value.  Four lanes bring 64 bytes of a row, so the runs of four
+// rows are swapped by the K value's quarter: neither the stores nor the loads meet a bank twice.
+__device__ __forceinline__ int f32_at(int k, int row4) { return k * 64 + ((row4 ^ (k / 4 * 2)) << 2); }
+
+// d += a b, two fp32 fused multiply-adds
+__device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t twice(float v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+  return r;
+}
 
 template <bool GATED>
-__global__ void __launch_bounds__(256) fused_f32_kernel(const DenseFusedArgs a, int C) {
-  constexpr int NH = GATED ? 2 : 1;
-  constexpr int kTile = kF32K * kF32Pitch;
-  __shared__ alignas(16) float sm[(NH + 1) * kTile > NH * 64 * kF32Pitch ? (NH + 1) * kTile : NH * 64 * kF32Pitch];
-  float* xs = sm;             // [kF32K][pitch], tokens along a row
-  float* ws = sm + kTile;     // [NH][kF32K][pitch], features along a row
-  float* part = sm;           // [NH][64 tokens][pitch], once the tiles are done
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const int rank = static_cast<int>(blockIdx.x) % C, f0 = static_cast<int>(blockIdx.x) / C * 64;
+__global__ void __launch_bounds__(kF32Threads, 3) fused_f32_kernel(const DenseFusedArgs a, int C) {
+  constexpr int kTile = kF32K * 64, kBuf = 3 * kTile;  // x, then the two halves of w
+  __shared__ alignas(16) float sm[2 * kBuf > 128 * kF32Pitch ? 2 * kBuf : 128 * kF32Pitch];
+  float* part = sm;  // [2 halves][64 tokens][pitch], once the tiles are done
+  const int tid = threadIdx.x, warp = tid >> 5;
+  // a warp has 32 tokens x one half's 64 rows, a lane runs of four of both, and four more 16
+  // tokens or 32 rows on
+  const int half_of = warp & 1, x4 = (warp >> 1) * 8 + ((tid >> 3) & 3), w4 = tid & 7;
+  const int rank = static_cast<int>(blockIdx.x) % C;
+  const int f0 = static_cast<int>(blockIdx.x) / C * (GATED ? 64 : 128);
+  const int second = GATED ? a.h_out : 64;  // the second half's rows follow the first's by
   const int t0 = blockIdx.y * 64;
   if (a.r == 0) {  // the call's only kernel
     pdl_wait();
@@ -87,79 +104,92 @@ __global__ void __launch_bounds__(256) fused_f32_kernel(const DenseFusedArgs a, 
   const int k1 = static_cast<int>(static_cast<long long>(nk) * (rank + 1) / C);
   const float* x = static_cast<const float*>(a.x);
   const float* w = static_cast<const float*>(a.w);
-  // a thread brings 4 K values of row tid % 64 twice per operand and K step
-  const int row = tid & 63, kq = (tid >> 6) * 4;
-  const float* xr = t0 + row < a.T ? x + static_cast<size_t>(t0 + row) * a.h_in : nullptr;
-  const float* wr[NH];
+  // a thread brings 4 K values of rows tid / 4 and 32 on of x and of both halves of w per K step
+  const int row = tid >> 2, kq = (tid & 3) * 4;
+  const float* from[3][2];
 #pragma unroll
-  for (int h = 0; h < NH; ++h)
-    wr[h] = f0 + row < a.h_out ? w + (static_cast<size_t>(h) * a.h_out + f0 + row) * a.h_in : nullptr;
-  float4 nx[2], nw[NH][2];
+  for (int u = 0; u < 2; ++u) {
+    const int rr = row + 32 * u;
+    from[0][u] = t0 + rr < a.T ? x + static_cast<size_t>(t0 + rr) * a.h_in : nullptr;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      from[1 + h][u] = f0 + rr + (GATED ? 0 : h * 64) < a.h_out
+                           ? w + (static_cast<size_t>(f0) + rr + static_cast<size_t>(h) * second) * a.h_in
+                           : nullptr;
+  }
+  float4 n[3][2];
   auto fetch = [&](int kb) {
+    const int k = kb * kF32K + kq;
+    const bool in = kb < k1 && k < a.h_in;  // (h_in is a multiple of 8)
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int k = kb * kF32K + kq + u * 16;
-      const bool in = kb < k1 && k < a.h_in;  // (h_in is a multiple of 8)
-      nx[u] = in && xr != nullptr ? __ldg(reinterpret_cast<const float4*>(xr + k)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int o = 0; o < 3; ++o)
 #pragma unroll
-      for (int h = 0; h < NH; ++h)
-        nw[h][u] = in && wr[h] != nullptr ? __ldg(reinterpret_cast<const float4*>(wr[h] + k)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+      for (int u = 0; u < 2; ++u)
+        n[o][u] = in && from[o][u] != nullptr ? __ldg(reinterpret_cast<const float4*>(from[o][u] + k))
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
   };
-  float acc[NH][4][4] = {};
-  fetch(k0);
-  for (int kb = k0; kb < k1; ++kb) {
+  auto store = [&](float* buf) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      float* d = xs + (kq + u * 16) * kF32Pitch + row;
-      d[0] = nx[u].x;
-      d[kF32Pitch] = nx[u].y;
-      d[2 * kF32Pitch] = nx[u].z;
-      d[3 * kF32Pitch] = nx[u].w;
+    for (int o = 0; o < 3; ++o)
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        float* e = ws + h * kTile + (kq + u * 16) * kF32Pitch + row;
-        e[0] = nw[h][u].x;
-        e[kF32Pitch] = nw[h][u].y;
-        e[2 * kF32Pitch] = nw[h][u].z;
-        e[3 * kF32Pitch] = nw[h][u].w;
+      for (int u = 0; u < 2; ++u) {
+        float* d = buf + o * kTile + f32_at(kq, (row >> 2) + 8 * u) + (row & 3);  // (one swap for all four)
+        d[0] = n[o][u].x;
+        d[64] = n[o][u].y;
+        d[128] = n[o][u].z;
+        d[192] = n[o][u].w;
       }
-    }
-    __syncthreads();
-    fetch(kb + 1);
-#pragma unroll 8
-    for (int k = 0; k < kF32K; ++k) {
-      const float4 xv = *reinterpret_cast<const float4*>(xs + k * kF32Pitch + ty * 4);
-      const float xa[4] = {xv.x, xv.y, xv.z, xv.w};
+  };
+  uint64_t acc[8][4] = {};  // [token][pair of rows]
+  fetch(k0);
+  store(sm);
+  fetch(k0 + 1);
+  __syncthreads();
+  for (int kb = k0; kb < k1; ++kb) {
+    const float* buf = sm + ((kb - k0) & 1) * kBuf;
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        const float4 wv = *reinterpret_cast<const float4*>(ws + h * kTile + k * kF32Pitch + tx * 4);
-        const float wa[4] = {wv.x, wv.y, wv.z, wv.w};
+    for (int k = 0; k < kF32K; ++k) {
+      uint64_t wv[4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(buf + (1 + half_of) * kTile + f32_at(k, w4 + 8 * u));
+        wv[2 * u] = v.x;
+        wv[2 * u + 1] = v.y;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float4 xv = *reinterpret_cast<const float4*>(buf + f32_at(k, x4 + 4 * u));
+        const uint64_t xa[4] = {twice(xv.x), twice(xv.y), twice(xv.z), twice(xv.w)};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[h][i][j] = fmaf(xa[i], wa[j], acc[h][i][j]);
+          for (int j = 0; j < 4; ++j) fma2(acc[4 * u + i][j], xa[i], wv[j]);
       }
     }
+    store(sm + ((kb + 1 - k0) & 1) * kBuf);  // (everyone left that buffer a barrier ago)
+    fetch(kb + 2);
     __syncthreads();
   }
 #pragma unroll
-  for (int h = 0; h < NH; ++h)
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<float4*>(part + (h * 64 + ty * 4 + i) * kF32Pitch + tx * 4) =
-          make_float4(acc[h][i][0], acc[h][i][1], acc[h][i][2], acc[h][i][3]);
+    for (int u = 0; u < 2; ++u)
+      *reinterpret_cast<ulonglong2*>(part + (half_of * 64 + (x4 + i / 4 * 4) * 4 + i % 4) * kF32Pitch + (w4 + 8 * u) * 4) =
+          make_ulonglong2(acc[i][2 * u], acc[i][2 * u + 1]);
   cluster_sync_all();
   pdl_trigger();  // a call behind this one may set itself up
   if (a.r) pdl_wait();  // z
-  // tokens [rank 64 / C, ...): 16 threads per token, 4 features each
-  for (int tok = rank * (64 / C) + ty; tok < (rank + 1) * (64 / C); tok += 16) {
-    const int t = t0 + tok, f = f0 + tx * 4;
+  // tokens [rank 64 / C, ...): 16 threads per token and half (gated: both halves at once), 4
+  // features each
+  constexpr int NH = GATED ? 2 : 1;
+  for (int o = tid; o < (64 / C) * (GATED ? 16 : 32); o += kF32Threads) {
+    const int tok = rank * (64 / C) + o / (GATED ? 16 : 32), half = GATED ? 0 : (o >> 4) & 1;
+    const int t = t0 + tok, f = f0 + half * 64 + (o & 15) * 4;
     if (t >= a.T || f >= a.h_out) continue;
     float v[NH][4];
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
-      const uint32_t at = smem_u32(part + (h * 64 + tok) * kF32Pitch + tx * 4);
+      const uint32_t at = smem_u32(part + ((half + h) * 64 + tok) * kF32Pitch + (o & 15) * 4);
       float4 p[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c)
@@ -208,12 +238,12 @@ __global__ void __launch_bounds__(256) fused_f32_kernel(const DenseFusedArgs a, 
       act_apply<false>(a.act, v[0]);
     }
     const size_t at = static_cast<size_t>(t) * a.h_out + f;
-    float4 o = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+    float4 y = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
     if (a.residual != nullptr) {
       const float4 res = *reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + at);
-      o = make_float4(o.x + res.x, o.y + res.y, o.z + res.z, o.w + res.w);
+      y = make_float4(y.x + res.x, y.y + res.y, y.z + res.z, y.w + res.w);
     }
-    *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = o;
+    *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = y;
   }
   cluster_sync_all();  // the peers have read this CTA's partial sums
 }
@@ -236,18 +266,30 @@ static cudaError_t launch_f32(const DenseFusedArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   ProfScope ps(K_DENSE_FUSED, st);
-  // splits of h_in: as many as keep two CTAs per SM, of two K steps at least
-  const int ft = (a.h_out + 63) / 64, tt = (a.T + 63) / 64, nk = (a.h_in + kF32K - 1) / kF32K;
-  int C = 8;
-  while (C > 1 && (static_cast<long long>(ft) * tt * C > 2 * a.num_sms || nk / C < 2)) C /= 2;
+  // splits of h_in, of four K steps at least: a CTA alone on its SM takes about 2.2 times, two
+  // take 2.5 times its share of a full SM, and a split adds its exchange (about two K steps)
+  const bool gated = a.act == ML_ACT_SILU_AND_MUL;
+  const int ft = (a.h_out + (gated ? 63 : 127)) / (gated ? 64 : 128), tt = (a.T + 63) / 64;
+  const int nk = (a.h_in + kF32K - 1) / kF32K;
+  int C = 1;
+  double best = 0.0;
+  for (int c = 1; c <= 8 && (c == 1 || nk / c >= 4); c *= 2) {
+    const long long per_sm = (static_cast<long long>(ft) * tt * c + a.num_sms - 1) / a.num_sms;
+    const double cost = (per_sm == 1 ? 2.2 : per_sm == 2 ? 2.5 : static_cast<double>(per_sm)) * (static_cast<double>(nk) / c + 2.0);
+    if (c == 1 || cost < best) {
+      best = cost;
+      C = c;
+    }
+  }
+  cfg.blockDim = dim3(kF32Threads);
   cfg.gridDim = dim3(ft * C, tt);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = C;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.numAttrs = 2;
-  const cudaError_t e = a.act == ML_ACT_SILU_AND_MUL ? cudaLaunchKernelEx(&cfg, fused_f32_kernel<true>, a, C)
-                                                     : cudaLaunchKernelEx(&cfg, fused_f32_kernel<false>, a, C);
+  const cudaError_t e = gated ? cudaLaunchKernelEx(&cfg, fused_f32_kernel<true>, a, C)
+                              : cudaLaunchKernelEx(&cfg, fused_f32_kernel<false>, a, C);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
