@@ -297,3 +297,55 @@ def test_operators_together():
         want, _ = fr.dense_fused(a64, f(dn["w"]), f(dn["a"]), f(dn["b"]), ids_ad, bias=f(dn["bias"]),
                                  residual=routed, lora_scale=0.5)
         assert rel_err(out, want) <= TOL_BF16
+
+
+@pytest.mark.parametrize("T,h_in,h_out", [(468, 1576, 864), (130, 2048, 200), (7, 1032, 2048), (512, 264, 1000)])
+def test_larger_sizes_f32(T, h_in, h_out):
+    """Every split of h_in, tiles that end inside a block."""
+    _check(T, h_in, h_out, 3, 8, F32, "gelu", True, True, T)
+    _check(T, h_in, h_out, 2, 128, F32, "silu_and_mul", True, False, T)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("T", [1, 64, 200, 300, 1100])
+def test_calls_that_feed_each_other(T, dt):
+    """A chain without a pause, each call reading what the one before wrote, a torch kernel among
+    them: the same bits as with a synchronisation after every call."""
+    ds = [dense_inputs(T, 520, 520, 4, r, dt, act, True, True, i, grouped=g)
+          for i, (r, act, g) in enumerate([(16, "gelu", True), (64, "silu", False), (8, "relu", True)])]
+    bare = dense_inputs(T, 520, 520, 0, 0, dt, "none", True, True, 9)
+    qs = [{k: dev(v) for k, v in d.items()} for d in ds + [bare]]
+    ws = ml.new_workspace(max(ml.workspace_size(ml.OP_DENSE_FUSED, T, 520, 520, 1, 1, 4, r) for r in (8, 16, 64)), "cuda")
+
+    def chain(pause):
+        h = qs[0]["x"]
+        for _ in range(6):
+            for q, act in zip(qs, ("gelu", "silu", "relu", "none")):
+                h = ml.dense_lora_fused(h, q["w"], q["a"], q["b"], q["offs"], q["segs"], bias=q["bias"],
+                                        activation=act, residual=q["residual"], lora_scale=0.5, workspace=ws)
+                pause()
+            h = h / 2
+            pause()
+        return h
+
+    want = chain(torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = chain(lambda: None)
+        assert torch.equal(got, want)
+
+
+def test_offsets_past_32_bits():
+    """An output of more than 2^31 elements: its last rows are what they are on their own."""
+    T, K, N = 270001, 64, 8192
+    d = dense_inputs(64, K, N, 2, 8, BF16, "silu", True, False, 5, grouped=False)
+    rows = fr.row_adapters(64, d["offs"].numpy(), d["segs"].numpy())
+    x = torch.zeros((T, K), dtype=BF16, device="cuda")
+    x[-64:] = d["x"].cuda()
+    offs = torch.cat([torch.zeros(1, dtype=torch.int32), d["offs"] + (T - 64)])
+    segs = torch.cat([torch.full((1,), -1, dtype=torch.int32), d["segs"]])
+    y = ml.dense_lora_fused(x, d["w"].cuda(), d["a"].cuda(), d["b"].cuda(), offs.cuda(), segs.cuda(),
+                            bias=d["bias"].cuda(), activation="silu", lora_scale=d["scale"])
+    assert y.numel() > 2 ** 31
+    check_dense(d, y[-64:], rows)
+    assert torch.equal(y[0], y[1000]) and torch.equal(y[0], y[T - 65])  # rows of zeros: act(bias)

@@ -295,3 +295,47 @@ def test_pairs_of_tiles(M, H, E):
     assert np.array_equal(res["logits"].cpu().numpy().astype(np.float64), lg + bias[None, :])
     check_route(res, lg + bias[None, :], ad, E, 4, 5, score_bias=b.astype(np.float64), **fmt)
     ml.check_status(res["workspace"])
+
+
+@pytest.mark.parametrize("M", [9, 300, 9500])
+def test_calls_that_follow_each_other(M):
+    """Routing and sorting without a pause on one workspace and one set of outputs, the inputs
+    rewritten between the calls."""
+    E, k, L, H = 48, 4, 6, 256
+    xs, wr, _ = grid_router(M, E, H, 3)
+    xs, wr = xs.cuda(), wr.cuda()
+    ads = [torch.from_numpy(adapters(M, L, s)).cuda() for s in range(3)]
+    x, ad = torch.empty_like(xs), torch.empty_like(ads[0])
+    ws = ml.new_workspace(ml.workspace_size(ml.OP_ROUTE_SCORED, M, H, 0, E, k, L, 0), "cuda")
+    out = {key: torch.empty_like(v) for key, v in
+           ml.route_scored(ads[0], k, L, x=xs, w_router=wr, score="sigmoid").items() if key != "workspace"}
+
+    def run(pause):
+        got = []
+        for i in range(6):
+            x.copy_(xs.roll(i, 0))
+            ad.copy_(ads[i % 3])
+            pause()
+            o = ml.route_scored(ad, k, L, x=x, w_router=wr, score="sigmoid" if i % 2 else "softmax", n_group=4,
+                                topk_group=2, out=out, workspace=ws)
+            pause()
+            got.append([o[key].clone() for key in ("topk_ids", "topk_w", "sorted_pairs", "seg_offsets")])
+        return got
+
+    want = run(torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    for a, b in zip(run(lambda: None), want):
+        for u, v in zip(a, b):
+            assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("M", [60, 1500])
+def test_logits_of_few_bits(M, score):
+    """Logits rounded to bf16, as many routers give them: ties among the first k and at the
+    borders of groups in most rows."""
+    lg = torch.from_numpy(np.random.default_rng(M).standard_normal((M, 64)).astype(np.float32) * 3)
+    lg = lg.to(torch.bfloat16).float().numpy()
+    _check(M, 64, 8, 3, 1, lg=lg, score=score)
+    _check(M, 64, 8, 3, 2, lg=lg, score=score, n_group=8, topk_group=4, group_rule="max")
+    _check(M, 64, 8, 3, 3, lg=lg, score=score, n_group=8, topk_group=4, group_rule="top2", renormalize=False)
