@@ -110,9 +110,9 @@ def _ptr(t: torch.Tensor | None):
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no stream object is made
 
 
-def _stream(stream=None):
+def _stream(stream=None, device=None):
     if stream is None and _current_raw_stream is not None:
-        return _current_raw_stream(torch.cuda.current_device())
+        return _current_raw_stream(torch.cuda.current_device() if device is None else device)
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
 
@@ -192,22 +192,26 @@ def _expect(name: str, t: torch.Tensor | None, shape: tuple, dtype: torch.dtype)
         raise ValueError(f"{name} must be {dtype} of shape {shape}, got {t.dtype} of shape {tuple(t.shape)}")
 
 
-def _one_device(*tensors) -> torch.device:
-    """The device of all tensors given (None left out): it has to be the current one, since the
-    library launches on the current device."""
-    first = None
+def _addresses(*tensors) -> tuple[int, list]:
+    """The current device's index and the tensors' addresses (None stays None): they have to be
+    contiguous and on that device, since the library launches on the current one."""
+    dev, at = -2, []
     for t in tensors:
         if t is None:
+            at.append(None)
             continue
-        if first is None:
-            first = t
-        elif t.get_device() != first.get_device():
-            raise ValueError(f"tensors on several devices: {first.device} and {t.device}")
-    if not first.is_cuda:
-        raise ValueError("tensors passed to the library must be CUDA tensors")
-    if first.get_device() != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {first.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return first.device
+        if t.get_device() != dev:
+            if dev != -2:
+                raise ValueError(f"tensors on several devices, cuda:{dev} and {t.device} among them")
+            dev = t.get_device()
+            if dev < 0:
+                raise ValueError("tensors passed to the library must be CUDA tensors")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        at.append(t.data_ptr())
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev, at
 
 
 @functools.lru_cache(maxsize=4096)
@@ -226,6 +230,12 @@ def _choice(name: str, value: str, of: dict) -> int:
     if value not in of:
         raise ValueError(f"{name} must be one of {', '.join(of)}, got {value!r}")
     return of[value]
+
+
+@functools.lru_cache(maxsize=256)
+def _route_format(score, n_group, topk_group, group_rule, renormalize, scale) -> RouteFormat:
+    return RouteFormat(_choice("score", score, SCORES), int(n_group), int(topk_group),
+                       _choice("group_rule", group_rule, GROUP_RULES), 1 if renormalize else 0, float(scale))
 
 
 def route_scored(adapter_ids: torch.Tensor, k: int, L: int, *, x=None, w_router=None, bias=None, logits_in=None,
@@ -248,48 +258,51 @@ def route_scored(adapter_ids: torch.Tensor, k: int, L: int, *, x=None, w_router=
         _expect("w_router", w_router, (E, H), torch.bfloat16)
         _expect("bias", bias, (E,), torch.float32)
     _expect("score_bias", score_bias, (E,), torch.float32)
-    fmt = RouteFormat(_choice("score", score, SCORES), int(n_group), int(topk_group),
-                      _choice("group_rule", group_rule, GROUP_RULES), 1 if renormalize else 0, scale)
-    o = out if out is not None else {}
-    dev = _one_device(adapter_ids, x, w_router, bias, logits_in, score_bias, workspace, *o.values())
+    fmt = _route_format(score, n_group, topk_group, group_rule, renormalize, scale)
+    given = out if out is not None else {}
     # what the caller did not pass is cut from one buffer, in pieces of whole 256 bytes
-    shapes = {"topk_ids": (M, k), "topk_w": (M, k), "sorted_pairs": (M * k,), "seg_offsets": (E * (L + 1) + 1,)}
+    spec = [("topk_ids", M * k, (M, k), (k, 1), torch.int32), ("topk_w", M * k, (M, k), (k, 1), torch.float32),
+            ("sorted_pairs", M * k, (M * k,), (1,), torch.int32),
+            ("seg_offsets", E * (L + 1) + 1, (E * (L + 1) + 1,), (1,), torch.int32)]
     if want_logits:
-        shapes["logits"] = (M, E)
-    need = 0 if workspace is not None else max(_sized(OP_ROUTE_SCORED, M, H, 0, E, k, L, 0), 256) // 4
-    place, total = {}, need
-    for name, shape in shapes.items():
-        t = o.get(name)
-        n = shape[0] * shape[1] if len(shape) == 2 else shape[0]
-        dtype = torch.float32 if name in ("topk_w", "logits") else torch.int32
-        if t is None:
-            place[name] = total
-            total += (n + 63) // 64 * 64
-        elif t.numel() < n or t.dtype != dtype:
+        spec.append(("logits", M * E, (M, E), (E, 1), torch.float32))
+    for name, n, _, _, dtype in spec if given else ():
+        t = given.get(name)
+        if t is not None and (t.dtype != dtype or t.numel() < n):
             raise ValueError(f"out[{name!r}] must be {dtype} with at least {n} elements")
-    made = []
-    if total:
-        made.append(torch.empty(total, dtype=torch.int32, device=dev))
-    got = {}
-    for name, shape in shapes.items():
-        if name not in place:
-            got[name] = o[name]
-            continue
-        t = made[0].as_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), place[name])
-        got[name] = t.view(torch.float32) if name in ("topk_w", "logits") else t
+    dev, at = _addresses(adapter_ids, x, w_router, bias, logits_in, score_bias, workspace, *given.values())
+    total = 0 if workspace is not None else max(_sized(OP_ROUTE_SCORED, M, H, 0, E, k, L, 0), 256) // 4
+    need = total
+    for name, n, _, _, _ in spec:
+        if given.get(name) is None:
+            total += (n + 63) // 64 * 64
+    buf = torch.empty(total, dtype=torch.int32, device=adapter_ids.device) if total else None
+    base, pos = buf.data_ptr() if total else 0, need
+    res, where = {}, {"logits": None}
+    for name, n, shape, stride, dtype in spec:
+        t = given.get(name)
+        if t is None:
+            t = buf.as_strided(shape, stride, pos)
+            res[name] = t.view(dtype) if dtype is torch.float32 else t
+            where[name] = base + 4 * pos
+            pos += (n + 63) // 64 * 64
+        else:
+            res[name], where[name] = t, t.data_ptr()
     if workspace is None:
-        workspace = made[0].as_strided((need,), (1,), 0).view(torch.uint8)
-    lg = got.get("logits")
-    ids, w, sp, so = got["topk_ids"], got["topk_w"], got["sorted_pairs"], got["seg_offsets"]
-    _check(lib().moe_lora_route_scored(
-        _ptr(x), _ptr(w_router), _ptr(bias), _ptr(logits_in), _ptr(score_bias), _ptr(adapter_ids), M, H, E, k, L,
-        ctypes.byref(fmt), _ptr(lg), _ptr(ids), _ptr(w), _ptr(sp), _ptr(so), _ptr(workspace), workspace.numel(),
-        _stream(stream)))
-    _used_on(stream, *made)
-    res = {"topk_ids": ids, "topk_w": w, "sorted_pairs": sp if sp.numel() == M * k else sp[: M * k],
-           "seg_offsets": so, "workspace": workspace}
-    if want_logits:
-        res["logits"] = lg
+        at[6], wsb = base, 4 * need
+        res["workspace"] = buf.as_strided((need,), (1,), 0).view(torch.uint8)
+    else:
+        res["workspace"], wsb = workspace, workspace.numel()
+    st = lib().moe_lora_route_scored(
+        at[1], at[2], at[3], at[4], at[5], at[0], M, H, E, k, L, ctypes.byref(fmt), where["logits"],
+        where["topk_ids"], where["topk_w"], where["sorted_pairs"], where["seg_offsets"], at[6], wsb,
+        _stream(stream, dev))
+    if st != OK:
+        _check(st)
+    if buf is not None:
+        _used_on(stream, buf)
+    if res["sorted_pairs"].numel() != M * k:
+        res["sorted_pairs"] = res["sorted_pairs"][: M * k]
     return res
 
 
@@ -396,17 +409,21 @@ def dense_lora_fused(x, w, lora_a=None, lora_b=None, seg_offsets=None, seg_adapt
     _expect("y", y, (T, h_out), dt)
     _expect("seg_adapter", seg_adapter, (S,), torch.int32)
     _expect("seg_offsets", seg_offsets, (S + 1,), torch.int32)
-    dev = _one_device(x, w, lora_a, lora_b, seg_offsets, seg_adapter, bias, residual, y, workspace)
-    made = []
+    dev, at = _addresses(x, w, bias, lora_a, lora_b, seg_offsets, seg_adapter, residual, y, workspace)
+    if L == 0:
+        at[3] = at[4] = None
     if y is None:
-        y = torch.empty((T, h_out), dtype=dt, device=dev)
-        made.append(y)
+        y = x.new_empty((T, h_out))
+        at[8] = y.data_ptr()
+        _used_on(stream, y)
+    wsb = workspace.numel() if workspace is not None else max(_sized(OP_DENSE_FUSED, T, h_in, h_out, 1, 1, L, r), 256)
     if workspace is None:
-        workspace = new_workspace(_sized(OP_DENSE_FUSED, T, h_in, h_out, 1, 1, L, r), dev)
-        made.append(workspace)
-    _check(lib().dense_lora_fused(_ptr(x), _ptr(w), _ptr(bias), _ptr(lora_a) if L else None,
-                                  _ptr(lora_b) if L else None, _ptr(seg_offsets), _ptr(seg_adapter), S, T, h_in,
-                                  h_out, r, L, act, float(lora_scale), _ptr(residual), _dt(x), _ptr(y),
-                                  _ptr(workspace), workspace.numel(), _stream(stream)))
-    _used_on(stream, *made)
+        workspace = torch.empty(wsb, dtype=torch.uint8, device=x.device)
+        at[9] = workspace.data_ptr()
+        _used_on(stream, workspace)
+    st = lib().dense_lora_fused(at[0], at[1], at[2], at[3], at[4], at[5], at[6], S, T, h_in, h_out, r, L, act,
+                                float(lora_scale), at[7], ML_BF16 if dt is torch.bfloat16 else ML_F32, at[8], at[9], wsb,
+                                _stream(stream, dev))
+    if st != OK:
+        _check(st)
     return y
