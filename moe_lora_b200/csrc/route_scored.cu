@@ -71,6 +71,7 @@ struct RsCore {
   float score_bias[256];
   alignas(16) uint4 map[256];  // tokens of the tile (this CTA's: 128 / C of them) by expert
   uint8_t ids[kRsWarps][256];  // a token's choice
+  alignas(16) uint8_t slot[256][16];  // up to 128 tokens: place of the expert among token i's choices
 };
 
 // ------------------------------------------------------------------ the choice of one token
@@ -545,8 +546,8 @@ __device__ __forceinline__ void weigh(const float* row, const RsParams& p, const
 }
 
 // ------------------------------------------------------------------ the stable sort
-// Slot of expert e among token t's k choices (the token chose it); written by this kernel's
-// peers or the kernel ahead.  No early exit: the loads of several calls overlap.
+// Slot of expert e among token t's k choices (the token chose it); written by the kernel
+// ahead.  No early exit: the loads of several calls overlap.
 __device__ __forceinline__ int slot_of_expert(const int32_t* topk_ids, int t, int k, int e) {
   const int32_t* row = topk_ids + static_cast<size_t>(t) * k;
   int at = 0;
@@ -683,6 +684,8 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   else __syncthreads();
   tc_fence_after();
 
+  ChoiceSetup<NI> cs;
+  if (given) cs.make(p, sm.score_bias);
   if (!given) {
     const uint32_t tmem = sm.tmem_base;
     const int nkb = (p.H + 63) / 64;
@@ -768,7 +771,8 @@ __global__ void __launch_bounds__(kRsThreads, 1)
       }
       __syncwarp();
     }
-    __syncthreads();  // the ring is idle
+    cs.make(p, sm.score_bias);  // (14 of the warps wait for the copies meanwhile)
+    __syncthreads();            // the ring is idle
     tc_fence_after();
     // accumulator -> partial sums: warps of a lane quarter take every fourth run of 32 experts
     const int q4 = warp & 3, m = q4 * 32 + lane;
@@ -826,8 +830,6 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   }
 
   // ---- a warp per token
-  ChoiceSetup<NI> cs;
-  cs.make(p, sm.score_bias);
   // (the next token goes to the first warp that is free: some take longer)
   for (int i = warp, after = 0; i < TC; i = __shfl_sync(0xffffffffu, after, 0)) {
     const int t = t0 + own0 + i;
@@ -850,8 +852,11 @@ __global__ void __launch_bounds__(kRsThreads, 1)
     bad |= a < -1 || a >= p.L;
     if (bad && lane == 0) atomicMin(&sm.flag, t);
     const int b = own0 + i;  // the token's bit
-    for (int j = lane; j < p.k; j += 32)
-      atomicOr(reinterpret_cast<unsigned*>(sm.map + sm.ids[warp][j]) + (b >> 5), 1u << (b & 31));
+    for (int j = lane; j < p.k; j += 32) {
+      const int e = sm.ids[warp][j];
+      atomicOr(reinterpret_cast<unsigned*>(sm.map + e) + (b >> 5), 1u << (b & 31));
+      if (p.tiles == 1) sm.slot[e][i] = static_cast<uint8_t>(j);  // (16 tokens per CTA then)
+    }
     __syncwarp();
   }
   __syncthreads();
@@ -893,6 +898,7 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   // ---- up to 128 tokens: the cluster sorts, a warp per expert
   pdl_trigger();  // a call behind this one may set itself up
   int* run = reinterpret_cast<int*>(scratch);            // next place by adapter, of this warp
+  uint4* s_slot = reinterpret_cast<uint4*>(scratch + 64);  // slots of the tile's tokens, one expert
   int* s_base = reinterpret_cast<int*>(sm.ids);          // pairs of lower experts (the ids are done)
   uint8_t* s_ad = reinterpret_cast<uint8_t*>(sm.ids) + 1024;  // adapters of the tokens
   const int my_ad = tid < p.M ? p.adapter_ids[tid] : -1;      // (of the first 128 threads)
@@ -917,24 +923,26 @@ __global__ void __launch_bounds__(kRsThreads, 1)
       p.status[1] = flag == kRsClean || flag < 0 ? 0 : flag;
     }
   }
-  cluster_sync_all();  // every peer has read the maps
+  uint4* s_map = reinterpret_cast<uint4*>(part);  // tokens by expert, of the whole tile
   const int base = block_prefix(n, sm.scan);
-  if (tid < 256) {
+  if (tid < p.E) {
     s_base[tid] = base;
-    sm.map[tid] = m;
+    s_map[tid] = m;
   }
   if (tid < 128) s_ad[tid] = static_cast<uint8_t>(my_ad >= 0 && my_ad < p.L ? my_ad : p.L);
   __syncthreads();
   const int LA = p.L + 1;
   for (int e = rank * kRsWarps + warp; e < p.E; e += C * kRsWarps) {
-    const unsigned* w = reinterpret_cast<const unsigned*>(sm.map + e);
+    const unsigned* w = reinterpret_cast<const unsigned*>(s_map + e);
+    if (lane < C)  // the tokens' slots, 16 from every CTA
+      s_slot[lane] = ld_cluster_u32x4(mapa_shared(smem_u32(sm.slot[e]), static_cast<uint32_t>(lane)));
     for (int a = lane; a < LA; a += 32) run[a] = 0;
     __syncwarp();
     int pair[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int t = q * 32 + lane;
-      pair[q] = w[q] >> lane & 1u ? t * p.k + slot_of_expert(p.topk_ids, t, p.k, e) : -1;
+      pair[q] = w[q] >> lane & 1u ? t * p.k + reinterpret_cast<const uint8_t*>(s_slot)[t] : -1;
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -946,6 +954,7 @@ __global__ void __launch_bounds__(kRsThreads, 1)
       if (w[q] != 0u) place32(p, pair[q] >= 0, pair[q], s_ad[q * 32 + lane], run);
   }
   if (rank == 0 && tid == 0) p.seg_offsets[p.E * LA] = p.M * p.k;
+  cluster_sync_all();  // the peers have read this CTA's maps, slots and flag
 }
 
 // ------------------------------------------------------------------ sort of large batches
@@ -1127,7 +1136,7 @@ cudaError_t launch_route_scored(const RouteScoredArgs& a, cudaStream_t st) {
   p.L = a.L;
   p.C = scored_split(a.M);
   p.tiles = (a.M + 127) / 128;
-  p.epad = std::max(48, (a.E + 15) / 16 * 16);  // (the sort's 65 counters fit a warp's doubles)
+  p.epad = std::max(48, (a.E + 15) / 16 * 16);  // (the sort's 65 counters and 128 slots fit a warp's scratch)
   p.wide = p.C == 1;
   if (p.wide) p.tiles = (p.tiles + 1) & ~1;
   p.stages = std::min(kRsMaxStages, kRsRing / ((128 + p.epad / (p.wide ? 2 : 1)) * 128));
