@@ -349,3 +349,51 @@ def test_offsets_past_32_bits():
     assert y.numel() > 2 ** 31
     check_dense(d, y[-64:], rows)
     assert torch.equal(y[0], y[1000]) and torch.equal(y[0], y[T - 65])  # rows of zeros: act(bias)
+
+
+def test_captured_on_two_branches():
+    """One graph whose branches run side by side and join: calls first on a branch, behind a copy,
+    behind a torch kernel, and behind two branches at once."""
+    T = 70
+    a = dense_inputs(T, 264, 392, 3, 16, BF16, "silu", True, True, 1)
+    b = dense_inputs(300, 264, 392, 3, 16, BF16, "gelu", True, False, 2)
+    c = dense_inputs(T, 392, 264, 0, 0, BF16, "none", True, False, 3)
+    f = dense_inputs(T, 264, 136, 2, 8, F32, "none", True, False, 4)
+    qs = [{k: dev(v) for k, v in d.items()} for d in (a, b, c, f)]
+    lg = torch.from_numpy(np.random.default_rng(1).standard_normal((200, 16)).astype(np.float32)).cuda()
+    ad = torch.from_numpy(adapters(200, 3, 1)).cuda()
+
+    def call(q, x=None):
+        return ml.dense_lora_fused(q["x"] if x is None else x, q["w"], q["a"], q["b"], q["offs"], q["segs"],
+                                   bias=q["bias"], activation=q["act"], residual=q["residual"], lora_scale=0.5)
+
+    def work(main, side):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            xb = qs[1]["x"].clone()
+            y1 = call(qs[1], xb)
+            r = ml.route_scored(ad, 3, 3, logits_in=lg, score="sigmoid")
+            y3 = call(qs[3])
+        y0 = call(qs[0])
+        h = y0 + 0
+        main.wait_stream(side)
+        y2 = call(qs[2], h)
+        return y0, y1, y2, y3, r["topk_ids"], r["sorted_pairs"]
+
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(main):
+        want = work(main, side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        got = work(main, side)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for u, v in zip(got, want):
+            assert torch.equal(u, v)
+    for d, o in ((a, got[0]), (b, got[1]), (f, got[3])):
+        check_dense(d, o)
