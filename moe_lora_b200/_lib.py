@@ -259,50 +259,59 @@ def route_scored(adapter_ids: torch.Tensor, k: int, L: int, *, x=None, w_router=
         _expect("bias", bias, (E,), torch.float32)
     _expect("score_bias", score_bias, (E,), torch.float32)
     fmt = _route_format(score, n_group, topk_group, group_rule, renormalize, scale)
-    given = out if out is not None else {}
-    # what the caller did not pass is cut from one buffer, in pieces of whole 256 bytes
-    spec = [("topk_ids", M * k, (M, k), (k, 1), torch.int32), ("topk_w", M * k, (M, k), (k, 1), torch.float32),
-            ("sorted_pairs", M * k, (M * k,), (1,), torch.int32),
-            ("seg_offsets", E * (L + 1) + 1, (E * (L + 1) + 1,), (1,), torch.int32)]
-    if want_logits:
-        spec.append(("logits", M * E, (M, E), (E, 1), torch.float32))
-    for name, n, _, _, dtype in spec if given else ():
-        t = given.get(name)
-        if t is not None and (t.dtype != dtype or t.numel() < n):
-            raise ValueError(f"out[{name!r}] must be {dtype} with at least {n} elements")
-    dev, at = _addresses(adapter_ids, x, w_router, bias, logits_in, score_bias, workspace, *given.values())
-    total = 0 if workspace is not None else max(_sized(OP_ROUTE_SCORED, M, H, 0, E, k, L, 0), 256) // 4
-    need = total
-    for name, n, _, _, _ in spec:
-        if given.get(name) is None:
-            total += (n + 63) // 64 * 64
-    buf = torch.empty(total, dtype=torch.int32, device=adapter_ids.device) if total else None
-    base, pos = buf.data_ptr() if total else 0, need
-    res, where = {}, {"logits": None}
-    for name, n, shape, stride, dtype in spec:
-        t = given.get(name)
-        if t is None:
-            t = buf.as_strided(shape, stride, pos)
-            res[name] = t.view(dtype) if dtype is torch.float32 else t
-            where[name] = base + 4 * pos
-            pos += (n + 63) // 64 * 64
-        else:
-            res[name], where[name] = t, t.data_ptr()
-    if workspace is None:
-        at[6], wsb = base, 4 * need
-        res["workspace"] = buf.as_strided((need,), (1,), 0).view(torch.uint8)
+    mk, ns = M * k, E * (L + 1) + 1
+    ids = w = sp = so = lg = None
+    if out:
+        ids, w, sp, so = out.get("topk_ids"), out.get("topk_w"), out.get("sorted_pairs"), out.get("seg_offsets")
+        lg = out.get("logits") if want_logits else None
+        for name, t, n, dtype in (("topk_ids", ids, mk, torch.int32), ("topk_w", w, mk, torch.float32),
+                                  ("sorted_pairs", sp, mk, torch.int32), ("seg_offsets", so, ns, torch.int32),
+                                  ("logits", lg, M * E, torch.float32)):
+            if t is not None and (t.dtype != dtype or t.numel() < n):
+                raise ValueError(f"out[{name!r}] must be {dtype} with at least {n} elements")
+    dev, at = _addresses(adapter_ids, x, w_router, bias, logits_in, score_bias, workspace, ids, w, sp, so, lg)
+    # what the caller did not pass is cut from one buffer, in pieces of whole 256 bytes (64 words)
+    wsn = 0 if workspace is not None else (_sized(OP_ROUTE_SCORED, M, H, 0, E, k, L, 0) + 255) // 256 * 64
+    pmk, pns = (mk + 63) // 64 * 64, (ns + 63) // 64 * 64
+    total = wsn
+    if not out:
+        total += 3 * pmk + pns
     else:
-        res["workspace"], wsb = workspace, workspace.numel()
-    st = lib().moe_lora_route_scored(
-        at[1], at[2], at[3], at[4], at[5], at[0], M, H, E, k, L, ctypes.byref(fmt), where["logits"],
-        where["topk_ids"], where["topk_w"], where["sorted_pairs"], where["seg_offsets"], at[6], wsb,
-        _stream(stream, dev))
+        total += pmk * ((ids is None) + (w is None) + (sp is None)) + pns * (so is None)
+    if want_logits and lg is None:
+        total += M * E
+    buf, o = None, wsn
+    if total:
+        buf = torch.empty(total, dtype=torch.int32, device=adapter_ids.device)
+        base = buf.data_ptr()
+    if workspace is None:
+        workspace, at[6], wsb = buf.as_strided((wsn,), (1,), 0).view(torch.uint8), base, 4 * wsn
+    else:
+        wsb = workspace.numel()
+    if ids is None:
+        ids, at[7] = buf.as_strided((M, k), (k, 1), o), base + 4 * o
+        o += pmk
+    if w is None:
+        w, at[8] = buf.as_strided((M, k), (k, 1), o).view(torch.float32), base + 4 * o
+        o += pmk
+    if sp is None:
+        sp, at[9] = buf.as_strided((mk,), (1,), o), base + 4 * o
+        o += pmk
+    if so is None:
+        so, at[10] = buf.as_strided((ns,), (1,), o), base + 4 * o
+        o += pns
+    if want_logits and lg is None:
+        lg, at[11] = buf.as_strided((M, E), (E, 1), o).view(torch.float32), base + 4 * o
+    st = lib().moe_lora_route_scored(at[1], at[2], at[3], at[4], at[5], at[0], M, H, E, k, L, ctypes.byref(fmt), at[11],
+                                     at[7], at[8], at[9], at[10], at[6], wsb, _stream(stream, dev))
     if st != OK:
         _check(st)
-    if buf is not None:
-        _used_on(stream, buf)
-    if res["sorted_pairs"].numel() != M * k:
-        res["sorted_pairs"] = res["sorted_pairs"][: M * k]
+    if stream is not None and buf is not None:
+        buf.record_stream(stream)
+    res = {"topk_ids": ids, "topk_w": w, "sorted_pairs": sp if sp.shape[0] == mk else sp[:mk], "seg_offsets": so,
+           "workspace": workspace}
+    if want_logits:
+        res["logits"] = lg
     return res
 
 
@@ -401,14 +410,13 @@ def dense_lora_fused(x, w, lora_a=None, lora_b=None, seg_offsets=None, seg_adapt
         raise ValueError("adapters need seg_offsets and seg_adapter")
     S = seg_adapter.shape[0] if seg_adapter is not None else 0
     dt = x.dtype
-    _expect("w", w, (n, h_in), dt)
-    _expect("bias", bias, (n,), dt)
-    _expect("residual", residual, (T, h_out), dt)
-    _expect("lora_a", lora_a, (L, r, h_in), dt)
-    _expect("lora_b", lora_b, (L, r, n), dt)
-    _expect("y", y, (T, h_out), dt)
-    _expect("seg_adapter", seg_adapter, (S,), torch.int32)
-    _expect("seg_offsets", seg_offsets, (S + 1,), torch.int32)
+    for name, t, shape in (("w", w, (n, h_in)), ("bias", bias, (n,)), ("residual", residual, (T, h_out)),
+                           ("lora_a", lora_a, (L, r, h_in)), ("lora_b", lora_b, (L, r, n)), ("y", y, (T, h_out))):
+        if t is not None and (t.dtype is not dt or t.shape != shape):
+            _expect(name, t, shape, dt)
+    if seg_adapter is not None:
+        _expect("seg_adapter", seg_adapter, (S,), torch.int32)
+        _expect("seg_offsets", seg_offsets, (S + 1,), torch.int32)
     dev, at = _addresses(x, w, bias, lora_a, lora_b, seg_offsets, seg_adapter, residual, y, workspace)
     if L == 0:
         at[3] = at[4] = None
