@@ -61,18 +61,6 @@ struct RsParams {
 
 constexpr int kRsClean = INT_MAX;  // a token that failed a check: its index; a wait that ran out: < 0
 
-struct RsCore {
-  uint64_t full[kRsMaxStages], empty[kRsMaxStages], tfull;
-  uint32_t tmem_base;
-  int abort_flag;
-  int flag;
-  int next;  // token that no warp has taken yet
-  int scan[kRsWarps];
-  float score_bias[256];
-  alignas(16) uint4 map[256];  // tokens of the tile (this CTA's: 128 / C of them) by expert
-  uint8_t ids[kRsWarps][256];  // a token's choice
-  alignas(16) uint8_t slot[256][16];  // up to 128 tokens: place of the expert among token i's choices
-};
 
 // ------------------------------------------------------------------ the choice of one token
 __device__ __forceinline__ float clamp_finite(float v) { return fminf(fmaxf(v, -FLT_MAX), FLT_MAX); }
@@ -114,61 +102,116 @@ __device__ __forceinline__ float rcp_approx(float x) {  // within a unit of the 
   return y;
 }
 
-// What the choice needs of the call, by lane (experts lane, lane + 32, ...).
-template <int NI>
-struct ChoiceSetup {
-  float above[NI];      // selection bias above the smallest one
-  unsigned group[NI];   // bit of the first lane of the expert's group (a group takes `per` lanes)
-  int at[NI];           // the expert's place among the groups' keys
-  int per, stride;      // ... a group's experts lie `stride` apart from the next one's
-  float range, most;    // of the biases: from the smallest to the largest; the magnitude, plus one
-  unsigned valid, nan, low, high;  // bit i: an expert, its bias NaN, or out of the range
-  bool odd;             // some expert of the call is not just valid
-  bool exact;           // every token in 64 bits
+// What the choice needs of the call.  One warp works it out for every expert while the copies
+// are on their way, into shared memory; the others pick their lanes' experts up from there.
+struct ExpertTable {
+  float above[256];   // selection bias above the smallest one
+  unsigned info[256];  // first lane of the expert's group | place among the groups' keys << 8 | kind << 28
+  float range, most;  // of the biases: from the smallest to the largest; the magnitude, plus one
+  int odd, exact;     // some expert is not just valid; every token in 64 bits
+};
+constexpr unsigned kValid = 1u, kNan = 2u, kLow = 4u, kHigh = 8u;  // kinds (a bias NaN, or out of the range)
 
-  __device__ __forceinline__ void make(const RsParams& p, const float* score_bias) {
-    const int lane = threadIdx.x & 31;
-    per = 32;
-    while (per > 1 && per * p.f.n_group > 32) per >>= 1;
-    exact = p.f.n_group > 32;
-    stride = p.f.group_size | 1;  // (lanes of neighbouring groups meet other banks)
-    valid = nan = low = high = 0u;
-    float bmin = FLT_MAX, bmax = -FLT_MAX;
+struct RsCore {
+  uint64_t full[kRsMaxStages], empty[kRsMaxStages], tfull;
+  uint32_t tmem_base;
+  int abort_flag;
+  int flag;
+  int next;  // token that no warp has taken yet
+  int scan[kRsWarps];
+  ExpertTable table;
+  alignas(16) uint4 map[256];  // tokens of the tile (this CTA's: 128 / C of them) by expert
+  uint8_t ids[kRsWarps][256];  // a token's choice
+  alignas(16) uint8_t slot[256][16];  // up to 128 tokens: place of the expert among token i's choices
+};
+
+// lanes of a warp per group of experts
+__device__ __forceinline__ int lanes_per_group(int n_group) {
+  int per = 32;
+  while (per > 1 && per * n_group > 32) per >>= 1;
+  return per;
+}
+
+template <int NI>
+__device__ __forceinline__ void make_table(const RsParams& p, ExpertTable& tab) {
+  const int lane = threadIdx.x & 31, per = lanes_per_group(p.f.n_group);
+  // a group's keys lie an odd number of words from the next one's (lanes meet other banks)
+  const int pad = 1 - (p.f.group_size & 1);
+  bool odd = false, exact = p.f.n_group > 32;
+  float b[NI], bmin = FLT_MAX, bmax = -FLT_MAX;
+  unsigned kind[NI];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int e = lane + 32 * i;
-      const float b = score_bias[e];
-      above[i] = 0.f;
-      group[i] = 0u;
-      at[i] = 0;
-      if (e >= p.E) continue;
-      valid |= 1u << i;
-      if (p.f.n_group > 1 && !exact) {
-        const int g = e / p.f.group_size;
-        group[i] = 1u << (g * per);
-        at[i] = e + g * (stride - p.f.group_size);
-      }
-      if (b != b) {
-        nan |= 1u << i;
-      } else if (fabsf(b) > kBiasMost) {
-        (b < 0.f ? low : high) |= 1u << i;
-        exact |= fabsf(b) < kBiasMost + 2.f;  // (a score is at most 1: it might cross over)
+  for (int i = 0; i < NI; ++i) {
+    const int e = lane + 32 * i;
+    kind[i] = 0u;
+    b[i] = 0.f;
+    if (e < p.E) {
+      kind[i] = kValid;
+      const float v = p.score_bias != nullptr ? p.score_bias[e] : 0.f;
+      if (v != v) {
+        kind[i] |= kNan;
+      } else if (fabsf(v) > kBiasMost) {
+        kind[i] |= v < 0.f ? kLow : kHigh;
+        exact |= fabsf(v) < kBiasMost + 2.f;  // (a score is at most 1: it might cross over)
       } else {
-        above[i] = b;
-        bmin = fminf(bmin, b);
-        bmax = fmaxf(bmax, b);
+        b[i] = v;
+        bmin = fminf(bmin, v);
+        bmax = fmaxf(bmax, v);
       }
     }
-    exact = __any_sync(0xffffffffu, exact);
-    odd = __any_sync(0xffffffffu, valid != (1u << NI) - 1u || (nan | low | high) != 0u);
-    bmin = -warp_max(-bmin);
-    bmax = warp_max(bmax);
-    if (bmin > bmax) bmin = bmax = 0.f;
+    odd |= kind[i] != kValid;
+  }
+  bmin = -warp_max(-bmin);
+  bmax = warp_max(bmax);
+  if (bmin > bmax) bmin = bmax = 0.f;
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-      if ((valid & ~(nan | low | high)) >> i & 1u) above[i] -= bmin;
-    range = bmax - bmin;
-    most = fmaxf(fabsf(bmin), fabsf(bmax)) + 1.f;
+  for (int i = 0; i < NI; ++i) {
+    const int e = lane + 32 * i;
+    const int g = e < p.E && p.f.n_group > 1 ? e / p.f.group_size : 0;
+    tab.above[e] = kind[i] == kValid ? b[i] - bmin : 0.f;
+    tab.info[e] = static_cast<unsigned>(g * per & 31) | static_cast<unsigned>(e + g * pad) << 8 | kind[i] << 28;
+  }
+  odd = __any_sync(0xffffffffu, odd);
+  exact = __any_sync(0xffffffffu, exact);
+  if (lane == 0) {
+    tab.range = bmax - bmin;
+    tab.most = fmaxf(fabsf(bmin), fabsf(bmax)) + 1.f;
+    tab.odd = odd;
+    tab.exact = exact;
+  }
+}
+
+// The table's part of a lane: experts lane, lane + 32, ...
+template <int NI>
+struct ChoiceSetup {
+  float above[NI];
+  unsigned group[NI];  // bit of the first lane of the expert's group
+  int at[NI];
+  int per, stride;     // lanes per group; words from a group's keys to the next one's
+  float range, most;
+  unsigned valid, nan, low, high;  // bit i: kind of expert lane + 32 i
+  bool odd, exact;
+
+  __device__ __forceinline__ void load(const RsParams& p, const ExpertTable& tab) {
+    const int lane = threadIdx.x & 31;
+    per = lanes_per_group(p.f.n_group);
+    stride = p.f.group_size | 1;
+    valid = nan = low = high = 0u;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const unsigned v = tab.info[lane + 32 * i];
+      above[i] = tab.above[lane + 32 * i];
+      group[i] = 1u << (v & 31u);
+      at[i] = static_cast<int>(v >> 8 & 0xffffu);
+      valid |= (v >> 28 & 1u) << i;
+      nan |= (v >> 29 & 1u) << i;
+      low |= (v >> 30 & 1u) << i;
+      high |= (v >> 31 & 1u) << i;
+    }
+    range = tab.range;
+    most = tab.most;
+    odd = tab.odd != 0;
+    exact = tab.exact != 0;
   }
 };
 
@@ -671,7 +714,6 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   if (p.tiles > 1) pdl_trigger();  // the sort may be launched
   if (tid < 256) {
     sm.map[tid] = make_uint4(0u, 0u, 0u, 0u);
-    sm.score_bias[tid] = p.score_bias != nullptr && tid < p.E ? p.score_bias[tid] : 0.f;
   }
   uint32_t cols = 32;
   while (cols < static_cast<uint32_t>(p.epad)) cols <<= 1;
@@ -684,8 +726,8 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   else __syncthreads();
   tc_fence_after();
 
-  ChoiceSetup<NI> cs;
-  if (given) cs.make(p, sm.score_bias);
+  if (warp == 2) make_table<NI>(p, sm.table);
+  if (given) __syncthreads();
   if (!given) {
     const uint32_t tmem = sm.tmem_base;
     const int nkb = (p.H + 63) / 64;
@@ -771,8 +813,7 @@ __global__ void __launch_bounds__(kRsThreads, 1)
       }
       __syncwarp();
     }
-    cs.make(p, sm.score_bias);  // (14 of the warps wait for the copies meanwhile)
-    __syncthreads();            // the ring is idle
+    __syncthreads();  // the ring is idle
     tc_fence_after();
     // accumulator -> partial sums: warps of a lane quarter take every fourth run of 32 experts
     const int q4 = warp & 3, m = q4 * 32 + lane;
@@ -830,6 +871,8 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   }
 
   // ---- a warp per token
+  ChoiceSetup<NI> cs;
+  cs.load(p, sm.table);
   // (the next token goes to the first warp that is free: some take longer)
   for (int i = warp, after = 0; i < TC; i = __shfl_sync(0xffffffffu, after, 0)) {
     const int t = t0 + own0 + i;
