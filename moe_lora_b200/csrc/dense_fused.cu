@@ -294,7 +294,7 @@ static cudaError_t launch_f32(const DenseFusedArgs& a, cudaStream_t st) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Up to here the adapters' shrink runs on CUDA cores (up to kFusedDecodeTokens where it is
+// Up to here the adapters' shrink runs on CUDA cores (with more tokens of a split projection where it is
 // small: 203 x 2056 -> 1000 with 5 adapters of rank 8: 16.7 us in all, on the tensor cores 18.4)
 constexpr int kSmallTokens = 64;
 
@@ -309,13 +309,13 @@ cudaError_t launch_dense_fused(const DenseFusedArgs& a, cudaStream_t st) {
     f.tile_mask = a.tile_mask;
     f.bad_part = a.bad_part;
     f.scan_ctas = std::min(kFusedScanMax, 2 * a.num_sms);
+    const bool stream = a.T <= kFusedDecodeTokens || fused_decode_pays(a);
     if (a.r > 0) {
-      const bool simt = a.T <= kSmallTokens || (a.T <= kFusedDecodeTokens && fused_shrink_is_small(a));
-      const cudaError_t e = simt ? launch_fused_shrink_simt(f, st)
-                                                : launch_fused_shrink_tc(f, a.T > kFusedDecodeTokens, st);
+      const bool simt = a.T <= kSmallTokens || (stream && fused_shrink_is_small(a));
+      const cudaError_t e = simt ? launch_fused_shrink_simt(f, st) : launch_fused_shrink_tc(f, !stream, st);
       if (e != cudaSuccess) return e;
     }
-    return a.T <= kFusedDecodeTokens ? launch_fused_decode_tc(f, st) : launch_fused_prefill_tc(f, st);
+    return stream ? launch_fused_decode_tc(f, st) : launch_fused_prefill_tc(f, st);
   }
   return launch_f32(a, st);
 }

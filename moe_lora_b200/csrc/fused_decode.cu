@@ -1,10 +1,11 @@
-// dense_lora_fused for few tokens (T <= 256): y = act(x W^T + bias + z B) + residual.
+// dense_lora_fused for few tokens (T <= 256, more where there are few tiles): y = act(x W^T + bias
+// + z B) + residual.
 //
 // Bound by the weight stream from HBM (64 x 4096 -> 2 x 11008 gated: 180 MB at 6.4 TB/s while it
-// lasts, 36 us for the call; 46 us with 22 adapters of rank 16).  As in the grouped GEMM the weight rows fill the
-// MMA's M (128 rows; gated: 64 gate rows and the matching 64 up rows) and all T tokens its N
-// ([SageMaker MoE kernels page], first item: the large dimension as the first operand), so
-// each weight is read once.  h_out / 128 tiles are too few or too uneven for 148 SMs, so a
+// lasts, 36 us for the call; 46 us with 22 adapters of rank 16).  As in the grouped GEMM the
+// weight rows fill the MMA's M (128 rows; gated: 64 gate rows and the matching 64 up rows) and
+// the tokens, up to 256, its N ([SageMaker MoE kernels page], first item: the large dimension as
+// the first operand), so each weight is read once per 256 tokens.  h_out / 128 tiles are too few or too uneven for 148 SMs, so a
 // cluster of C CTAs splits h_in for one tile: each streams its K range, then adds up every
 // C-th token's partial sums from its peers' shared memory, in rank order (the same bits
 // every time), and finishes those rows: bias, activation, residual, one rounding, 8-byte
@@ -72,6 +73,11 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
   volatile int* abort_flag = &sm.abort_flag;
   const int rank = static_cast<int>(blockIdx.x) % p.C;
   const int tile = static_cast<int>(blockIdx.x) / p.C;
+  // this CTA's tokens: all, or up to BN of them
+  const int t0 = static_cast<int>(blockIdx.y) * BN, T = min(BN, p.T - t0);
+  const __nv_bfloat16* z = p.z + static_cast<size_t>(t0) * p.r;
+  const __nv_bfloat16* residual = p.residual != nullptr ? p.residual + static_cast<size_t>(t0) * p.h_out : nullptr;
+  __nv_bfloat16* y = p.y + static_cast<size_t>(t0) * p.h_out;
   const int f0 = tile * (p.gated ? 64 : 128);
   const int row1 = p.gated ? p.h_out + f0 : f0 + 64;  // the tile's second 64 weight rows
   const int nkb = (p.K + 63) / 64;
@@ -101,7 +107,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
   const uint32_t tmem = sm.tmem_base;
   if (p.r == 0) {  // the call's only kernel: what ran ahead is done
     pdl_wait();
-    if (blockIdx.x == 0 && tid == 0) p.status[0] = 0;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) p.status[0] = 0;
   }
 
   // the tokens' adapters, looked up by the epilogue warps while the stream starts
@@ -147,7 +153,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         mbar_arrive_expect_tx(&sm.full[stage], Cfg::kStageBytes);
         tma_load_2d(s, &tmw, &sm.full[stage], kb * 64, f0);
         tma_load_2d(s + 64 * 128, &tmw, &sm.full[stage], kb * 64, row1);
-        tma_load_2d(s + 128 * 128, &tmx, &sm.full[stage], kb * 64, 0);
+        tma_load_2d(s + 128 * 128, &tmx, &sm.full[stage], kb * 64, t0);
         advance();
         if (kb < kbz) continue;
         if (kb == kbz) {
@@ -185,7 +191,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
       int stage = 0;
       uint32_t phase = 0, zi = 0;
       bool ok = true;
-      const int n_mma = min(BN, (p.T + 15) & ~15);
+      const int n_mma = min(BN, (T + 15) & ~15);
       const uint32_t idesc = umma_idesc_bf16(128, n_mma);
       auto advance = [&]() {
         umma_commit(&sm.empty[stage]);
@@ -238,8 +244,8 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
     if (p.r) {
       for (int t = e; t < BN; t += 128) {
         int a = -1;
-        if (t < p.T) {
-          const int s = segment_of(p.seg_offsets, p.S, t);
+        if (t < T) {
+          const int s = segment_of(p.seg_offsets, p.S, t0 + t);
           if (s >= 0) a = p.seg_adapter[s];
           if (a < 0 || a >= p.L) a = -1;
           if (a >= 0) atomicOr(&sm.mask[a >> 5], 1u << (a & 31));
@@ -260,7 +266,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         const uint32_t lap = static_cast<uint32_t>(at / S) & 1u;
         if (!waited) pdl_wait();  // z comes from the shrink kernel
         waited = true;
-        zt.load(g, p.z, 0, p.r, e);
+        zt.load(g, z, 0, p.r, e);
         // (after zgo the barrier `full` is in this lap's phase)
         ok = mbar_wait(&sm.zgo[stage], zi >> stage & 1u, abort_flag, p.status, kFtWaitNs, 55) &&
              mbar_wait(&sm.full[stage], lap, abort_flag, p.status, kFtWaitNs, 58);
@@ -309,7 +315,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
     if (got) {
       tc_fence_after();
       const int g4 = warp & 3, m = g4 * 32 + lane;
-      for (int c0 = 0; c0 < p.T; c0 += 32) {
+      for (int c0 = 0; c0 < T; c0 += 32) {
         float v[32];
         tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(g4 * 32) << 16) + c0, v);
 #pragma unroll
@@ -351,16 +357,16 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
     float4 v[8];
     uint2 res_next = make_uint2(0u, 0u);
     auto fetch = [&](int t) {
-      if (t >= p.T) return;
+      if (t >= T) return;
       const uint32_t at = smem_u32(part + t * kFdPitch + 4 * lane);
 #pragma unroll
       for (int c = 0; c < 8; ++c)
         if (c < p.C) v[c] = ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(c)));
-      if (p.residual != nullptr && writer)
-        res_next = *reinterpret_cast<const uint2*>(p.residual + static_cast<size_t>(t) * p.h_out + feat);
+      if (residual != nullptr && writer)
+        res_next = *reinterpret_cast<const uint2*>(residual + static_cast<size_t>(t) * p.h_out + feat);
     };
     fetch(rank + p.C * warp);
-    for (int t = rank + p.C * warp; t < p.T; t += t_step) {
+    for (int t = rank + p.C * warp; t < T; t += t_step) {
       float h[4] = {b[0], b[1], b[2], b[3]};
 #pragma unroll
       for (int c = 0; c < 8; ++c)
@@ -377,7 +383,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         const bool lo = ad >= 0 && (bad >> ad & 1ull), up = ad >= 0 && (bad_up >> ad & 1ull);
         if ((lo || up) && in)  // the rank rows that left the product
           for (int i = lo ? 0 : 64; i < (up ? p.r : min(p.r, 64)); ++i) {
-            const float zi = __bfloat162float(p.z[static_cast<size_t>(t) * p.r + i]);
+            const float zi = __bfloat162float(z[static_cast<size_t>(t) * p.r + i]);
             const __nv_bfloat16* br = p.lora_b + (static_cast<size_t>(ad) * p.r + i) * p.n + col;
 #pragma unroll
             for (int j = 0; j < 4; ++j) h[j] = fmaf(zi, __bfloat162float(br[j]), h[j]);
@@ -394,13 +400,27 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
       h[2] += __uint_as_float(res.y << 16);
       h[3] += __uint_as_float(res.y & 0xFFFF0000u);
       if (writer)
-        *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(t) * p.h_out + feat) =
+        *reinterpret_cast<uint2*>(y + static_cast<size_t>(t) * p.h_out + feat) =
             make_uint2(pack2_bf16(h[0], h[1]), pack2_bf16(h[2], h[3]));
     }
   }
   __syncwarp();
   cluster_sync_all();  // the peers have read this CTA's partial sums
   if (warp == 1) tmem_dealloc(tmem, Cfg::kTmemCols);
+}
+
+static int weight_tiles(const DenseFusedArgs& a) {
+  return a.act == ML_ACT_SILU_AND_MUL ? (a.h_out + 63) / 64 : (a.h_out + 127) / 128;
+}
+
+// Splitting h_in pays against 256 x 256 tiles when it takes more K blocks off each CTA than the
+// exchange of partial sums costs: 300 x 2048 -> 1024 13.4 against 18.4 us (16 tiles of 128 rows x
+// 256 tokens, 8 splits), 512 x 4096 -> 4096 27.0 against 30.3 (64 tiles, 2), 400 x 11008 -> 1000 31
+// against 60; but 700 x 600 -> 2000 23.1 against 15.5 (48 tiles, 3 splits of 10 K blocks).
+bool fused_decode_pays(const DenseFusedArgs& a) {
+  const long long tiles = static_cast<long long>(weight_tiles(a)) * ((a.T + 255) / 256);
+  const long long splits = std::min<long long>(8, a.num_sms / tiles), nkb = (a.h_in + 63) / 64;
+  return nkb * (splits - 1) >= 48;
 }
 
 template <int BN>
@@ -436,7 +456,7 @@ static cudaError_t launch_bn(const FusedTcArgs& f, cudaStream_t st) {
   p.r = a.r;
   p.act = a.act;
   p.gated = a.act == ML_ACT_SILU_AND_MUL;
-  const int tiles = p.gated ? (a.h_out + 63) / 64 : (a.h_out + 127) / 128;
+  const int wtiles = weight_tiles(a), ttiles = (a.T + BN - 1) / BN, tiles = wtiles * ttiles;
   // CTAs per SM and K splits.  As many splits as keep one wave (a second wave starts its stream
   // anew) and two K blocks per split: 1, 2, 4 and 8 splits take 73, 40, 24 and 22 us for 64 x
   // 11008 -> 4096 (32 tiles), 28, 19.5, 19.3 and 19.3 for one token 4096 -> 11008 (86 tiles, 3 at
@@ -473,7 +493,7 @@ static cudaError_t launch_bn(const FusedTcArgs& f, cudaStream_t st) {
   }
   ProfScope ps(K_DENSE_FUSED, st);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(tiles * p.C);
+  cfg.gridDim = dim3(wtiles * p.C, ttiles);
   cfg.blockDim = dim3(kFdThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

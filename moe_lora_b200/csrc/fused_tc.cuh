@@ -195,6 +195,8 @@ bool fused_shrink_is_small(const DenseFusedArgs& a);
 // operand: what launch_fused_prefill_tc asks for as well (zc, the masks, the scan)
 cudaError_t launch_fused_shrink_tc(const FusedTcArgs& p, bool operand, cudaStream_t st);
 cudaError_t launch_fused_decode_tc(const FusedTcArgs& p, cudaStream_t st);
+// above kFusedDecodeTokens: few tiles, so that splitting h_in pays more than larger tiles
+bool fused_decode_pays(const DenseFusedArgs& a);
 cudaError_t launch_fused_prefill_tc(const FusedTcArgs& p, cudaStream_t st);
 
 }  // namespace mlb

@@ -248,8 +248,8 @@ struct DenseFusedArgs {
   int* status;
   int num_sms;
 };
-// Token counts up to here take the weight-streaming kernel (all tokens in the MMA's N), more
-// the tiled one.
+// Token counts up to here take the weight-streaming kernel (all tokens in the MMA's N), more the
+// tiled one, unless it has few tiles.
 constexpr int kFusedDecodeTokens = 256;
 constexpr int kFusedScanMax = 512;  // CTAs of the adapters' scan at most
 cudaError_t launch_dense_fused(const DenseFusedArgs& a, cudaStream_t st);

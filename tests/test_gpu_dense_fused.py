@@ -131,11 +131,11 @@ def test_a_broken_adapter_stays_with_its_tenant(T):
 
 
 @pytest.mark.parametrize("row", [3, 64, 127])
-@pytest.mark.parametrize("T", [12, 40, 150, 300])
-def test_a_broken_half_of_a_wide_adapter(T, row):
+@pytest.mark.parametrize("T,K", [(12, 520), (40, 520), (150, 520), (300, 520), (300, 264), (900, 264)])
+def test_a_broken_half_of_a_wide_adapter(T, K, row):
     """Rank 128, one infinity in either half of the rank rows: the tenant's features beside it
     still get every rank row once."""
-    d = dense_inputs(T, 520, 328, 5, 128, BF16, "none", True, True, 11, none_frac=0.1)
+    d = dense_inputs(T, K, 328, 5, 128, BF16, "none", True, True, 11, none_frac=0.1)
     good = dict(d, b=d["b"].clone())
     rows = fr.row_adapters(T, d["offs"].numpy(), d["segs"].numpy())
     assert (rows == 2).any()
@@ -397,3 +397,27 @@ def test_captured_on_two_branches():
             assert torch.equal(u, v)
     for d, o in ((a, got[0]), (b, got[1]), (f, got[3])):
         check_dense(d, o)
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu_and_mul"])
+@pytest.mark.parametrize("T,h_in,h_out", [(257, 1032, 72), (300, 2048, 1024), (513, 4104, 136), (1000, 520, 520),
+                                          (2100, 2056, 200)])
+def test_more_tokens_with_few_tiles(T, h_in, h_out, act):
+    """Several blocks of 256 tokens whose reduction is split, adapters in each."""
+    _check(T, h_in, h_out, 5, 16, BF16, act, True, True, T)
+    _check(T, h_in, h_out, 3, 128, BF16, act, False, False, T + 1)
+    _check(T, h_in, h_out, 0, 0, BF16, act, True, False, T + 2)
+    d = dense_inputs(T, h_in, h_out, 20, 8, BF16, act, False, True, T, grouped=False)
+    check_dense(d, run_dense(d))
+
+
+def test_a_broken_adapter_among_few_tiles():
+    T = 700
+    d = dense_inputs(T, 2056, 136, 5, 16, BF16, "none", True, True, 3, none_frac=0.1)
+    rows = fr.row_adapters(T, d["offs"].numpy(), d["segs"].numpy())
+    good = dict(d, b=d["b"].clone())
+    d["b"][2, 3, 17], good["b"][2, 3, 17] = float("inf"), 0.0
+    y = run_dense(d).float().cpu()
+    assert not torch.isfinite(y[torch.from_numpy(rows == 2), 17]).any()
+    check_dense(good, y, where=np.ix_(np.arange(T), np.flatnonzero(np.arange(136) != 17)))
+    check_dense(good, y, where=np.flatnonzero(rows != 2))
