@@ -421,3 +421,33 @@ def test_a_broken_adapter_among_few_tiles():
     assert not torch.isfinite(y[torch.from_numpy(rows == 2), 17]).any()
     check_dense(good, y, where=np.ix_(np.arange(T), np.flatnonzero(np.arange(136) != 17)))
     check_dense(good, y, where=np.flatnonzero(rows != 2))
+
+
+@pytest.mark.parametrize("act", ["silu", "silu_and_mul"])
+@pytest.mark.parametrize("T,r", [(1, 8), (1, 16), (2, 8), (1, 32), (1, 128), (2, 16), (3, 8), (4, 16)])
+@pytest.mark.parametrize("h_in,h_out", [(8, 8), (72, 200), (4104, 1000), (11008, 264)])
+def test_a_token_or_a_few(T, r, h_in, h_out, act):
+    """The smallest calls, over every split of the reduction."""
+    _check(T, h_in, h_out, 6, r, BF16, act, True, True, T + r, none_frac=0.0, grouped=False)
+    _check(T, h_in, h_out, 6, r, BF16, act, False, False, T + r + 1, none_frac=0.5, grouped=False)
+
+
+@pytest.mark.parametrize("r", [8, 16, 128])
+def test_one_tokens_broken_adapter_and_segments(r):
+    d = dense_inputs(2, 520, 264, 4, r, BF16, "none", True, False, 1)
+    d["offs"], d["segs"] = torch.tensor([0, 1, 2], dtype=torch.int32), torch.tensor([2, 1], dtype=torch.int32)
+    good = dict(d, b=d["b"].clone())
+    d["b"][2, 5, 40], good["b"][2, 5, 40] = float("nan"), 0.0
+    y = run_dense(d).float().cpu()
+    assert torch.isnan(y[0, 40])
+    check_dense(good, y, where=np.ix_([0], np.flatnonzero(np.arange(264) != 40)))
+    check_dense(good, y, where=[1])
+    ws = ml.new_workspace(ml.workspace_size(ml.OP_DENSE_FUSED, 2, 520, 264, 1, 1, 4, r), "cuda")
+    for segs, offs in ([2, 9], [0, 1, 2]), ([2, 1], [0, 2, 1]), ([2, 1], [0, 1, 7]):
+        bad = dict(good, segs=torch.tensor(segs, dtype=torch.int32), offs=torch.tensor(offs, dtype=torch.int32))
+        assert torch.isfinite(run_dense(bad, workspace=ws)).all()
+        with pytest.raises(ml.MoELoRAError) as ei:
+            ml.check_status(ws)
+        assert ei.value.status == ml.ERR_DEVICE_CHECK
+    check_dense(good, run_dense(good, workspace=ws))
+    ml.check_status(ws)
