@@ -322,8 +322,9 @@ MOE_LORA_API moe_lora_status dense_lora_forward(
  *   y [T, h_out] of type dt, overwritten; it may be the residual itself (the same
  *   pointer: an update in place) and may overlap no other argument.
  *   workspace >= moe_lora_workspace_size(MOE_LORA_OP_DENSE_FUSED, T, h_in, h_out, 1, 1, L, r).
- * Sums, bias, activation and residual are fp32 and rounded to dt once (the adapters' xA is
- * rounded to bf16 for ML_BF16).  A tenant's adapter reaches only its own tokens, whatever
+ * Sums, bias, activation and residual are fp32 and rounded to dt once (for ML_BF16 the
+ * adapters' xA goes on as two bf16 numbers, the rounded value and what it left: 2^-17 of it
+ * is lost).  A tenant's adapter reaches only its own tokens, whatever
  * it holds.  An adapter id outside [-1, L) or offsets that are not monotone set
  * MOE_LORA_ERR_DEVICE_CHECK; the tokens concerned count as without an adapter.
  * h_in and h_out are multiples of 8; T <= 2^20.

@@ -316,7 +316,7 @@ FusedWs fused_layout(void* base, int T, int r, int L) {
   w.row_adapter = reinterpret_cast<int32_t*>(take(r ? static_cast<size_t>(T) * 4 : 0));
   w.tile_mask = reinterpret_cast<uint64_t*>(take(r ? (static_cast<size_t>(T) + 255) / 256 * 8 : 0));
   w.bad_part = reinterpret_cast<uint64_t*>(take(r && T ? kFusedScanMax * 8 : 0));
-  w.zc_pitch = (L * r + 63) / 64 * 64;
+  w.zc_pitch = (L * r + 31) / 32 * 64;  // each value of z takes two
   w.zc = take(r && T > kFusedDecodeTokens ? static_cast<size_t>(T) * w.zc_pitch * 2 : 0);
   w.bytes = off;
   return w;

@@ -2,7 +2,7 @@
 // + z B) + residual.
 //
 // Bound by the weight stream from HBM (64 x 4096 -> 2 x 11008 gated: 180 MB at 6.4 TB/s while it
-// lasts, 36 us for the call; 46 us with 22 adapters of rank 16).  As in the grouped GEMM the
+// lasts, 36 us for the call; 43 us with 22 adapters of rank 16).  As in the grouped GEMM the
 // weight rows fill the MMA's M (128 rows; gated: 64 gate rows and the matching 64 up rows) and
 // the tokens, up to 256, its N ([SageMaker MoE kernels page], first item: the large dimension as
 // the first operand), so each weight is read once per 256 tokens.  h_out / 128 tiles are too few or too uneven for 148 SMs, so a
@@ -47,8 +47,9 @@ struct FdCore {
   uint32_t tmem_base;
   int abort_flag;
   alignas(8) unsigned mask[2];    // adapters of the tokens
-  // ... whose B rows of this tile hold a value that is not finite ([2, 4): rank rows 64 to 127)
-  alignas(8) unsigned broken[4];
+  uint8_t list[64];               // ... in ascending order
+  // ... whose B rows of this tile hold a value that is not finite, by 32 rank rows
+  alignas(8) unsigned broken[2 * (128 / kGroupRank)];
   int row_ad[256];
 };
 
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
   const int tile = static_cast<int>(blockIdx.x) / p.C;
   // this CTA's tokens: all, or up to BN of them
   const int t0 = static_cast<int>(blockIdx.y) * BN, T = min(BN, p.T - t0);
-  const __nv_bfloat16* z = p.z + static_cast<size_t>(t0) * p.r;
+  const __nv_bfloat16* z = p.z + static_cast<size_t>(t0) * 2 * p.r;
   const __nv_bfloat16* residual = p.residual != nullptr ? p.residual + static_cast<size_t>(t0) * p.h_out : nullptr;
   __nv_bfloat16* y = p.y + static_cast<size_t>(t0) * p.h_out;
   const int f0 = tile * (p.gated ? 64 : 128);
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
     mbar_init(&sm.rows, 128);
     sm.abort_flag = 0;
     sm.mask[0] = sm.mask[1] = 0u;
-    sm.broken[0] = sm.broken[1] = sm.broken[2] = sm.broken[3] = 0u;
+    for (unsigned& b : sm.broken) b = 0u;
     fence_mbarrier_init();
     tma_prefetch_desc(&tmw);
     tma_prefetch_desc(&tmx);
@@ -110,22 +111,19 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) p.status[0] = 0;
   }
 
-  // the tokens' adapters, looked up by the epilogue warps while the stream starts
-  auto adapter_mask = [&]() -> uint64_t {
-    if (p.r == 0 || !mbar_wait(&sm.rows, 0, abort_flag, p.status, kFtWaitNs, 57)) return 0ull;
-    return sm.mask[0] | (static_cast<uint64_t>(sm.mask[1]) << 32);
+  // how many adapters the tokens have, looked up by the epilogue warps while the stream starts
+  auto adapter_count = [&]() -> int {
+    if (p.r == 0 || !mbar_wait(&sm.rows, 0, abort_flag, p.status, kFtWaitNs, 57)) return 0;
+    return __popc(sm.mask[0]) + __popc(sm.mask[1]);
   };
   // The adapters' K columns come one group at a time between the last K blocks: late, for the
   // shrink kernel to be done, and a few blocks apart, so that the weight stream goes on while a
-  // group's z is written.  group_at(j): K block that this CTA's j-th group follows; not before
-  // kbz, where the roles look the tokens' adapters up.
+  // group's z is written.  This CTA's j-th group (group rank + j C) follows K block group_at(j);
+  // not before kbz, where the roles look the tokens' adapters up.
   const int kbz = kb0 + (kb1 - kb0) / 4;
   int groups = 0, step = 1;
-  auto deal = [&](uint64_t mask) {
-    if (p.r == 0) return;
-    const int cap = p.r > 64 ? 1 : 64 / p.r, cnt = __popcll(mask);
-    const int total = p.r > 64 ? 2 * cnt : (cnt + cap - 1) / cap;
-    groups = (total + p.C - 1 - rank) / p.C;
+  auto deal = [&](const AdapterGroups& g, int cnt) {
+    if (cnt > 0) groups = (g.count(cnt) + p.C - 1 - rank) / p.C;
     if (groups > 0) step = min(kGroupStep, (kb1 - kbz) / groups);
   };
   auto group_at = [&](int j) -> int { return max(kbz, kb1 - 1 - kGroupTail - step * (groups - 1 - j)); };
@@ -144,8 +142,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         }
       };
       AdapterGroups g(0ull, p.r);
-      int j = 0;
-      bool more = false;
+      int j = 0, cnt = 0;
       for (int kb = kb0; ok && kb < kb1; ++kb) {
         ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 50);
         if (!ok) break;
@@ -157,19 +154,19 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         advance();
         if (kb < kbz) continue;
         if (kb == kbz) {
-          g.start(adapter_mask());
-          deal(g.rem);
-          more = g.next_of(rank, p.C);
+          cnt = adapter_count();
+          deal(g, cnt);
         }
-        for (; ok && more && group_at(j) == kb; ++j, more = g.next_of(0, p.C)) {
+        for (; ok && j < groups && group_at(j) == kb; ++j) {
+          g.pick(sm.list, cnt, rank + j * p.C);
           ok = mbar_wait(&sm.empty[stage], phase ^ 1u, abort_flag, p.status, kFtWaitNs, 51);
           if (!ok) break;
           mbar_arrive(&sm.zgo[stage]);  // the z tile may be written
           uint8_t* zs = ring + stage * Cfg::kStageBytes;
-          const int rb = p.r < 64 ? p.r : 64, boxes = g.boxes();
+          const int rb = g.box_rows(), boxes = g.boxes();
           mbar_arrive_expect_tx(&sm.full[stage], static_cast<uint32_t>(2 * boxes * rb) * 128u);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
+          for (int q = 0; q < kGroupRank / 8; ++q) {
             if (q >= boxes) break;
             const int id = (q > 0 && q >= g.na) ? g.ids[q > 0 ? q - 1 : 0] : g.ids[q];
             tma_load_2d(zs + q * rb * 128, &tmb, &sm.full[stage], f0, id * p.r + g.k0);
@@ -202,8 +199,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
       };
       const uint32_t zdesc = umma_idesc_bf16_amn(128, n_mma);
       AdapterGroups g(0ull, p.r);
-      int j = 0;
-      bool more = false;
+      int j = 0, cnt = 0;
       for (int kb = kb0; ok && kb < kb1; ++kb) {
         ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 52);
         if (!ok) break;
@@ -215,12 +211,12 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         advance();
         if (kb < kbz) continue;
         if (kb == kbz) {
-          g.start(adapter_mask());
-          deal(g.rem);
-          more = g.next_of(rank, p.C);
+          cnt = adapter_count();
+          deal(g, cnt);
         }
-        // adapters: A = B_a^T, MN-major (64-feature blocks 8 KB apart), 16 rank rows per step
-        for (; ok && more && group_at(j) == kb; ++j, more = g.next_of(0, p.C)) {
+        // adapters: A = B_a^T, MN-major (64-feature blocks 8 KB apart), 16 rank rows per two steps
+        for (; ok && j < groups && group_at(j) == kb; ++j) {
+          g.pick(sm.list, cnt, rank + j * p.C);
           ok = mbar_wait(&sm.full[stage], phase, abort_flag, p.status, kFtWaitNs, 53) &&
                mbar_wait(&sm.zfull[stage], static_cast<uint32_t>(zi >> stage) & 1u, abort_flag, p.status, kFtWaitNs, 54);
           if (!ok) break;
@@ -228,7 +224,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
           const uint32_t zs = smem_u32(ring + stage * Cfg::kStageBytes);
           const uint64_t zad = umma_desc_mn_sw128(zs, 64 * 128), zbd = umma_desc_sw128(zs + 128 * 128);
           const int steps = g.steps();
-          for (int k = 0; k < steps; ++k) umma_bf16(tmem, zad + 128 * k, zbd + 2 * k, zdesc, 1u);
+          for (int k = 0; k < steps; ++k) umma_bf16(tmem, zad + 128 * (k >> 1), zbd + 2 * k, zdesc, 1u);
           zi ^= 1u << stage;  // parity of the stage's uses for adapters
           advance();
         }
@@ -252,20 +248,25 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         }
         sm.row_ad[t] = a;
       }
+      named_bar_sync(1, 128);
+      {
+        const uint64_t mask = sm.mask[0] | (static_cast<uint64_t>(sm.mask[1]) << 32);
+        if (e < 64 && (mask >> e & 1ull)) sm.list[__popcll(mask & ((1ull << e) - 1ull))] = static_cast<uint8_t>(e);
+      }
       mbar_arrive(&sm.rows);
-      AdapterGroups g(adapter_mask(), p.r);
-      deal(g.rem);
+      AdapterGroups g(0ull, p.r);
+      const int cnt = adapter_count();
+      deal(g, cnt);
       uint32_t zi = 0;
       ZTile<128, BN / 16> zt;
       zt.rows(sm.row_ad, 0, BN, e);
-      bool ok = true, waited = false;
-      int j = 0;
-      for (bool more = g.next_of(rank, p.C); ok && more; ++j, more = g.next_of(0, p.C)) {
+      bool ok = true;
+      if (groups > 0) pdl_wait();  // z comes from the shrink kernel
+      for (int j = 0; ok && j < groups; ++j) {
         const int at = group_at(j) + 1 - kb0 + j;  // ring stages ahead of this one
         const int stage = at % S;
         const uint32_t lap = static_cast<uint32_t>(at / S) & 1u;
-        if (!waited) pdl_wait();  // z comes from the shrink kernel
-        waited = true;
+        g.pick(sm.list, cnt, rank + j * p.C);
         zt.load(g, z, 0, p.r, e);
         // (after zgo the barrier `full` is in this lap's phase)
         ok = mbar_wait(&sm.zgo[stage], zi >> stage & 1u, abort_flag, p.status, kFtWaitNs, 55) &&
@@ -279,8 +280,8 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         zt.store(zs + 128 * 128, e);
         // B rows that are not finite would reach every token through its zeros: their adapter
         // leaves the product, the final rows add it for its own tokens alone
-        const int per = p.r < 64 ? p.r : 64, used = g.boxes() * per * 8;  // 16-byte chunks of a block
-        unsigned* broken = sm.broken + (g.k0 != 0 ? 2 : 0);
+        const int per = g.box_rows(), used = g.boxes() * per * 8;  // 16-byte chunks of a block
+        unsigned* broken = sm.broken + 2 * (g.k0 / kGroupRank);
         uint32_t hit = 0u;  // adapters of the group
         for (int c = e; c < used; c += 128) {
           const uint4* b = reinterpret_cast<const uint4*>(zs) + c;
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         if (!named_bar_and(1, 128, hit == 0u)) {
           if (hit != 0u && lane == 0) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
+            for (int q = 0; q < kGroupRank / 8; ++q)
               if (hit >> q & 1u) atomicOr(&broken[g.ids[q] >> 5], 1u << (g.ids[q] & 31));
           }
           named_bar_sync(1, 128);
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
             const int q = min(c / 8 / per, g.na - 1);
             int id = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < kGroupRank / 8; ++j)
               if (j == q) id = g.ids[j];
             if (broken[id >> 5] >> (id & 31) & 1u) {
               uint4* b = reinterpret_cast<uint4*>(zs) + c;
@@ -344,13 +345,14 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
       b[2] = __uint_as_float(v.y << 16);
       b[3] = __uint_as_float(v.y & 0xFFFF0000u);
     }
-    // the tile's broken adapters, whichever CTA met them (rank rows below 64, and from there)
-    uint64_t bad = 0ull, bad_up = 0ull;
-    if (p.r)
-      for (int c = 0; c < p.C; ++c) {
-        bad |= ld_cluster_u64(mapa_shared(smem_u32(sm.broken), static_cast<uint32_t>(c)));
-        bad_up |= ld_cluster_u64(mapa_shared(smem_u32(sm.broken + 2), static_cast<uint32_t>(c)));
-      }
+    // the tile's broken adapters, whichever CTA met them: by 32 rank rows, and all
+    auto broken_at = [&](int part) -> uint64_t {
+      uint64_t b = 0ull;
+      for (int c = 0; c < p.C; ++c) b |= ld_cluster_u64(mapa_shared(smem_u32(sm.broken + 2 * part), static_cast<uint32_t>(c)));
+      return b;
+    };
+    uint64_t bad = 0ull;
+    for (int part = 0; part * kGroupRank < p.r; ++part) bad |= broken_at(part);
     // the next token's partial sums are on their way while one is finished
     const int t_step = p.C * (kFdThreads / 32);
     const bool writer = in && (!p.gated || lane < 16);
@@ -378,15 +380,17 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         }
       const uint2 res = res_next;
       fetch(t + t_step);
-      if ((bad | bad_up) != 0) {  // an adapter with values that are not finite: its own tokens only
+      if (bad != 0) {  // an adapter with values that are not finite: its own tokens only
         const int ad = sm.row_ad[t];
-        const bool lo = ad >= 0 && (bad >> ad & 1ull), up = ad >= 0 && (bad_up >> ad & 1ull);
-        if ((lo || up) && in)  // the rank rows that left the product
-          for (int i = lo ? 0 : 64; i < (up ? p.r : min(p.r, 64)); ++i) {
-            const float zi = __bfloat162float(z[static_cast<size_t>(t) * p.r + i]);
-            const __nv_bfloat16* br = p.lora_b + (static_cast<size_t>(ad) * p.r + i) * p.n + col;
+        if (ad >= 0 && (bad >> ad & 1ull) && in)
+          for (int i0 = 0; i0 < p.r; i0 += kGroupRank) {
+            if (!(broken_at(i0 / kGroupRank) >> ad & 1ull)) continue;  // (those rows are in the product)
+            for (int i = i0; i < min(i0 + kGroupRank, p.r); ++i) {
+              const float zi = z_value(z, t, p.r, i);
+              const __nv_bfloat16* br = p.lora_b + (static_cast<size_t>(ad) * p.r + i) * p.n + col;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = fmaf(zi, __bfloat162float(br[j]), h[j]);
+              for (int j = 0; j < 4; ++j) h[j] = fmaf(zi, __bfloat162float(br[j]), h[j]);
+            }
           }
       }
       if (p.gated) {
@@ -435,7 +439,7 @@ static cudaError_t launch_bn(const FusedTcArgs& f, cudaStream_t st) {
     return cudaErrorInvalidValue;
   tmb = tmx;
   if (a.r && encode_tmap_2d(&tmb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.lora_b, a.n, static_cast<uint64_t>(a.L) * a.r,
-                            static_cast<uint64_t>(a.n) * 2, 64, a.r < 64 ? a.r : 64,
+                            static_cast<uint64_t>(a.n) * 2, 64, std::min(a.r, kGroupRank),
                             CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   FdParams p{};

@@ -150,13 +150,12 @@ __global__ void __launch_bounds__(kFpThreads, 1)
           if (!ok) break;
           uint8_t* s = ring + stage * kFpStageBytes;
           const uint32_t fb = leader(&sm.full[stage]);
-          const int rb = p.r < 64 ? p.r : 64;
-          const int boxes = g.boxes();
+          const int rb = g.box_rows(), boxes = g.boxes();
           if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], 2u * 128u * 128u + static_cast<uint32_t>(4 * boxes * rb) * 128u);
           tma_load_2d_pair(s, &tmz, fb, gi * 64, t0);
           s += 128 * 128;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
+          for (int q = 0; q < kGroupRank / 8; ++q) {
             if (q >= boxes) break;
             const int id = (q > 0 && q >= g.na) ? g.ids[q > 0 ? q - 1 : 0] : g.ids[q];
             const int row = bad >> id & 1ull ? p.L * p.r : id * p.r + g.k0;
@@ -229,7 +228,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
             const uint32_t s = smem_u32(ring + stage * kFpStageBytes);
             const uint64_t ad = umma_desc_sw128(s), bd = umma_desc_mn_sw128(s + 128 * 128, 64 * 128);
             const int steps = g.steps();
-            for (int k = 0; k < steps; ++k) umma_bf16_pair(d, ad + 2 * k, bd + 128 * k, zidesc, 1u);
+            for (int k = 0; k < steps; ++k) umma_bf16_pair(d, ad + 2 * k, bd + 128 * (k >> 1), zidesc, 1u);
             advance();
           }
         }
@@ -290,7 +289,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
         if (!row_ok || f >= p.h_out) continue;
         if (bad_ad >= 0) {  // an adapter with values that are not finite: its own tokens only
           for (int i = 0; i < p.r; ++i) {
-            const float zi = __bfloat162float(p.z[static_cast<size_t>(tok) * p.r + i]);
+            const float zi = z_value(p.z, tok, p.r, i);
             const __nv_bfloat16* br = p.lora_b + (static_cast<size_t>(bad_ad) * p.r + i) * p.n + f;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -363,7 +362,7 @@ cudaError_t launch_fused_prefill_tc(const FusedTcArgs& f, cudaStream_t st) {
     return cudaErrorInvalidValue;
   tmb = tmz = tmx;
   if (a.r && encode_tmap_2d(&tmb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.lora_b, a.n, static_cast<uint64_t>(a.L) * a.r,
-                            static_cast<uint64_t>(a.n) * 2, 64, a.r < 64 ? a.r : 64,
+                            static_cast<uint64_t>(a.n) * 2, 64, std::min(a.r, kGroupRank),
                             CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   if (a.r && encode_tmap_2d(&tmz, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f.zc, f.zc_pitch, a.T,

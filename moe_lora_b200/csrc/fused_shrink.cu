@@ -3,8 +3,8 @@
 //
 // A tile of 128 tokens fills the MMA's M; its N takes the rank rows of 256 / r of the tile's
 // adapters at a time, so every token meets each of them and keeps the columns of its own.
-// Ahead of the tiled projection z is also laid out as that kernel's operand: the columns of a
-// 256-token tile's adapters side by side, zeros where a token has another one.
+// Ahead of the tiled projection z is also laid out as that kernel's operand: the K columns of a
+// 256-token tile's adapters side by side (see AdapterGroups), zeros where a token has another one.
 // A cluster of C CTAs splits h_in: each holds fp32 partial sums of all 128 tokens, then adds
 // up 128 / C tokens' partials in rank order from its peers' shared memory (no atomics: the
 // same bits every time).
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
         const int row = rank * rows + e / per_row, q = e % per_row / r8, j = e % per_row % r8, a = sm.ids[q];
         const int t = t0 + row;
         if (t >= p.T) continue;
-        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+        uint4 o = make_uint4(0u, 0u, 0u, 0u), l = o;
         if (sm.row_ad[row] == a) {
           const uint32_t at = smem_u32(part + row * pitch + 8 * j);
           float s[8] = {};
@@ -308,34 +308,43 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
                 s[4 * u + 2] += v[u][c].z;
                 s[4 * u + 3] += v[u][c].w;
               }
-          o = make_uint4(pack2_bf16(p.scale * s[0], p.scale * s[1]), pack2_bf16(p.scale * s[2], p.scale * s[3]),
-                         pack2_bf16(p.scale * s[4], p.scale * s[5]), pack2_bf16(p.scale * s[6], p.scale * s[7]));
-          *reinterpret_cast<uint4*>(p.z + static_cast<size_t>(t) * p.r + 8 * j) = o;
+          split2(p.scale * s[0], p.scale * s[1], o.x, l.x);
+          split2(p.scale * s[2], p.scale * s[3], o.y, l.y);
+          split2(p.scale * s[4], p.scale * s[5], o.z, l.z);
+          split2(p.scale * s[6], p.scale * s[7], o.w, l.w);
+          uint4* zt = reinterpret_cast<uint4*>(p.z + static_cast<size_t>(t) * 2 * p.r + 8 * j);
+          zt[0] = o;
+          zt[r8] = l;
         }
-        const int pos = __popcll(mask & ((1ull << a) - 1ull));
-        __nv_bfloat16* zt = p.zc + static_cast<size_t>(t) * p.zc_pitch + pos * p.r + 8 * j;
-        *reinterpret_cast<uint4*>(zt) = o;
+        // rank column R of the tile's adapters: K columns 32 (R / 16) + R % 16 (values) and 16 on
+        const int R = __popcll(mask & ((1ull << a) - 1ull)) * p.r + 8 * j;
+        uint4* zt = reinterpret_cast<uint4*>(p.zc + static_cast<size_t>(t) * p.zc_pitch + 32 * (R >> 4) + (R & 15));
+        zt[0] = o;
+        zt[2] = l;
         // an odd adapter of rank 8 ends inside an MMA step
-        if (p.r == 8 && !(pos & 1) && pos + 1 == cnt) reinterpret_cast<uint4*>(zt)[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (p.r == 8 && !(R & 8) && R + 8 == cnt * 8) zt[1] = zt[3] = make_uint4(0u, 0u, 0u, 0u);
       }
-    } else
-    for (int e = tid; e < rows * q4; e += kShThreads) {
-      const int row = rank * rows + e / q4, i = (e % q4) * 4;
-      const int a = sm.row_ad[row];
-      if (a < 0 || !(rem >> a & 1ull) || __popcll(rem & ((1ull << a) - 1ull)) >= na) continue;
-      const uint32_t at = smem_u32(part + row * pitch + i);
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c = 0; c < p.C; ++c) {
-        const float4 v = ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(c)));
-        s.x += v.x;
-        s.y += v.y;
-        s.z += v.z;
-        s.w += v.w;
+    } else {
+      for (int e = tid; e < rows * q4; e += kShThreads) {
+        const int row = rank * rows + e / q4, i = (e % q4) * 4;
+        const int a = sm.row_ad[row];
+        if (a < 0 || !(rem >> a & 1ull) || __popcll(rem & ((1ull << a) - 1ull)) >= na) continue;
+        const uint32_t at = smem_u32(part + row * pitch + i);
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < p.C; ++c) {
+          const float4 v = ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(c)));
+          s.x += v.x;
+          s.y += v.y;
+          s.z += v.z;
+          s.w += v.w;
+        }
+        uint2 o, l;
+        split2(p.scale * s.x, p.scale * s.y, o.x, l.x);
+        split2(p.scale * s.z, p.scale * s.w, o.y, l.y);
+        __nv_bfloat16* zt = p.z + static_cast<size_t>(t0 + row) * 2 * p.r + i;
+        *reinterpret_cast<uint2*>(zt) = o;
+        *reinterpret_cast<uint2*>(zt + p.r) = l;
       }
-      uint2 o;
-      o.x = pack2_bf16(p.scale * s.x, p.scale * s.y);
-      o.y = pack2_bf16(p.scale * s.z, p.scale * s.w);
-      *reinterpret_cast<uint2*>(p.z + static_cast<size_t>(t0 + row) * p.r + i) = o;
     }
     cluster_sync_all();  // the peers have read this CTA's partials
   }
@@ -532,8 +541,12 @@ __global__ void __launch_bounds__(kSsThreads, CTAS) fused_shrink_small_kernel(co
         for (int w = 0; w < 8; ++w)
 #pragma unroll
           for (int i = 0; i < kSsRank; ++i) s[i] += s_red[w][tid * kSsRank + i];
-        *reinterpret_cast<uint2*>(p.z + static_cast<size_t>(t) * p.r + i0) =
-            make_uint2(pack2_bf16(p.scale * s[0], p.scale * s[1]), pack2_bf16(p.scale * s[2], p.scale * s[3]));
+        uint2 o, l;
+        split2(p.scale * s[0], p.scale * s[1], o.x, l.x);
+        split2(p.scale * s[2], p.scale * s[3], o.y, l.y);
+        __nv_bfloat16* zt = p.z + static_cast<size_t>(t) * 2 * p.r + i0;
+        *reinterpret_cast<uint2*>(zt) = o;
+        *reinterpret_cast<uint2*>(zt + p.r) = l;
       }
     }
     __syncthreads();

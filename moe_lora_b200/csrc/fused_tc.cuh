@@ -58,54 +58,64 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t cluster_addr) {
 }
 
 // ------------------------------------------------------------------ adapters of a tile
-// The adapters of a token tile as extra K of the product: h = [x, z] [W; B].  A group of 64
-// K columns holds 64 / r adapters (half an adapter for r = 128); a token's z stands in its
-// own adapter's columns, zeros elsewhere.  Walks the groups of a 64-bit adapter mask.
+// The adapters of a token tile as extra K of the product: h = [x, z] [W; B].  z = c x A is an fp32
+// sum, given to the product as two bf16 numbers, the rounded value and what it left (2^-17 of z is
+// lost; one bf16 would lose 2^-9, as much as the rounding of the output).  A group of 64 K columns
+// covers 32 rank columns: 32 / r adapters, or 32 of one adapter's ranks.  Each 16 rank columns take
+// 32 of K, values first, then remainders, both against the same 16 rows of B.  A token's z stands
+// in its own adapter's columns, zeros elsewhere.
+constexpr int kGroupRank = 32;
+
 struct AdapterGroups {
-  uint64_t rem;
-  int r, half;
-  int ids[8];  // adapters of the current group (-2: none)
-  int na;      // how many
-  __device__ __forceinline__ AdapterGroups(uint64_t mask, int rank) : rem(mask), r(rank), half(0), na(0) {}
-  __device__ __forceinline__ void start(uint64_t mask) { rem = mask; }
-  // groups dealt out over n CTAs: the next of this CTA's (first: skip = its rank, then 0)
-  __device__ __forceinline__ bool next_of(int skip, int n) {
-    if (taken) skip += n - 1;
-    taken = true;
-    for (int i = 0; i < skip; ++i)
-      if (!next()) return false;
-    return next();
+  uint64_t rem;  // next(): adapters still to come
+  int r, part = 0;
+  int k0 = 0;   // first rank row of the group's adapter (r > 32)
+  int ids[kGroupRank / 8];  // adapters of the current group (-2: none)
+  int na = 0;   // how many
+  __device__ __forceinline__ AdapterGroups(uint64_t mask, int rank) : rem(mask), r(rank) {}
+  // groups of `cnt` adapters
+  __device__ __forceinline__ int count(int cnt) const {
+    return r > kGroupRank ? cnt * (r / kGroupRank) : (cnt + kGroupRank / r - 1) / (kGroupRank / r);
   }
-  bool taken = false;
+  // rank rows per box of B
+  __device__ __forceinline__ int box_rows() const { return min(r, kGroupRank); }
   // B boxes per 64 features: an odd adapter of rank 8 fills half an MMA step, so its rows come
   // once more and meet zeros of z
   __device__ __forceinline__ int boxes() const { return (r == 8 && (na & 1)) ? na + 1 : na; }
-  // MMA steps of 16 K columns
-  __device__ __forceinline__ int steps() const { return r > 64 ? 4 : (na * r + 15) / 16; }
+  // MMA steps of 16 K columns; step s takes rows 16 (s / 2) of B
+  __device__ __forceinline__ int steps() const { return r > kGroupRank ? 4 : 2 * ((na * r + 15) / 16); }
+  // group gi of the `cnt` adapters in `list`, in ascending order
+  __device__ __forceinline__ void pick(const uint8_t* list, int cnt, int gi) {
+    if (r > kGroupRank) {
+      const int parts = r / kGroupRank;
+      ids[0] = list[gi / parts];
+      na = 1;
+      k0 = gi % parts * kGroupRank;
+      return;
+    }
+    const int cap = kGroupRank / r;
+    na = min(cap, cnt - gi * cap);
+#pragma unroll
+    for (int q = 0; q < kGroupRank / 8; ++q) ids[q] = q < na ? list[gi * cap + q] : -2;
+  }
+  // the next group of the adapters in the mask
   __device__ __forceinline__ bool next() {
-    if (r > 64) {
-      if (half == 0) {
+    if (r > kGroupRank) {
+      if (part == 0) {
         if (rem == 0) return false;
         ids[0] = __ffsll(static_cast<long long>(rem)) - 1;
         rem &= rem - 1;
         na = 1;
-        half = 1;
-      } else {
-        half = 2;
       }
-      if (half == 2) {
-        half = 0;
-        k0 = 64;
-      } else {
-        k0 = 0;
-      }
+      k0 = part * kGroupRank;
+      if (++part == r / kGroupRank) part = 0;
       return true;
     }
     if (rem == 0) return false;
-    const int cap = 64 / r;
+    const int cap = kGroupRank / r;
     na = 0;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < kGroupRank / 8; ++q) {
       ids[q] = -2;
       if (q < cap && rem != 0) {
         ids[q] = __ffsll(static_cast<long long>(rem)) - 1;
@@ -115,8 +125,15 @@ struct AdapterGroups {
     }
     return true;
   }
-  int k0 = 0;  // first rank row of the group's adapter (r = 128)
 };
+
+// Two values of z as pairs of bf16 numbers: rounded, and the remainders (0 where there is none:
+// an infinity or NaN)
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack2_bf16(a, b);
+  const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xFFFF0000u);
+  lo = pack2_bf16(fabsf(ra) < INFINITY ? ra : 0.f, fabsf(rb) < INFINITY ? rb : 0.f);
+}
 
 // Token t's segment: the last one that begins at or before it, if it ends behind it (-1: none).
 // Every kernel of a call asks here, so that they agree even on segments out of order.
@@ -147,6 +164,7 @@ __device__ __forceinline__ bool not_finite8(uint4 v) {
 // holds 64 K columns, its 16-byte chunk c at c ^ (row & 7).  Thread i of NT takes chunk i & 7
 // of rows i / 8 + j NT / 8, j < N: the rows' adapters once per tile, the z values ahead of
 // the stage that takes them, so that only the shared-memory stores wait for it.
+// z: [tokens][2][r], values and remainders.
 template <int NT, int N>
 struct ZTile {
   int ad[N];
@@ -159,16 +177,19 @@ struct ZTile {
     }
   }
   __device__ __forceinline__ void load(const AdapterGroups& g, const __nv_bfloat16* z, int t0, int r, int i) {
-    const int per = r >= 64 ? 64 : r, k = 8 * (i & 7), q = k / per;
+    // chunk: 8 rank columns k, ..., their values (chunks 0, 1, 4, 5) or remainders
+    const int k = (i & 4) * 4 + (i & 1) * 8, per = g.box_rows(), q = k / per;
     int want = -2;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < kGroupRank / 8; ++e)
       if (e == q) want = g.ids[e];
-    const __nv_bfloat16* zp = z + static_cast<size_t>(t0 + (i >> 3)) * r + g.k0 + k - q * per;
+    const __nv_bfloat16* zp =
+        z + static_cast<size_t>(t0 + (i >> 3)) * 2 * r + ((i & 2) ? r : 0) + g.k0 + k - q * per;
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      v[j] = (ad[j] >= 0 && ad[j] == want) ? *reinterpret_cast<const uint4*>(zp + static_cast<size_t>(j) * (NT / 8) * r)
-                                           : make_uint4(0u, 0u, 0u, 0u);
+      v[j] = (ad[j] >= 0 && ad[j] == want)
+                 ? *reinterpret_cast<const uint4*>(zp + static_cast<size_t>(j) * (NT / 8) * 2 * r)
+                 : make_uint4(0u, 0u, 0u, 0u);
   }
   __device__ __forceinline__ void store(uint8_t* dst, int i) const {
 #pragma unroll
@@ -179,11 +200,17 @@ struct ZTile {
   }
 };
 
+// a z value of the pair
+__device__ __forceinline__ float z_value(const __nv_bfloat16* z, size_t t, int r, int i) {
+  const __nv_bfloat16* at = z + t * 2 * r + i;
+  return __bfloat162float(at[0]) + __bfloat162float(at[r]);
+}
+
 // Host side: launches of the tensor-core projection.
 struct FusedTcArgs {
   DenseFusedArgs a;
-  __nv_bfloat16* z;        // [T][r]
-  __nv_bfloat16* zc;       // z of each 256-token tile's adapters side by side: [T][zc_pitch]
+  __nv_bfloat16* z;        // [T][2][r]: values and remainders
+  __nv_bfloat16* zc;       // K columns of each 256-token tile's groups (see AdapterGroups): [T][zc_pitch]
   int zc_pitch;
   uint64_t* tile_mask;     // ... those adapters
   uint64_t* bad_part;      // adapters whose B holds a value that is not finite, by CTA of the scan

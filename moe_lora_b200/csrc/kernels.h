@@ -239,7 +239,7 @@ struct DenseFusedArgs {
   const void* residual;       // [T][h_out] or null (may be y)
   void* y;
   bool f32;
-  float* z;                   // workspace [T][r]: scale (x A), fp32 (bf16 projections: bf16)
+  float* z;                   // workspace: scale (x A), fp32 [T][r] (bf16: [T][2][r], rounded and remainder)
   int32_t* row_adapter;       // workspace [T]
   void* zc;                   // workspace (bf16, T > kFusedDecodeTokens): z as a matrix operand
   int zc_pitch;
