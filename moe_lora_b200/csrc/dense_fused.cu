@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kF32Threads, 3) fused_f32_kernel(const DenseFu
     }
     if (GATED) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[0][j] = silu(v[0][j]) * v[NH - 1][j];
+      for (int j = 0; j < 4; ++j) v[0][j] = sigmoid_of<false>(v[0][j], v[0][j]) * v[NH - 1][j];
     } else {
       act_apply<false>(a.act, v[0]);
     }

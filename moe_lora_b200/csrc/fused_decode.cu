@@ -346,13 +346,13 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
       b[3] = __uint_as_float(v.y & 0xFFFF0000u);
     }
     // the tile's broken adapters, whichever CTA met them: by 32 rank rows, and all
-    auto broken_at = [&](int part) -> uint64_t {
+    auto broken_at = [&](int i) -> uint64_t {
       uint64_t b = 0ull;
-      for (int c = 0; c < p.C; ++c) b |= ld_cluster_u64(mapa_shared(smem_u32(sm.broken + 2 * part), static_cast<uint32_t>(c)));
+      for (int c = 0; c < p.C; ++c) b |= ld_cluster_u64(mapa_shared(smem_u32(sm.broken + 2 * i), static_cast<uint32_t>(c)));
       return b;
     };
     uint64_t bad = 0ull;
-    for (int part = 0; part * kGroupRank < p.r; ++part) bad |= broken_at(part);
+    for (int i = 0; i * kGroupRank < p.r; ++i) bad |= broken_at(i);
     // the next token's partial sums are on their way while one is finished
     const int t_step = p.C * (kFdThreads / 32);
     const bool writer = in && (!p.gated || lane < 16);

@@ -9,13 +9,16 @@ namespace mlb {
 
 constexpr uint64_t kFtWaitNs = 2000000000ull;  // limit of every bounded wait: 2 s
 
-// Activations behind a projection.  Fp32 outputs take expf, erff and IEEE divisions.  Bf16
-// outputs (FAST) are rounded to 2^-8 behind them, so the sigmoid forms use the hardware
-// exponential and reciprocal, off by a few 2^-22 of the result.
+// Activations behind a projection.  The exponential's argument is at most 0, so that nothing
+// overflows at either end.  Fp32 outputs take expf and an IEEE division; bf16 outputs (FAST),
+// rounded to 2^-9 behind them, __expf (off by 2 + 1.2 |x| units of the last place) and
+// __fdividef (2 units: the divisor lies in [1, 2]).  30000 x 512 -> 1024, bound by this epilogue,
+// takes 122 us so and 130 with expf.
 template <bool FAST>
 __device__ __forceinline__ float sigmoid_of(float x, float v) {  // v / (1 + exp(-x))
-  if constexpr (FAST) return __fdividef(v, 1.f + __expf(-x));
-  return v / (1.f + expf(-x));
+  const float t = FAST ? __expf(-fabsf(x)) : expf(-fabsf(x)), n = x < 0.f ? v * t : v;
+  if constexpr (FAST) return __fdividef(n, 1.f + t);
+  return n / (1.f + t);
 }
 
 template <bool FAST, int N>

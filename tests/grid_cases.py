@@ -76,13 +76,17 @@ def grid_tolerance(d, y, m):
 
     h: exact.  act: none and relu exact; the others within 2^-20 of the result in fp32 (expf, erff
     and tanh forms, a quotient and a product, each within a few 2^-23), plus 2^-22 |h| where
-    1 + erf or 1 + tanh cancels; a gated product adds 2^-23.  The residual's add in fp32: half a
+    1 + erf or 1 + tanh cancels; a gated product adds 2^-23.  The fast exponential of bf16 outputs
+    is off by 2 + 1.173 |x| units of at most 2^-23: 2^-22 |x| on top, x = h or 1.6 (h + 0.045 h^3).  The residual's add in fp32: half a
     step of 2^-23.  y: half of its type's spacing."""
     dt = d["x"].dtype
     h = m["h"][:, : y.shape[1]]
     ea = np.zeros_like(y)
     if d["act"] not in ("none", "relu"):
-        ea = 2.0 ** -20 * np.abs(m["act"]) + (2.0 ** -22 * np.abs(h) if d["act"].startswith("gelu") else 0.0)
+        rel = 2.0 ** -20
+        if dt == torch.bfloat16 and d["act"] != "gelu":
+            rel = rel + 2.0 ** -22 * np.abs(1.6 * (h + 0.045 * h ** 3) if d["act"] == "gelu_tanh" else h)
+        ea = rel * np.abs(m["act"]) + (2.0 ** -22 * np.abs(h) if d["act"].startswith("gelu") else 0.0)
     if d["residual"] is not None and d["act"] not in ("none", "relu"):
         ea = ea + 2.0 ** -24 * np.abs(y)
     return ea + 0.5 * spacing(np.abs(y) + ea, dt)
