@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -233,9 +234,18 @@ def _choice(name: str, value: str, of: dict) -> int:
 
 
 @functools.lru_cache(maxsize=256)
+def _kept_format(score, n_group, topk_group, group_rule, renormalize, scale) -> RouteFormat:
+    return RouteFormat(_choice("score", score, SCORES), n_group, topk_group,
+                       _choice("group_rule", group_rule, GROUP_RULES), renormalize, scale)
+
+
 def _route_format(score, n_group, topk_group, group_rule, renormalize, scale) -> RouteFormat:
-    return RouteFormat(_choice("score", score, SCORES), int(n_group), int(topk_group),
-                       _choice("group_rule", group_rule, GROUP_RULES), 1 if renormalize else 0, float(scale))
+    # plain numbers only are kept: a tensor would be by its identity, with the value of its first call
+    if type(scale) is not float:
+        scale = float(scale)
+    if not type(n_group) is type(topk_group) is int:
+        n_group, topk_group = int(n_group), int(topk_group)
+    return _kept_format(score, n_group, topk_group, group_rule, 1 if renormalize else 0, scale)
 
 
 def route_scored(adapter_ids: torch.Tensor, k: int, L: int, *, x=None, w_router=None, bias=None, logits_in=None,
@@ -248,7 +258,7 @@ def route_scored(adapter_ids: torch.Tensor, k: int, L: int, *, x=None, w_router=
     divided by their sum if renormalize, then multiplied by scale.  Returns what route() does."""
     if logits_in is None and (x is None or w_router is None):
         raise ValueError("route_scored needs x and w_router, or logits_in")
-    M = adapter_ids.shape[0]
+    M, k, L = adapter_ids.shape[0], operator.index(k), operator.index(L)
     E, H = (logits_in.shape[1], 0) if logits_in is not None else w_router.shape
     _expect("adapter_ids", adapter_ids, (M,), torch.int32)
     if logits_in is not None:
