@@ -220,11 +220,18 @@ def _sized(op: int, M: int, H: int, I: int, E: int, k: int, L: int, r: int) -> i
     return workspace_size(op, M, H, I, E, k, L, r)
 
 
-def _used_on(stream, *tensors) -> None:
-    """Buffers made here for a stream other than the current one are not reused before it is done."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+def _made(stream, n, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    """A buffer for a call on `stream` (None: the current one).  It comes from that stream's memory,
+    since a block of the current one's may still wait for work queued there; and as the caller goes
+    on on the current stream, it is not reused before that one is done with it either."""
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):
+        t = torch.empty(n, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _choice(name: str, value: str, of: dict) -> int:
@@ -292,7 +299,7 @@ def route_scored(adapter_ids: torch.Tensor, k: int, L: int, *, x=None, w_router=
         total += M * E
     buf, o = None, wsn
     if total:
-        buf = torch.empty(total, dtype=torch.int32, device=adapter_ids.device)
+        buf = _made(stream, total, torch.int32, adapter_ids.device)
         base = buf.data_ptr()
     if workspace is None:
         workspace, at[6], wsb = buf.as_strided((wsn,), (1,), 0).view(torch.uint8), base, 4 * wsn
@@ -316,8 +323,6 @@ def route_scored(adapter_ids: torch.Tensor, k: int, L: int, *, x=None, w_router=
                                      at[7], at[8], at[9], at[10], at[6], wsb, _stream(stream, dev))
     if st != OK:
         _check(st)
-    if stream is not None and buf is not None:
-        buf.record_stream(stream)
     res = {"topk_ids": ids, "topk_w": w, "sorted_pairs": sp if sp.shape[0] == mk else sp[:mk], "seg_offsets": so,
            "workspace": workspace}
     if want_logits:
@@ -431,14 +436,12 @@ def dense_lora_fused(x, w, lora_a=None, lora_b=None, seg_offsets=None, seg_adapt
     if L == 0:
         at[3] = at[4] = None
     if y is None:
-        y = x.new_empty((T, h_out))
+        y = _made(stream, (T, h_out), dt, x.device)
         at[8] = y.data_ptr()
-        _used_on(stream, y)
     wsb = workspace.numel() if workspace is not None else max(_sized(OP_DENSE_FUSED, T, h_in, h_out, 1, 1, L, r), 256)
     if workspace is None:
-        workspace = torch.empty(wsb, dtype=torch.uint8, device=x.device)
+        workspace = _made(stream, wsb, torch.uint8, x.device)
         at[9] = workspace.data_ptr()
-        _used_on(stream, workspace)
     st = lib().dense_lora_fused(at[0], at[1], at[2], at[3], at[4], at[5], at[6], S, T, h_in, h_out, r, L, act,
                                 float(lora_scale), at[7], ML_BF16 if dt is torch.bfloat16 else ML_F32, at[8], at[9], wsb,
                                 _stream(stream, dev))
