@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kF32Threads, 3) fused_f32_kernel(const DenseFu
     }
     *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = y;
   }
+  __syncwarp();
   cluster_sync_all();  // the peers have read this CTA's partial sums
 }
 

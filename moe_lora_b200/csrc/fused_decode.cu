@@ -248,6 +248,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         }
         sm.row_ad[t] = a;
       }
+      __syncwarp();
       named_bar_sync(1, 128);
       {
         const uint64_t mask = sm.mask[0] | (static_cast<uint64_t>(sm.mask[1]) << 32);
@@ -271,6 +272,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         // (after zgo the barrier `full` is in this lap's phase)
         ok = mbar_wait(&sm.zgo[stage], zi >> stage & 1u, abort_flag, p.status, kFtWaitNs, 55) &&
              mbar_wait(&sm.full[stage], lap, abort_flag, p.status, kFtWaitNs, 58);
+        __syncwarp();
         if (!named_bar_and(1, 128, ok)) {
           ok = false;
           break;
@@ -294,6 +296,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
             for (int q = 0; q < kGroupRank / 8; ++q)
               if (hit >> q & 1u) atomicOr(&broken[g.ids[q] >> 5], 1u << (g.ids[q] & 31));
           }
+          __syncwarp();
           named_bar_sync(1, 128);
           for (int c = e; c < used; c += 128) {
             const int q = min(c / 8 / per, g.na - 1);
@@ -312,6 +315,7 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
       }
     }
     bool got = mbar_wait(&sm.tfull, 0, abort_flag, p.status, kFtWaitNs, 56);
+    __syncwarp();
     got = named_bar_and(1, 128, got);
     if (got) {
       tc_fence_after();

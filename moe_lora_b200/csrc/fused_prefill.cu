@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
   }
   if (warp == 1) tmem_alloc_pair(&sm.tmem_base, 512);
   tc_fence_before();
+  __syncwarp();
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
@@ -279,6 +280,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
       for (int c = half * width; c < (half + 1) * width; c += 32) {
         const int f = ft * 2 * width + c;  // first of 32 output features
         float h[32], u[32];
+        __syncwarp();  // (rows behind the last token left the run before this one early)
         tmem_ld_32x32b_x32(acc + c, h);
         if (p.gated) tmem_ld_32x32b_x32(acc + 128 + c, u);
         if (c + 32 == (half + 1) * width) {  // the warp has read its last columns

@@ -248,6 +248,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
       // this token's columns of its own adapter -> its partial row
       const int g4 = warp & 3, row = g4 * 32 + lane;
       bool got = mbar_wait(&sm.tfull, static_cast<uint32_t>(it) & 1u, abort_flag, p.status, kFtWaitNs, 43);
+      __syncwarp();
       got = named_bar_and(1, 128, got);
       if (got && kb1 > kb0) {
         tc_fence_after();
@@ -259,6 +260,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
         }
         for (int c0 = 0; c0 < na * p.r; c0 += 32) {
           float v[32];
+          __syncwarp();  // (lanes whose adapter is elsewhere stored nothing)
           tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(g4 * 32) << 16) + c0, v);
           // columns [c0, c0 + 32) against this token's [mine r, mine r + r)
 #pragma unroll
@@ -278,6 +280,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
       mbar_arrive(&sm.tempty);
     }
     if (work) ++it;
+    __syncwarp();
     cluster_sync_all();
     // rows [rank 128 / C, ...): sum over the cluster in rank order
     const int rows = 128 / p.C, q4 = p.r / 4;
@@ -346,6 +349,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
         *reinterpret_cast<uint2*>(zt + p.r) = l;
       }
     }
+    __syncwarp();
     cluster_sync_all();  // the peers have read this CTA's partials
   }
   if (warp == 0 && lane == 0 && *abort_flag)  // let our own copies land before the CTA exits

@@ -722,6 +722,7 @@ __global__ void __launch_bounds__(kRsThreads, 1)
     else tmem_alloc(&sm.tmem_base, cols);
   }
   tc_fence_before();
+  __syncwarp();
   if (p.wide) cluster_sync_all();  // the pair's barriers are ready
   else __syncthreads();
   tc_fence_after();
@@ -932,6 +933,7 @@ __global__ void __launch_bounds__(kRsThreads, 1)
     }
     if (tid == 0) p.flags[chunk] = sm.flag;
     tc_fence_before();
+    __syncwarp();
     cluster_sync_all();  // the peers have read this CTA's partial sums
     tc_fence_after();
     if (p.wide && !given && warp == 1) tmem_dealloc_pair(sm.tmem_base, cols);
@@ -945,6 +947,7 @@ __global__ void __launch_bounds__(kRsThreads, 1)
   int* s_base = reinterpret_cast<int*>(sm.ids);          // pairs of lower experts (the ids are done)
   uint8_t* s_ad = reinterpret_cast<uint8_t*>(sm.ids) + 1024;  // adapters of the tokens
   const int my_ad = tid < p.M ? p.adapter_ids[tid] : -1;      // (of the first 128 threads)
+  __syncwarp();
   cluster_sync_all();
   uint4 m = make_uint4(0u, 0u, 0u, 0u);
   int n = 0;
@@ -997,6 +1000,7 @@ __global__ void __launch_bounds__(kRsThreads, 1)
       if (w[q] != 0u) place32(p, pair[q] >= 0, pair[q], s_ad[q * 32 + lane], run);
   }
   if (rank == 0 && tid == 0) p.seg_offsets[p.E * LA] = p.M * p.k;
+  __syncwarp();
   cluster_sync_all();  // the peers have read this CTA's maps, slots and flag
 }
 
