@@ -107,7 +107,7 @@ __device__ __forceinline__ float rcp_approx(float x) {  // within a unit of the 
 struct ExpertTable {
   float above[256];   // selection bias above the smallest one
   unsigned info[256];  // first lane of the expert's group | place among the groups' keys << 8 | kind << 28
-  float range, most;  // of the biases: from the smallest to the largest; the magnitude, plus one
+  float range;        // of the biases: from the smallest to the largest
   int odd, exact;     // some expert is not just valid; every token in 64 bits
 };
 constexpr unsigned kValid = 1u, kNan = 2u, kLow = 4u, kHigh = 8u;  // kinds (a bias NaN, or out of the range)
@@ -175,7 +175,6 @@ __device__ __forceinline__ void make_table(const RsParams& p, ExpertTable& tab) 
   exact = __any_sync(0xffffffffu, exact);
   if (lane == 0) {
     tab.range = bmax - bmin;
-    tab.most = fmaxf(fabsf(bmin), fabsf(bmax)) + 1.f;
     tab.odd = odd;
     tab.exact = exact;
   }
@@ -188,7 +187,7 @@ struct ChoiceSetup {
   unsigned group[NI];  // bit of the first lane of the expert's group
   int at[NI];
   int per, stride;     // lanes per group; words from a group's keys to the next one's
-  float range, most;
+  float range;
   unsigned valid, nan, low, high;  // bit i: kind of expert lane + 32 i
   bool odd, exact;
 
@@ -209,7 +208,6 @@ struct ChoiceSetup {
       high |= (v >> 31 & 1u) << i;
     }
     range = tab.range;
-    most = tab.most;
     odd = tab.odd != 0;
     exact = tab.exact != 0;
   }
@@ -366,7 +364,7 @@ __device__ __forceinline__ bool choose(const float* row, const RsParams& p, cons
   const ScoreFormat& f = p.f;
   float v[NI];       // logits, then scores (exponentials, for a softmax)
   uint32_t key[NI];  // q and 255 - expert
-  unsigned nan = cs.nan;
+  unsigned unread = 0u;  // bit i: the logit of expert lane + 32 i is a NaN
   float probe = 0.f;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
@@ -378,10 +376,11 @@ __device__ __forceinline__ bool choose(const float* row, const RsParams& p, cons
   if (odd) {  // infinities, NaN; no experts
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      if (v[i] != v[i]) nan |= 1u << i;
+      if (v[i] != v[i]) unread |= 1u << i;
       v[i] = v[i] != v[i] || !(cs.valid >> i & 1u) ? -FLT_MAX : clamp_finite(v[i]);
     }
   }
+  const unsigned nan = cs.nan | unread;
   mx = -FLT_MAX;
   sum = 1.f;
   if (!f.sigmoid || f.by_logit) {
@@ -397,7 +396,7 @@ __device__ __forceinline__ bool choose(const float* row, const RsParams& p, cons
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       s[i] = cs.valid >> i & 1u ? expf(v[i] - mx) : 0.f;
-      if (odd && (nan & ~cs.nan) >> i & 1u) s[i] = 0.f;
+      if (odd && unread >> i & 1u) s[i] = 0.f;
       sum += s[i];
     }
     sum = warp_sum(sum);
