@@ -318,7 +318,8 @@ MOE_LORA_API moe_lora_status dense_lora_forward(
  *   x [T, h_in], w [n][h_in], bias [n] or NULL, residual [T, h_out] or NULL, all of type
  *   dt (ML_F32 or ML_BF16); lora_a [L][r][h_in], lora_b [L][r][n] (NULL iff L = 0).
  *   seg_offsets, seg_adapter: segments as in sgmv_shrink; a token outside every segment
- *   counts as one without an adapter.  Both may be NULL, with S = 0, when L = 0.
+ *   counts as one without an adapter.  With L = 0 they are not looked at, and not checked
+ *   either: both may be NULL, with S = 0.
  *   y [T, h_out] of type dt, overwritten; it may be the residual itself (the same
  *   pointer: an update in place) and may overlap no other argument.
  *   workspace >= moe_lora_workspace_size(MOE_LORA_OP_DENSE_FUSED, T, h_in, h_out, 1, 1, L, r).

@@ -409,7 +409,9 @@ def dense_lora_fused(x, w, lora_a=None, lora_b=None, seg_offsets=None, seg_adapt
     """dense_lora_fused: y = act(x w^T + bias + lora_scale (x A) B) + residual, bf16 or fp32.
     activation: "none", "relu", "gelu", "gelu_tanh", "silu", or "silu_and_mul", where w (and
     bias and lora_b) hold 2 h_out features, the gate first.  Without lora_a and lora_b no
-    segments are needed; y may be the residual (an update in place)."""
+    segments are needed, and given ones are not looked at; y may be the residual (an update in
+    place).  What the kernels find wrong (segments out of order, an adapter id out of range, a wait
+    that ran out) is recorded in the workspace alone: pass one and give it to check_status()."""
     act = _choice("activation", activation, ACTIVATIONS)
     if x.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")

@@ -1159,7 +1159,15 @@ moe_lora_status dense_lora_fused(const void* x, const void* w, const void* bias,
   const FusedWs need = fused_layout(nullptr, T, rr, L);
   moe_lora_status st = check_ws(workspace, workspace_bytes, need.bytes);
   if (st != MOE_LORA_OK) return st;
-  if (T == 0) return MOE_LORA_OK;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) {  // nothing to do but to clear the status word, where a device holds it
+    cudaPointerAttributes at{};
+    const cudaError_t e = cudaPointerGetAttributes(&at, workspace);
+    if (e != cudaSuccess) cudaGetLastError();  // (no device: no call has left a status either)
+    else if (at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged)
+      ML_CUDA(cudaMemsetAsync(workspace, 0, 8, cs), "status clear");
+    return MOE_LORA_OK;
+  }
   ML_PTR(x);
   ML_PTR(w);
   ML_PTR(y);
@@ -1173,7 +1181,6 @@ moe_lora_status dense_lora_fused(const void* x, const void* w, const void* bias,
   }
   st = check_device();
   if (st != MOE_LORA_OK) return st;
-  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const FusedWs ws = fused_layout(workspace, T, rr, L);
   if (dt == ML_BF16 && !tensor_map_encode_available())
     return fail(MOE_LORA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
