@@ -453,14 +453,15 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool operand, cudaStrea
 // ---------------------------------------------------------------- few tokens
 // z of a small batch on CUDA cores: latency counts, and CTAs that need no shared memory run
 // beside the projection's, which starts meanwhile.  An item is up to 4 tokens of a segment; a
-// CTA takes 4 rank rows of an item, its 8 warps split h_in.
+// CTA takes 4 rank rows of an item, its 8 warps split h_in.  Segments that are wrong may overlap
+// without end, so there an item is one token, of the segment that every kernel finds for it.
 constexpr int kSsTok = 4, kSsRank = 4, kSsThreads = 256;
 
 template <int CTAS, int AHEAD>
 __global__ void __launch_bounds__(kSsThreads, CTAS) fused_shrink_small_kernel(const ShParams p, const __nv_bfloat16* __restrict__ x,
                                                                        const __nv_bfloat16* __restrict__ lora_a) {
   __shared__ float s_red[8][kSsTok * kSsRank];
-  __shared__ int s_item[5];  // segment, first token, tokens (0: no such item), any segment wrong, adapter
+  __shared__ int s_item[3];  // first token, tokens (0: no such item), adapter
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();  // what ran ahead of the call is done, for the projection too
   pdl_trigger();
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(kSsThreads, CTAS) fused_shrink_small_kernel(co
   for (int item = blockIdx.x;; item += gridDim.x) {
     if (warp == 0) {
       int base = 0, first_wrong = 0x7fffffff;
-      if (lane == 0) s_item[2] = 0;
+      if (lane == 0) s_item[1] = 0;
       __syncwarp();
       for (int s0 = 0; s0 < p.S; s0 += 32) {
         const int s = s0 + lane;
@@ -490,27 +491,31 @@ __global__ void __launch_bounds__(kSsThreads, CTAS) fused_shrink_small_kernel(co
         }
         const int at = item - base - (incl - n);
         if (at >= 0 && at < n) {
-          s_item[0] = s;
-          s_item[1] = lo + at * kSsTok;
-          s_item[2] = min(kSsTok, hi - lo - at * kSsTok);
-          s_item[4] = a;
+          s_item[0] = lo + at * kSsTok;
+          s_item[1] = min(kSsTok, hi - lo - at * kSsTok);
+          s_item[2] = a;
         }
         base += __shfl_sync(0xffffffffu, incl, 31);
       }
       first_wrong = __reduce_min_sync(0xffffffffu, first_wrong);
+      __syncwarp();
+      const bool wrong = first_wrong != 0x7fffffff;
       if (lane == 0) {
-        s_item[3] = first_wrong != 0x7fffffff;
+        if (wrong) {  // (without an adapter: some z that nobody reads)
+          const int s = item < p.T ? segment_of(p.seg_offsets, p.S, item) : -1, a = s >= 0 ? p.seg_adapter[s] : 0;
+          s_item[0] = item;
+          s_item[1] = item < p.T ? 1 : 0;
+          s_item[2] = a >= 0 && a < p.L ? a : 0;
+        }
         if (blockIdx.x == 0 && blockIdx.y == 0 && item == 0) {  // the call's first kernel: its status word
-          p.status[0] = s_item[3] ? MOE_LORA_ERR_DEVICE_CHECK : MOE_LORA_OK;
-          p.status[1] = s_item[3] ? first_wrong : 0;
+          p.status[0] = wrong ? MOE_LORA_ERR_DEVICE_CHECK : MOE_LORA_OK;
+          p.status[1] = wrong ? first_wrong : 0;
         }
       }
     }
     __syncthreads();
-    const int seg = s_item[0], t0 = s_item[1], nt = s_item[2];
-    const bool wrong = s_item[3];
+    const int t0 = s_item[0], nt = s_item[1], a = s_item[2];
     if (nt == 0) return;
-    const int a = s_item[4];
     float acc[kSsRank][kSsTok] = {};
     const int h8 = p.K / 8;
     const uint4* A = reinterpret_cast<const uint4*>(lora_a) + (static_cast<size_t>(a) * p.r + i0) * h8;
@@ -538,20 +543,17 @@ __global__ void __launch_bounds__(kSsThreads, CTAS) fused_shrink_small_kernel(co
       }
     __syncthreads();
     if (tid < nt) {
-      const int t = t0 + tid;
-      if (!wrong || segment_of(p.seg_offsets, p.S, t) == seg) {
-        float s[kSsRank] = {};
+      float s[kSsRank] = {};
 #pragma unroll
-        for (int w = 0; w < 8; ++w)
+      for (int w = 0; w < 8; ++w)
 #pragma unroll
-          for (int i = 0; i < kSsRank; ++i) s[i] += s_red[w][tid * kSsRank + i];
-        uint2 o, l;
-        split2(p.scale * s[0], p.scale * s[1], o.x, l.x);
-        split2(p.scale * s[2], p.scale * s[3], o.y, l.y);
-        __nv_bfloat16* zt = p.z + static_cast<size_t>(t) * 2 * p.r + i0;
-        *reinterpret_cast<uint2*>(zt) = o;
-        *reinterpret_cast<uint2*>(zt + p.r) = l;
-      }
+        for (int i = 0; i < kSsRank; ++i) s[i] += s_red[w][tid * kSsRank + i];
+      uint2 o, l;
+      split2(p.scale * s[0], p.scale * s[1], o.x, l.x);
+      split2(p.scale * s[2], p.scale * s[3], o.y, l.y);
+      __nv_bfloat16* zt = p.z + static_cast<size_t>(t0 + tid) * 2 * p.r + i0;
+      *reinterpret_cast<uint2*>(zt) = o;
+      *reinterpret_cast<uint2*>(zt + p.r) = l;
     }
     __syncthreads();
   }
