@@ -111,3 +111,13 @@ SIZES = [(1, 4104, 264, 6, 16), (1, 11008, 136, 6, 128), (4, 2056, 264, 5, 16), 
          (64, 4096, 520, 22, 16), (64, 11008, 136, 5, 64), (65, 1032, 392, 9, 8), (128, 72, 136, 3, 128),
          (203, 2056, 1000, 5, 8), (256, 776, 264, 12, 64), (300, 2048, 264, 6, 32), (520, 4104, 136, 20, 8),
          (300, 264, 520, 7, 16), (700, 328, 264, 9, 64), (1100, 200, 520, 33, 8), (900, 264, 264, 5, 128)]
+
+# a token or a few, over every split of the reduction
+FEW = [(T, h_in, h_out, 6, r) for T, r in [(1, 8), (1, 16), (2, 8), (1, 32), (1, 128), (2, 16), (3, 8), (4, 16)]
+       for h_in, h_out in [(8, 8), (72, 200), (4104, 1000), (11008, 264)]]
+# token counts on both sides of every tile width; K and features that end inside a block
+EDGES = [(T, h_in, h_out, 5, 16) for T, h_in, h_out in
+         [(1, 8, 8), (2, 72, 8), (8, 4096, 512), (16, 512, 520), (17, 2056, 264), (32, 1024, 1000), (33, 64, 136),
+          (64, 2048, 1408), (65, 520, 392), (127, 128, 128), (128, 1032, 640), (129, 256, 264), (200, 776, 1000),
+          (255, 64, 512), (256, 2048, 256), (257, 264, 520), (384, 1000, 776), (511, 512, 512), (640, 200, 1032),
+          (1025, 328, 264)]]

@@ -7,7 +7,7 @@ import torch
 
 from oracle import fused_ref as fr
 from tests.fused_cases import dense_oracle, run_dense
-from tests.grid_cases import SIZES, check_grid, grid_inputs, grid_tolerance
+from tests.grid_cases import EDGES, FEW, SIZES, check_grid, grid_inputs, grid_tolerance
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -20,6 +20,13 @@ def test_sums_are_exact(T, h_in, h_out, L, r, act):
         d = grid_inputs(T, h_in, h_out, L, r, BF16, act, True, True, T + h_in, **kw)
         check_grid(d, run_dense(d))
     d = grid_inputs(T, h_in, h_out, 0, 0, BF16, act, True, False, T + h_in + 1)
+    check_grid(d, run_dense(d))
+
+
+@pytest.mark.parametrize("act", ["none", "silu_and_mul"])
+@pytest.mark.parametrize("T,h_in,h_out,L,r", FEW + EDGES)
+def test_sums_are_exact_at_the_edges(T, h_in, h_out, L, r, act):
+    d = grid_inputs(T, h_in, h_out, L, r, BF16, act, True, True, T + h_in, none_frac=0.0, grouped=T > 4)
     check_grid(d, run_dense(d))
 
 

@@ -5,7 +5,7 @@ import torch
 
 from oracle import fused_ref as fr
 from tests.fused_cases import dense_oracle
-from tests.grid_cases import SIZES, grid_inputs, grid_tolerance
+from tests.grid_cases import EDGES, FEW, SIZES, grid_inputs, grid_tolerance
 
 
 class Case:
@@ -39,8 +39,8 @@ class Case:
         return out
 
 
-@pytest.mark.parametrize("act", ["none", "silu_and_mul"])
-@pytest.mark.parametrize("T,h_in,h_out,L,r", SIZES)
+@pytest.mark.parametrize("T,h_in,h_out,L,r,act", [(*s, a) for s in SIZES for a in ("none", "silu_and_mul")] +
+                         [(*s, "none") for s in FEW + EDGES])
 def test_lost_pieces_are_seen(T, h_in, h_out, L, r, act):
     c = Case(T, h_in, h_out, L, r, torch.bfloat16, act)
     assert c.error(0.0) <= 1.0
