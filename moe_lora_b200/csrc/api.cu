@@ -317,7 +317,7 @@ FusedWs fused_layout(void* base, int T, int r, int L) {
   w.tile_mask = reinterpret_cast<uint64_t*>(take(r ? (static_cast<size_t>(T) + 255) / 256 * 8 : 0));
   w.bad_part = reinterpret_cast<uint64_t*>(take(r && T ? kFusedScanMax * 8 : 0));
   w.zc_pitch = (L * r + 31) / 32 * 64;  // each value of z takes two
-  w.zc = take(r && T > kFusedDecodeTokens ? static_cast<size_t>(T) * w.zc_pitch * 2 : 0);
+  w.zc = take(r && T > kFusedDecodeTokens ? static_cast<size_t>(std::min(T, fused_band(w.zc_pitch))) * w.zc_pitch * 2 : 0);
   w.bytes = off;
   return w;
 }

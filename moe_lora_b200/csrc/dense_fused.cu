@@ -311,12 +311,22 @@ cudaError_t launch_dense_fused(const DenseFusedArgs& a, cudaStream_t st) {
     f.bad_part = a.bad_part;
     f.scan_ctas = std::min(kFusedScanMax, 2 * a.num_sms);
     const bool stream = a.T <= kFusedDecodeTokens || fused_decode_pays(a);
-    if (a.r > 0) {
-      const bool simt = a.T <= kSmallTokens || (stream && fused_shrink_is_small(a));
-      const cudaError_t e = simt ? launch_fused_shrink_simt(f, st) : launch_fused_shrink_tc(f, !stream, st);
+    if (stream) {
+      if (a.r > 0) {
+        const bool simt = a.T <= kSmallTokens || fused_shrink_is_small(a);
+        const cudaError_t e = simt ? launch_fused_shrink_simt(f, st) : launch_fused_shrink_tc(f, false, 0, a.T, st);
+        if (e != cudaSuccess) return e;
+      }
+      return launch_fused_decode_tc(f, st);
+    }
+    const int band = a.r > 0 ? fused_band(a.zc_pitch) : a.T;
+    for (int t0 = 0; t0 < a.T; t0 += band) {
+      const int t1 = std::min(a.T, t0 + band);
+      cudaError_t e = a.r > 0 ? launch_fused_shrink_tc(f, true, t0, t1, st) : cudaSuccess;
+      if (e == cudaSuccess) e = launch_fused_prefill_tc(f, t0, t1, st);
       if (e != cudaSuccess) return e;
     }
-    return stream ? launch_fused_decode_tc(f, st) : launch_fused_prefill_tc(f, st);
+    return cudaSuccess;
   }
   return launch_f32(a, st);
 }

@@ -38,7 +38,8 @@ struct FpParams {
   const uint64_t* tile_mask;
   const uint64_t* bad_part;
   int* status;
-  int T, K, h_out, n, r, L, act, gated, scan_ctas;
+  int t_first, T;  // this launch's tokens: [t_first, T)
+  int K, h_out, n, r, L, act, gated, scan_ctas;
   int tok_tiles, feat_tiles;
 };
 
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
       for (int t = pair; ok && t < total; t += pairs) {
         int tt, ft;
         fp_tile(p, t, tt, ft);
-        const int t0 = tt * 256 + static_cast<int>(rank) * 128;
+        const int z0 = tt * 256 + static_cast<int>(rank) * 128, t0 = p.t_first + z0;
         const int wrow = p.gated ? static_cast<int>(rank) * p.h_out + ft * 128 : ft * 256 + static_cast<int>(rank) * 128;
         uint64_t mask = t != pair ? adapter_mask(tt) : 0ull;
         for (int kb = 0; kb < nk; ++kb) {
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
           const uint32_t fb = leader(&sm.full[stage]);
           const int rb = g.box_rows(), boxes = g.boxes();
           if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], 2u * 128u * 128u + static_cast<uint32_t>(4 * boxes * rb) * 128u);
-          tma_load_2d_pair(s, &tmz, fb, gi * 64, t0);
+          tma_load_2d_pair(s, &tmz, fb, gi * 64, z0);
           s += 128 * 128;
 #pragma unroll
           for (int q = 0; q < kGroupRank / 8; ++q) {
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
       const bool got = mbar_wait(&sm.tfull[buf], static_cast<uint32_t>(it >> 1) & 1u, abort_flag, p.status, kFtWaitNs, 66);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
-      const int tok = tt * 256 + static_cast<int>(rank) * 128 + g4 * 32 + lane;
+      const int tok = p.t_first + tt * 256 + static_cast<int>(rank) * 128 + g4 * 32 + lane;
       const bool row_ok = tok < p.T;
       int bad_ad = -1;
       if (p.r) {
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(kFpThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-cudaError_t launch_fused_prefill_tc(const FusedTcArgs& f, cudaStream_t st) {
+cudaError_t launch_fused_prefill_tc(const FusedTcArgs& f, int t_first, int t_end, cudaStream_t st) {
   const DenseFusedArgs& a = f.a;
   CUtensorMap tmw, tmx, tmb, tmz;
   if (encode_tmap_2d(&tmw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.w, a.h_in, a.n, static_cast<uint64_t>(a.h_in) * 2, 64,
@@ -367,7 +368,7 @@ cudaError_t launch_fused_prefill_tc(const FusedTcArgs& f, cudaStream_t st) {
                             static_cast<uint64_t>(a.n) * 2, 64, std::min(a.r, kGroupRank),
                             CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  if (a.r && encode_tmap_2d(&tmz, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f.zc, f.zc_pitch, a.T,
+  if (a.r && encode_tmap_2d(&tmz, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f.zc, f.zc_pitch, t_end - t_first,
                             static_cast<uint64_t>(f.zc_pitch) * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   FpParams p{};
@@ -377,19 +378,20 @@ cudaError_t launch_fused_prefill_tc(const FusedTcArgs& f, cudaStream_t st) {
   p.z = f.z;
   p.lora_b = static_cast<const __nv_bfloat16*>(a.lora_b);
   p.row_adapter = a.row_adapter;
-  p.tile_mask = f.tile_mask;
+  p.tile_mask = f.tile_mask + t_first / 256;
   p.bad_part = f.bad_part;
   p.scan_ctas = f.scan_ctas;
   p.L = a.L;
   p.status = a.status;
-  p.T = a.T;
+  p.t_first = t_first;
+  p.T = t_end;
   p.K = a.h_in;
   p.h_out = a.h_out;
   p.n = a.n;
   p.r = a.r;
   p.act = a.act;
   p.gated = a.act == ML_ACT_SILU_AND_MUL;
-  p.tok_tiles = (a.T + 255) / 256;
+  p.tok_tiles = (t_end - t_first + 255) / 256;
   p.feat_tiles = p.gated ? (a.h_out + 127) / 128 : (a.h_out + 255) / 256;
   const long long total = static_cast<long long>(p.tok_tiles) * p.feat_tiles;
   const int grid = 2 * static_cast<int>(std::min<long long>(a.num_sms / 2, total));

@@ -34,6 +34,7 @@ struct ShParams {
   const int32_t* seg_adapter;
   int S, T, L, r, K, n;
   float scale;
+  int t_first;  // this launch's tokens: [t_first, t_end)
   const __nv_bfloat16* lora_b;
   __nv_bfloat16* z;
   __nv_bfloat16* zc;
@@ -44,6 +45,7 @@ struct ShParams {
   int* status;
   int C, P;
   int operand;  // the tiled projection follows: zc, row_adapter and tile_mask as well
+  int t_end;
 };
 
 struct ShCore {
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
   const int rank = static_cast<int>(blockIdx.x) % p.C;
   const int group = static_cast<int>(blockIdx.x) / p.C;  // cluster index
   const int tile = group / p.P, chunk0 = group % p.P;
-  const int t0 = tile * 128;
+  const int t0 = p.t_first + tile * 128;
   volatile int* abort_flag = &sm.abort_flag;
   if (tid == 0) {
     for (int s = 0; s < kShStages; ++s) {
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
   const int32_t* seg_off = near ? sm.off : p.seg_offsets;
   const int32_t* seg_ad = near ? sm.ad : p.seg_adapter;
   __syncthreads();
-  if (blockIdx.x == 0) {  // the call's first kernel: its status word
+  if (blockIdx.x == 0 && p.t_first == 0) {  // the call's first kernel: its status word
     int wrong = 0x7fffffff;
     for (int s = tid; s < p.S; s += kShThreads)
       if (segment_wrong(seg_off[s], seg_off[s + 1], seg_ad[s], p.T, p.L)) wrong = min(wrong, s);
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
   for (int i = tid; i < (operand ? 256 : 128); i += kShThreads) {  // own tokens, then the other half's
     const int t = i < 128 ? t0 + i : (t0 ^ 128) + i - 128;
     int a = -1;
-    if (t < p.T) {
+    if (t < p.t_end) {
       const int s = segment_of(seg_off, p.S, t);
       if (s >= 0) a = seg_ad[s];
       if (a >= p.L || a < 0) a = -1;
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
   tc_fence_after();
   const uint64_t mask = sm.mask[0] | (static_cast<uint64_t>(sm.mask[1]) << 32);
   const uint64_t own = sm.own[0] | (static_cast<uint64_t>(sm.own[1]) << 32);
-  if (operand && tid == 0 && chunk0 == 0 && rank == 0 && (tile & 1) == 0) p.tile_mask[tile >> 1] = mask;
+  if (operand && tid == 0 && chunk0 == 0 && rank == 0 && (tile & 1) == 0) p.tile_mask[t0 >> 8] = mask;
   const uint32_t tmem = sm.tmem_base;
   const int apc = kShN / p.r;  // adapters per chunk
   const int cnt = __popcll(mask);
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
       for (int e = tid; e < rows * per_row; e += kShThreads) {
         const int row = rank * rows + e / per_row, q = e % per_row / r8, j = e % per_row % r8, a = sm.ids[q];
         const int t = t0 + row;
-        if (t >= p.T) continue;
+        if (t >= p.t_end) continue;
         uint4 o = make_uint4(0u, 0u, 0u, 0u), l = o;
         if (sm.row_ad[row] == a) {
           const uint32_t at = smem_u32(part + row * pitch + 8 * j);
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kShThreads) fused_shrink_kernel(const __grid_c
         }
         // rank column R of the tile's adapters: K columns 32 (R / 16) + R % 16 (values) and 16 on
         const int R = __popcll(mask & ((1ull << a) - 1ull)) * p.r + 8 * j;
-        uint4* zt = reinterpret_cast<uint4*>(p.zc + static_cast<size_t>(t) * p.zc_pitch + 32 * (R >> 4) + (R & 15));
+        uint4* zt = reinterpret_cast<uint4*>(p.zc + static_cast<size_t>(t - p.t_first) * p.zc_pitch + 32 * (R >> 4) + (R & 15));
         zt[0] = o;
         zt[2] = l;
         // an odd adapter of rank 8 ends inside an MMA step
@@ -381,7 +383,7 @@ static cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, c
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool operand, cudaStream_t st) {
+cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool operand, int t_first, int t_end, cudaStream_t st) {
   const DenseFusedArgs& a = f.a;
   CUtensorMap tmx, tma;
   if (encode_tmap_2d(&tmx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.h_in, a.T, static_cast<uint64_t>(a.h_in) * 2, 64,
@@ -408,13 +410,15 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool operand, cudaStrea
   p.bad_part = f.bad_part;
   p.status = a.status;
   // K splits: as many as keep one wave of CTAs (one per SM: 144 KB of ring each)
-  const int tiles = (a.T + 127) / 128;
+  const int tiles = (t_end - t_first + 127) / 128;
   p.C = 8;
   while (p.C > 1 && tiles * p.C > a.num_sms) p.C /= 2;
   // chunks of a tile side by side while SMs are left
   const int apc = kShN / a.r, most = (std::min(std::min(a.L, a.S), 128) + apc - 1) / apc;
   p.P = std::max(1, std::min(most, a.num_sms / (tiles * p.C)));
   p.operand = operand;
+  p.t_first = t_first;
+  p.t_end = t_end;
   const size_t smem = 1024 + kShRing + 128u * (a.r + 4) * 4;
   static std::atomic<bool> attr_set[kMaxDevices];
   const int dev = current_device_index();
@@ -446,7 +450,7 @@ cudaError_t launch_fused_shrink_tc(const FusedTcArgs& f, bool operand, cudaStrea
   cfg.numAttrs = 2;
   cudaError_t e = cudaLaunchKernelEx(&cfg, fused_shrink_kernel, tmx, tma, p);
   count_launch();
-  if (e == cudaSuccess && operand) return launch_behind(fused_scan_kernel, dim3(f.scan_ctas), kScanThreads, st, p);
+  if (e == cudaSuccess && operand && t_first == 0) return launch_behind(fused_scan_kernel, dim3(f.scan_ctas), kScanThreads, st, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -213,7 +213,7 @@ __device__ __forceinline__ float z_value(const __nv_bfloat16* z, size_t t, int r
 struct FusedTcArgs {
   DenseFusedArgs a;
   __nv_bfloat16* z;        // [T][2][r]: values and remainders
-  __nv_bfloat16* zc;       // K columns of each 256-token tile's groups (see AdapterGroups): [T][zc_pitch]
+  __nv_bfloat16* zc;       // K columns of each 256-token tile's groups (see AdapterGroups): [a band][zc_pitch]
   int zc_pitch;
   uint64_t* tile_mask;     // ... those adapters
   uint64_t* bad_part;      // adapters whose B holds a value that is not finite, by CTA of the scan
@@ -222,11 +222,12 @@ struct FusedTcArgs {
 cudaError_t launch_fused_shrink_simt(const FusedTcArgs& p, cudaStream_t st);
 // the shrink on CUDA cores is two CTAs per SM at most
 bool fused_shrink_is_small(const DenseFusedArgs& a);
-// operand: what launch_fused_prefill_tc asks for as well (zc, the masks, the scan)
-cudaError_t launch_fused_shrink_tc(const FusedTcArgs& p, bool operand, cudaStream_t st);
+// Tokens [t0, t1), t0 a multiple of 256.  operand: what launch_fused_prefill_tc asks for as well
+// (zc, the masks; with the first tokens the scan)
+cudaError_t launch_fused_shrink_tc(const FusedTcArgs& p, bool operand, int t0, int t1, cudaStream_t st);
 cudaError_t launch_fused_decode_tc(const FusedTcArgs& p, cudaStream_t st);
 // above kFusedDecodeTokens: few tiles, so that splitting h_in pays more than larger tiles
 bool fused_decode_pays(const DenseFusedArgs& a);
-cudaError_t launch_fused_prefill_tc(const FusedTcArgs& p, cudaStream_t st);
+cudaError_t launch_fused_prefill_tc(const FusedTcArgs& p, int t0, int t1, cudaStream_t st);
 
 }  // namespace mlb

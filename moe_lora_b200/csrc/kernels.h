@@ -241,7 +241,7 @@ struct DenseFusedArgs {
   bool f32;
   float* z;                   // workspace: scale (x A), fp32 [T][r] (bf16: [T][2][r], rounded and remainder)
   int32_t* row_adapter;       // workspace [T]
-  void* zc;                   // workspace (bf16, T > kFusedDecodeTokens): z as a matrix operand
+  void* zc;                   // workspace (bf16, T > kFusedDecodeTokens): z as a matrix operand of fused_band tokens
   int zc_pitch;
   uint64_t* tile_mask;        // workspace (bf16): adapters of each 256-token tile
   uint64_t* bad_part;         // workspace (bf16): kFusedScanMax words
@@ -252,6 +252,11 @@ struct DenseFusedArgs {
 // tiled one, unless it has few tiles.
 constexpr int kFusedDecodeTokens = 256;
 constexpr int kFusedScanMax = 512;  // CTAs of the adapters' scan at most
+// The operand zc has room for every adapter in every 256 tokens, though they use few of them: it is
+// kept to 256 MB, and longer batches go band by band (64 adapters of rank 128: 8192 tokens; 16 of
+// rank 64: 65536).
+constexpr size_t kFusedBandBytes = size_t(256) << 20;
+constexpr int fused_band(int zc_pitch) { return static_cast<int>(kFusedBandBytes / (size_t(2) * zc_pitch) / 4096) * 4096; }
 cudaError_t launch_dense_fused(const DenseFusedArgs& a, cudaStream_t st);
 
 // Tensor-core grouped GEMM with operand swap: the weight rows fill the 128-row MMA
