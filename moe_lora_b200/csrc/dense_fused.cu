@@ -296,7 +296,7 @@ static cudaError_t launch_f32(const DenseFusedArgs& a, cudaStream_t st) {
 }
 
 // Up to here the adapters' shrink runs on CUDA cores (with more tokens of a split projection where it is
-// small: 203 x 2056 -> 1000 with 5 adapters of rank 8: 16.7 us in all, on the tensor cores 18.4)
+// small: 203 x 2056 -> 1000 with 5 adapters of rank 8: 15.7 us in all, on the tensor cores 19.4)
 constexpr int kSmallTokens = 64;
 
 cudaError_t launch_dense_fused(const DenseFusedArgs& a, cudaStream_t st) {

@@ -26,7 +26,7 @@ namespace mlb {
 constexpr int kFdThreads = 192;
 constexpr int kFdMaxStages = 8;
 // K blocks between two groups of adapters, at most, and behind the last (64 x 4096 -> 2 x 11008
-// with 22 adapters: 46.2 us; 2 between 47.4, none behind 46.9)
+// with 22 adapters: 43.1 us; 2 between 44.2, none behind 43.7)
 constexpr int kGroupStep = 4, kGroupTail = 2;
 constexpr int kFdPitch = 132;  // floats per token row of partial sums (128 features)
 
@@ -422,9 +422,10 @@ static int weight_tiles(const DenseFusedArgs& a) {
 }
 
 // Splitting h_in pays against 256 x 256 tiles when it takes more K blocks off each CTA than the
-// exchange of partial sums costs: 300 x 2048 -> 1024 13.4 against 18.4 us (16 tiles of 128 rows x
-// 256 tokens, 8 splits), 512 x 4096 -> 4096 27.0 against 30.3 (64 tiles, 2), 400 x 11008 -> 1000 31
-// against 60; but 700 x 600 -> 2000 23.1 against 15.5 (48 tiles, 3 splits of 10 K blocks).
+// exchange of partial sums costs: 300 x 2048 -> 1024 12.6 against 15.7 us (16 tiles of 128 rows x
+// 256 tokens, 8 splits), 512 x 4096 -> 4096 25.8 against 26.0 (64 tiles, 2), with 16 adapters of
+// rank 16 42 against 51, 400 x 11008 -> 1000 31 against 60; but 700 x 600 -> 2000 23.1 against 15.5
+// (48 tiles, 3 splits of 10 K blocks).
 bool fused_decode_pays(const DenseFusedArgs& a) {
   const long long tiles = static_cast<long long>(weight_tiles(a)) * ((a.T + 255) / 256);
   const long long splits = std::min<long long>(8, a.num_sms / tiles), nkb = (a.h_in + 63) / 64;

@@ -1,7 +1,7 @@
 // dense_lora_fused for many tokens: y = act(x W^T + bias + z B) + residual.
 //
 // Bound by the tensor pipe under the power cap (4096 x 4096 -> 11008: 260 us without adapters,
-// 1.42 PFLOP/s over the call; 293 us with 16 of rank 64).  CTA pairs (tcgen05 cta_group::2, M = 256) compute tiles of 256
+// 1.42 PFLOP/s over the call; 310 us with 16 of rank 64).  CTA pairs (tcgen05 cta_group::2, M = 256) compute tiles of 256
 // tokens x 256 weight rows (gated: 128 gate rows and the matching 128 up rows): tokens in M,
 // so that a thread of the epilogue holds one token's neighbouring features and bias,
 // activation, residual and store work on whole 16-byte runs.  Each CTA stages its 128 tokens

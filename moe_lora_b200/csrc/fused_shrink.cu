@@ -99,8 +99,8 @@ __global__ void __launch_bounds__(kScanThreads) fused_scan_kernel(const ShParams
   }
   __syncthreads();
   // The launch ends behind the shrink kernel by one CTA; the others leave their SMs to the
-  // projection, whose CTAs do not fit beside them (600 x 4096 -> 2 x 2048 with 16 adapters: 49.5
-  // against 51.2 us with all of them waiting).
+  // projection, whose CTAs do not fit beside them (600 x 4096 -> 2 x 2048 with 16 adapters: 51.2
+  // against 52.8 us with all of them waiting).
   if (blockIdx.x == 0) pdl_wait();
   if (tid == 0) p.bad_part[blockIdx.x] = s_bad[0] | (static_cast<uint64_t>(s_bad[1]) << 32);
 }
