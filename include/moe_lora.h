@@ -326,8 +326,10 @@ MOE_LORA_API moe_lora_status dense_lora_forward(
  * Sums, bias, activation and residual are fp32 and rounded to dt once (for ML_BF16 the
  * adapters' xA goes on as two bf16 numbers, the rounded value and what it left: 2^-17 of it
  * is lost).  A tenant's adapter reaches only its own tokens, whatever
- * it holds.  An adapter id outside [-1, L) or offsets that are not monotone set
- * MOE_LORA_ERR_DEVICE_CHECK; the tokens concerned count as without an adapter.
+ * it holds.  An adapter id outside [-1, L) or offsets that are not monotone or leave [0, T]
+ * set MOE_LORA_ERR_DEVICE_CHECK; a token of such an id counts as without an adapter, and where
+ * offsets are out of order each token counts by the one segment that a binary search for the
+ * last one beginning at or before it ends at, if that segment holds it.
  * h_in and h_out are multiples of 8; T <= 2^20.
  * ------------------------------------------------------------------------------- */
 MOE_LORA_API moe_lora_status dense_lora_fused(

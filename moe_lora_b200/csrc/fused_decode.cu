@@ -349,14 +349,15 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
       b[2] = __uint_as_float(v.y << 16);
       b[3] = __uint_as_float(v.y & 0xFFFF0000u);
     }
-    // the tile's broken adapters, whichever CTA met them: by 32 rank rows, and all
-    auto broken_at = [&](int i) -> uint64_t {
-      uint64_t b = 0ull;
-      for (int c = 0; c < p.C; ++c) b |= ld_cluster_u64(mapa_shared(smem_u32(sm.broken + 2 * i), static_cast<uint32_t>(c)));
-      return b;
+    // the tile's broken adapters, whichever CTA met them: a lane per CTA and 32 rank rows asks
+    auto broken_at = [&](int i, int c) -> uint64_t {
+      return ld_cluster_u64(mapa_shared(smem_u32(sm.broken + 2 * i), static_cast<uint32_t>(c)));
     };
-    uint64_t bad = 0ull;
-    for (int i = 0; i * kGroupRank < p.r; ++i) bad |= broken_at(i);
+    static_assert(8 * (128 / kGroupRank) <= 32, "eight CTAs' words for a warp");
+    const int parts = (p.r + kGroupRank - 1) / kGroupRank;
+    uint64_t bad = lane < p.C * parts ? broken_at(lane / p.C, lane % p.C) : 0ull;
+    bad = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(bad)) |
+          static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(bad >> 32))) << 32;
     // the next token's partial sums are on their way while one is finished
     const int t_step = p.C * (kFdThreads / 32);
     const bool writer = in && (!p.gated || lane < 16);
@@ -388,7 +389,9 @@ __global__ void __launch_bounds__(kFdThreads, BN <= 64 ? 4 : BN <= 128 ? 2 : 1)
         const int ad = sm.row_ad[t];
         if (ad >= 0 && (bad >> ad & 1ull) && in)
           for (int i0 = 0; i0 < p.r; i0 += kGroupRank) {
-            if (!(broken_at(i0 / kGroupRank) >> ad & 1ull)) continue;  // (those rows are in the product)
+            bool out = false;  // (else those rows are in the product)
+            for (int c = 0; c < p.C; ++c) out |= broken_at(i0 / kGroupRank, c) >> ad & 1ull;
+            if (!out) continue;
             for (int i = i0; i < min(i0 + kGroupRank, p.r); ++i) {
               const float zi = z_value(z, t, p.r, i);
               const __nv_bfloat16* br = p.lora_b + (static_cast<size_t>(ad) * p.r + i) * p.n + col;

@@ -12,7 +12,7 @@
 // Batches that fill the SMs with 128 tokens each are bound by what the SMs read (x once, W_r
 // once per tile): there CTA pairs (tcgen05 cta_group::2) share W_r, each reading half of it.
 //
-// 16384 tokens x 256 experts (H 7168) take 107 us (108 to 117 as calls among others): 47 us in which x streams (240 MB; 36 us at the
+// 16384 tokens x 256 experts (H 7168) take 107 us (106 to 117 as calls among others): 47 us in which x streams (240 MB; 36 us at the
 // copy rate), about 30 us of choice and weights (some 1000 instructions per token and warp),
 // 10 us of sort.  One token in 12.6 us and 64 x 128 (H 7168) in 20.4 us are bound by latency: launch,
 // copies, three cluster barriers and the choice follow each other at 1 to 2 us each.
